@@ -1,5 +1,6 @@
 """Builds the libraries in-tree with hipcc for gfx950 (no JIT, no site-packages install):
-  libipttt.so        the layer (include/ipttt.h)
+  libipttt.so        the layer (include/ipttt.h) and the operators around it
+                     (include/ipttt_block.h)
   libipttt_probe.so  measurement-only micro-benchmarks (include/ipttt_probe.h)
 Host and device code compile with -Wall -Wextra -Werror."""
 from __future__ import annotations
@@ -16,7 +17,8 @@ LIB = os.path.join(HERE, "libipttt.so")
 PROBE_LIB = os.path.join(HERE, "libipttt_probe.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["ipttt.cpp", "kernels_generic.hip", "kernels_mfma.hip", "kernels_decode.hip",
-           "kernels_backward.hip", "scratch.hip"]
+           "kernels_backward.hip", "scratch.hip", "block.cpp", "kernels_norm.hip",
+           "kernels_recurrence.hip", "kernels_ff.hip"]
 PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"
 FLAGS = [

@@ -15,6 +15,9 @@ namespace ipttt {
 // chunk starts on a 64-row boundary (one K step of the MFMA update).
 constexpr int kChunkAlign = 64;
 
+// Sets this thread's ipttt_last_error message ("<status>: <text>") and returns s.
+ipttt_status set_error(ipttt_status s, const char *text);
+
 inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
 // Geometry of one slab of a prefill call.

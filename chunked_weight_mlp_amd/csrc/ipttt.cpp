@@ -53,8 +53,7 @@ ipttt_status fail(ipttt_status s, const char *fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  g_last_error = std::string(ipttt_status_str(s)) + ": " + buf;
-  return s;
+  return ipttt::set_error(s, buf);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -162,6 +161,11 @@ struct ProfScope {
 }  // namespace
 
 namespace ipttt {
+
+ipttt_status set_error(ipttt_status s, const char *text) {
+  g_last_error = std::string(ipttt_status_str(s)) + ": " + text;
+  return s;
+}
 
 WsLayout ws_layout(int elem, int n_seq, int d, int F, int Bp, int nc_cap, int G, int mse,
                    int need_z) {

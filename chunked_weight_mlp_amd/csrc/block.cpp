@@ -103,6 +103,9 @@ ipttt_status check_rec_sizes(const ipttt_recurrence *r) {
     return fail(IPTTT_E_INVALID, "seq_len=%lld must be >= 0", (long long)r->seq_len);
   if (r->seq_len > ((int64_t)1 << 30))
     return fail(IPTTT_E_UNSUPPORTED, "seq_len=%lld exceeds 2^30", (long long)r->seq_len);
+  if (!rec_size_ok(r->batch, r->d, r->seq_len))
+    return fail(IPTTT_E_UNSUPPORTED, "batch=%d x seq_len=%lld x d=%d exceed 2^31 tiles", r->batch,
+                (long long)r->seq_len, r->d);
   return IPTTT_OK;
 }
 
@@ -338,7 +341,7 @@ ipttt_status ipttt_norm_backward(const ipttt_norm_desc *desc, const void *h, int
 
 size_t ipttt_recurrence_workspace_bytes(const ipttt_recurrence *r) {
   if (!r || r->d < 1 || r->d > (1 << 16) || r->batch < 0 || r->batch > 65535 || r->seq_len < 0 ||
-      r->seq_len > ((int64_t)1 << 30) || (r->dtype != IPTTT_F32 && r->dtype != IPTTT_BF16))
+      r->seq_len > ((int64_t)1 << 30) || !rec_size_ok(r->batch, r->d, r->seq_len) || (r->dtype != IPTTT_F32 && r->dtype != IPTTT_BF16))
     return 0;
   return rec_workspace(r->batch, r->d, r->seq_len);
 }

@@ -45,6 +45,8 @@ struct RecArgs {
   float *dh0;             // or null
   void *ws;
 };
+// Whether the tiles of such a call can be launched and counted in 31 bits.
+bool rec_size_ok(int n, int d, int64_t L);
 size_t rec_workspace(int n, int d, int64_t L);
 // One token per sequence (L = 1): state h0 -> h_last, which may be the same.
 template <typename T>

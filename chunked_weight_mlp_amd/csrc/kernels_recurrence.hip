@@ -1,5 +1,15 @@
 // The gated linear recurrence h_t = f_t h_{t-1} + (1 - f_t) v_t, f = sigmoid(g),
 // forward and backward.
+//
+// Each step is an affine map of the state, s -> A s + B, and maps compose:
+// (A2, B2) after (A1, B1) is (A2 A1, A2 B1 + B2). So a sequence is cut into tiles
+// of tokens that are read once and kept in registers: a tile reduces its tokens to
+// one map per channel, learns the state before it from the maps of the tiles in
+// front of it, and then runs its own tokens from that state. A document start
+// makes a map that ignores the state (kept as a flag, not as A = 0, so that a
+// state that is not finite does not leak through 0 x inf). The backward runs the
+// same way from the last token to the first on the gradient of the state.
+// Few tokens (SEQ_MAX) are walked by one thread per channel pair instead.
 #include <algorithm>
 
 #include "block_internal.h"
@@ -138,9 +148,453 @@ __global__ __launch_bounds__(64) void k_rec_seq_bwd(RecArgs a) {
   if (a.dh0) store_ch<float, SEQ_V>(a.dh0 + (int64_t)n * a.d, c, a.d, s);
 }
 
+// ---- tiles ---------------------------------------------------------------------------
+// A block of NW waves takes TT = NW R tokens of 64 V channels of one sequence;
+// a lane holds V channels, a wave R consecutive tokens.
+//
+// Tiles of one (sequence, channel block) meet in `slots`, 8 bytes per tile and
+// channel: all ones (empty, written by k_rec_clear), then the tile's own map
+// (A, B) as soon as it is known, then (-1, s), the state after the tile (before
+// it, in the backward). A waits for nothing but its own 8 bytes, so a slot needs
+// no flag and no fence. A tile walks back from its neighbour, composing maps,
+// until it meets a state. Tiles are handed out by a counter in chain order, so
+// every tile a block waits for is held by a block that already runs and, by
+// induction from the first tile of each chain, ends.
+
+constexpr uint64_t kEmpty = ~(uint64_t)0;
+// Polls of a tile before it gives up and returns NaN (about a second; a chain in
+// order never gets near it): a wait that cannot last for ever.
+constexpr int kMaxPolls = 1 << 20;
+
+__device__ __forceinline__ uint64_t slot_pack(float a, float b) {
+  uint32_t ua = __builtin_bit_cast(uint32_t, a);
+  const uint32_t ub = __builtin_bit_cast(uint32_t, b);
+  if ((ua & ub) == ~0u) ua = 0x7fc00000u;  // a NaN pair that would read as empty
+  return (uint64_t)ub << 32 | ua;
+}
+__device__ __forceinline__ void slot_put(uint64_t *p, float a, float b) {
+  __hip_atomic_store(p, slot_pack(a, b), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t slot_get(const uint64_t *p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state handed to this lane's V channels by the tiles behind slot pointer
+// `at` (the neighbour's slots); `step` slots further back per tile, `count` tiles
+// in all, the last of which publishes a state at once. B tiles are read ahead.
+template <int V>
+__device__ __forceinline__ void look_back(const uint64_t *at, int64_t step, int count,
+                                          float (&state)[V]) {
+  constexpr int B = 4;
+  float A[V], S[V];
+  bool done[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    A[e] = 1.f;
+    S[e] = 0.f;
+    done[e] = false;
+  }
+  int left = count, polls = 0;
+  while (left > 0) {
+    uint64_t w[B][V];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[b][e] = slot_get(at - min(b, left - 1) * step + e);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (b >= left) break;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        while (w[b][e] == kEmpty && polls < kMaxPolls) {
+          __builtin_amdgcn_s_sleep(1);
+          w[b][e] = slot_get(at - b * step + e);
+          ++polls;
+        }
+        const float a = __builtin_bit_cast(float, (uint32_t)w[b][e]);
+        const float s = __builtin_bit_cast(float, (uint32_t)(w[b][e] >> 32));
+        if (!done[e]) {
+          S[e] = fmaf(A[e], s, S[e]);
+          if (a == -1.f)
+            done[e] = true;
+          else
+            A[e] *= a;
+        }
+      }
+      bool all = true;
+#pragma unroll
+      for (int e = 0; e < V; ++e) all = all && done[e];
+      if (__all(all)) {
+        left = 0;
+        break;
+      }
+    }
+    if (left > 0) {
+      left -= min(B, left);
+      at -= B * step;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) state[e] = S[e];
+}
+
+// A raw pack of V channels; channels at or past d are zero.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_raw(const T *row, int c, int d) {
+  if (c + V <= d) return *(const Pack<T, V> *)(row + c);
+  Pack<T, V> p;
+#pragma unroll
+  for (int e = 0; e < V; ++e) p.v[e] = c + e < d ? row[c + e] : (T)0.f;
+  return p;
+}
+
+// Where a block's tile is. `ord`: position in its chain (0 runs first).
+struct Tile {
+  int n, cb;
+  int64_t ord;
+};
+template <int V>
+__device__ __forceinline__ Tile next_tile(const RecArgs &a, int nt) {
+  __shared__ unsigned ticket;
+  unsigned id = blockIdx.x;
+  if (nt > 1) {
+    if (threadIdx.x == 0)
+      ticket = __hip_atomic_fetch_add((unsigned *)a.ws, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    id = ticket;
+  }
+  const unsigned cbs = (a.d + 64 * V - 1) / (64 * V), per = cbs * a.n;
+  return {(int)((id % per) / cbs), (int)(id % cbs), (int64_t)(id / per)};
+}
+
+// Bit r: a document starts at token t0 + r, for the R tokens from t0 below `end`.
+template <int R>
+__device__ __forceinline__ uint64_t start_bits(const RecArgs &a, int n, int64_t t0, int64_t end) {
+  if (!a.starts) return 0;
+  const int lane = threadIdx.x & 63;
+  const int64_t t = t0 + lane;
+  return __ballot(lane < R && t < end && a.starts[(int64_t)n * a.L + t] != 0);
+}
+
+constexpr int64_t kSlotBase = 256;  // bytes in front of the slots: the tile counter
+
+template <typename T, int V, int R, int NW>
+__global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
+  constexpr int TT = NW * R, CH = 64 * V;
+  __shared__ float sA[NW][CH], sB[NW][CH], sIn[CH];
+  __shared__ int sCut[NW];
+  const Tile tl = next_tile<V>(a, nt);
+  const int lane = threadIdx.x & 63, n = tl.n;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t len = seq_length(a, n), t0 = tl.ord * TT;
+  const int c = CH * tl.cb + V * lane, d = a.d;
+  const int64_t tb = t0 + wave * R;
+  const int cnt = (int)min(max(len - tb, (int64_t)0), (int64_t)R);
+  T *h = seq_of<T>(a.h, n);
+  const float zero[V] = {};
+  if (c < d)
+    for (int r = cnt; r < R && tb + r < a.L; ++r) store_ch<T, V>(h + (tb + r) * a.h.tok_stride, c, d, zero);
+  float s[V] = {};
+  if (tl.ord == 0 && a.h0 && c < d) load_ch<float, V>(a.h0 + (int64_t)n * d, c, d, s);
+  if (t0 >= len) {  // nothing of the sequence here, and nobody waits for it
+    if (tl.ord == 0 && wave == 0 && a.h_last && c < d)
+      store_ch<float, V>(a.h_last + (int64_t)n * d, c, d, s);
+    return;
+  }
+  // the wave's tokens as local states hl (from a zero state) and products P
+  float P[R][V], hl[R][V];
+  const uint64_t cuts = start_bits<R>(a, n, tb, tb + cnt);
+  {
+    const T *g = seq_of<T>(a.g, n), *v = seq_of<T>(a.v, n);
+    Pack<T, V> gr[R], vr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t t = min(tb + r, len - 1);
+      gr[r] = load_raw<T, V>(g + t * a.g.tok_stride, c, d);
+      vr[r] = load_raw<T, V>(v + t * a.v.tok_stride, c, d);
+    }
+    float p[V], q[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      p[e] = 1.f;
+      q[e] = 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r < cnt) {
+        const bool cut = cuts >> r & 1;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float f, i;
+          gate((float)gr[r].v[e], f, i);
+          const float b = i * (float)vr[r].v[e];
+          q[e] = cut ? b : fmaf(f, q[e], b);
+          p[e] *= f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        P[r][e] = p[e];
+        hl[r][e] = q[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    sA[wave][V * lane + e] = P[R - 1][e];
+    sB[wave][V * lane + e] = hl[R - 1][e];
+  }
+  if (lane == 0) sCut[wave] = cuts != 0;
+  __syncthreads();
+  // the map of the waves in front of this one; wave 0 takes the whole tile's
+  const int upto = wave == 0 ? NW : wave;
+  float A[V], B[V];
+  bool cut = false;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    A[e] = 1.f;
+    B[e] = 0.f;
+  }
+  for (int w = 0; w < upto; ++w) {
+    const bool k = sCut[w] != 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float x = sA[w][V * lane + e], y = sB[w][V * lane + e];
+      B[e] = k ? y : fmaf(x, B[e], y);
+      A[e] *= x;
+    }
+    cut = cut || k;
+  }
+  if (wave == 0) {
+    uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) +
+                     ((int64_t)tl.ord * a.n + n) * (int64_t)((d + CH - 1) / CH) * CH +
+                     (int64_t)tl.cb * CH + V * lane;
+    const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
+    const bool more = t0 + TT < len;  // a tile behind this one reads the slots
+    if (tl.ord > 0) {
+      if (more) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
+      }
+      look_back<V>(mine - step, step, (int)tl.ord, s);
+    }
+    if (more && !(cut && tl.ord > 0)) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sIn[V * lane + e] = s[e];
+  }
+  __syncthreads();
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s[e] = sIn[V * lane + e];
+      s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
+    }
+  }
+  if (c >= d) return;
+  float o[V] = {};
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < cnt) {
+      const bool k = (cuts & ((uint64_t)2 << r) - 1) != 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = k ? hl[r][e] : fmaf(P[r][e], s[e], hl[r][e]);
+      store_ch<T, V>(h + (tb + r) * a.h.tok_stride, c, d, o);
+    }
+  if (a.h_last && cnt > 0 && tb + cnt == len) store_ch<float, V>(a.h_last + (int64_t)n * d, c, d, o);
+}
+
+// The gradient G of the state before token t: G_t = f_t (dh_t + G_{t+1}), 0 at a
+// document start; chain order runs from the last tile of the longest sequence.
+template <typename T, int V, int R, int NW>
+__global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
+  constexpr int TT = NW * R, CH = 64 * V;
+  __shared__ float sA[NW][CH], sB[NW][CH], sIn[CH];
+  __shared__ int sCut[NW];
+  const Tile tl = next_tile<V>(a, nt);
+  const int lane = threadIdx.x & 63, n = tl.n;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t len = seq_length(a, n), tile = nt - 1 - tl.ord, t0 = tile * TT;
+  const int c = CH * tl.cb + V * lane, d = a.d;
+  const int64_t tb = t0 + wave * R;
+  const int cnt = (int)min(max(len - tb, (int64_t)0), (int64_t)R);
+  T *dg = seq_of<T>(a.dg, n), *dv = seq_of<T>(a.dv, n);
+  const float zero[V] = {};
+  if (c < d)
+    for (int r = cnt; r < R && tb + r < a.L; ++r) {
+      store_ch<T, V>(dg + (tb + r) * a.dg.tok_stride, c, d, zero);
+      store_ch<T, V>(dv + (tb + r) * a.dv.tok_stride, c, d, zero);
+    }
+  const bool first = t0 + TT >= len;  // the chain's first tile of this sequence
+  float s[V] = {};
+  if (first && a.dh_last && c < d) load_ch<float, V>(a.dh_last + (int64_t)n * d, c, d, s);
+  if (t0 >= len) {
+    if (tile == 0 && wave == 0 && a.dh0 && c < d)
+      store_ch<float, V>(a.dh0 + (int64_t)n * d, c, d, s);
+    return;
+  }
+  const uint64_t cuts = start_bits<R>(a, n, tb, tb + cnt);
+  Pack<T, V> gr[R], dr[R], vr[R], pr[R];
+  {
+    const T *g = seq_of<T>(a.g, n), *dh = seq_of<T>(a.dh, n);
+    const T *v = seq_of<T>(a.v, n), *h = seq_of<T>(a.h, n);
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      const int64_t t = min(tb + r, len - 1);
+      gr[r] = load_raw<T, V>(g + t * a.g.tok_stride, c, d);
+      dr[r] = load_raw<T, V>(dh + t * a.dh.tok_stride, c, d);
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {  // used after the wait
+      const int64_t t = min(tb + r, len - 1);
+      vr[r] = load_raw<T, V>(v + t * a.v.tok_stride, c, d);
+      pr[r] = load_raw<T, V>(h + max(t - 1, (int64_t)0) * a.h.tok_stride, c, d);
+    }
+  }
+  float A[V], B[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    A[e] = 1.f;
+    B[e] = 0.f;
+  }
+#pragma unroll
+  for (int r = R - 1; r >= 0; --r)
+    if (r < cnt) {
+      const bool k = cuts >> r & 1;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float f, i;
+        gate((float)gr[r].v[e], f, i);
+        B[e] = k ? 0.f : f * ((float)dr[r].v[e] + B[e]);
+        A[e] *= f;
+      }
+    }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    sA[wave][V * lane + e] = A[e];
+    sB[wave][V * lane + e] = B[e];
+  }
+  if (lane == 0) sCut[wave] = cuts != 0;
+  __syncthreads();
+  // the map of the waves behind this one; the last wave takes the whole tile's
+  const int down = wave == NW - 1 ? 0 : wave + 1;
+  bool cut = false;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    A[e] = 1.f;
+    B[e] = 0.f;
+  }
+  for (int w = NW - 1; w >= down; --w) {
+    const bool k = sCut[w] != 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float x = sA[w][V * lane + e], y = sB[w][V * lane + e];
+      B[e] = k ? y : fmaf(x, B[e], y);
+      A[e] *= x;
+    }
+    cut = cut || k;
+  }
+  if (wave == NW - 1) {
+    const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
+    uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) + tl.ord * step +
+                     (int64_t)n * ((d + CH - 1) / CH) * CH + (int64_t)tl.cb * CH + V * lane;
+    const bool more = tile > 0;
+    if (!first) {
+      if (more) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
+      }
+      // tiles between this one and the sequence's last
+      look_back<V>(mine - step, step, (int)((len - 1) / TT - tile), s);
+    }
+    if (more && !(cut && !first)) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sIn[V * lane + e] = s[e];
+  }
+  __syncthreads();
+  if (wave < NW - 1) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s[e] = sIn[V * lane + e];
+      s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
+    }
+  }
+  if (c >= d) return;
+#pragma unroll
+  for (int r = R - 1; r >= 0; --r)
+    if (r < cnt) {
+      const bool k = cuts >> r & 1;
+      float prev[V], og[V], ov[V];
+      if (tb + r == 0) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) prev[e] = 0.f;
+        if (a.h0) load_ch<float, V>(a.h0 + (int64_t)n * d, c, d, prev);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) prev[e] = (float)pr[r].v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float f, i;
+        gate((float)gr[r].v[e], f, i);
+        const float delta = (float)dr[r].v[e] + s[e];
+        ov[e] = i * delta;
+        og[e] = delta * ((k ? 0.f : prev[e]) - (float)vr[r].v[e]) * (f * i);
+        s[e] = k ? 0.f : f * delta;
+      }
+      store_ch<T, V>(dg + (tb + r) * a.dg.tok_stride, c, d, og);
+      store_ch<T, V>(dv + (tb + r) * a.dv.tok_stride, c, d, ov);
+    }
+  if (a.dh0 && tb == 0) store_ch<float, V>(a.dh0 + (int64_t)n * d, c, d, s);
+}
+
+// Empties the slots and the tile counter.
+__global__ __launch_bounds__(256) void k_rec_clear(uint64_t *ws, int64_t slots) {
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i0 == 0) *(unsigned *)ws = 0;
+  uint64_t *s = ws + kSlotBase / 8;
+  for (int64_t i = 2 * i0; i < slots; i += (int64_t)gridDim.x * 512) {
+    s[i] = kEmpty;
+    s[i + 1] = kEmpty;  // slots come in multiples of 64
+  }
+}
+
+constexpr int64_t SEQ_MAX = 16;
+
+template <typename T>
+struct Shape {  // channels per lane, tokens per wave (forward, backward), waves
+  static constexpr int V = 2, RF = 16, RB = sizeof(T) == 2 ? 16 : 8, NW = 8;
+};
+
+int64_t tile_slots(int n, int d, int64_t nt, int v) { return nt * n * round_up(d, 64 * v); }
+
+hipError_t clear_slots(const RecArgs &a, int64_t nt, int v, hipStream_t st) {
+  if (nt <= 1) return hipSuccess;
+  const int64_t slots = tile_slots(a.n, a.d, nt, v);
+  hipLaunchKernelGGL(k_rec_clear, dim3((unsigned)std::min<int64_t>((slots + 511) / 512, 2048)),
+                     dim3(256), 0, st, (uint64_t *)a.ws, slots);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-size_t rec_workspace(int, int, int64_t) { return 256; }
+// the smallest tile of any type's forward and backward
+constexpr int kMinTile = Shape<float>::RB * Shape<float>::NW;
+
+bool rec_size_ok(int n, int d, int64_t L) {
+  const int64_t nt = (L + kMinTile - 1) / kMinTile, cb = (d + 64 * Shape<float>::V - 1) / (64 * Shape<float>::V);
+  return nt * n <= INT32_MAX && nt * n * cb <= INT32_MAX;
+}
+
+size_t rec_workspace(int n, int d, int64_t L) {
+  const int64_t nt = (L + kMinTile - 1) / kMinTile;
+  return (size_t)kSlotBase + (L <= SEQ_MAX || nt <= 1 ? 0 : 8 * tile_slots(n, d, nt, Shape<float>::V));
+}
 
 template <typename T>
 hipError_t rec_step(const RecArgs &a, hipStream_t st) {
@@ -151,15 +605,31 @@ hipError_t rec_step(const RecArgs &a, hipStream_t st) {
 
 template <typename T>
 hipError_t rec_forward(const RecArgs &a, hipStream_t st) {
-  hipLaunchKernelGGL(k_rec_seq_fwd<T>, dim3((a.d + 64 * SEQ_V - 1) / (64 * SEQ_V), a.n), dim3(64), 0,
-                     st, a);
+  if (a.L <= SEQ_MAX) return rec_step<T>(a, st);
+  using S = Shape<T>;
+  const int64_t nt = (a.L + S::RF * S::NW - 1) / (S::RF * S::NW);
+  const hipError_t e = clear_slots(a, nt, S::V, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_rec_fwd<T, S::V, S::RF, S::NW>),
+                     dim3((unsigned)(nt * a.n * ((a.d + 64 * S::V - 1) / (64 * S::V)))),
+                     dim3(64 * S::NW), 0, st, a, (int)nt);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t rec_backward(const RecArgs &a, hipStream_t st) {
-  hipLaunchKernelGGL(k_rec_seq_bwd<T>, dim3((a.d + 64 * SEQ_V - 1) / (64 * SEQ_V), a.n), dim3(64), 0,
-                     st, a);
+  using S = Shape<T>;
+  if (a.L <= SEQ_MAX) {
+    hipLaunchKernelGGL(k_rec_seq_bwd<T>, dim3((a.d + 64 * SEQ_V - 1) / (64 * SEQ_V), a.n), dim3(64),
+                       0, st, a);
+    return hipGetLastError();
+  }
+  const int64_t nt = (a.L + S::RB * S::NW - 1) / (S::RB * S::NW);
+  const hipError_t e = clear_slots(a, nt, S::V, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_rec_bwd<T, S::V, S::RB, S::NW>),
+                     dim3((unsigned)(nt * a.n * ((a.d + 64 * S::V - 1) / (64 * S::V)))),
+                     dim3(64 * S::NW), 0, st, a, (int)nt);
   return hipGetLastError();
 }
 

@@ -11,6 +11,7 @@
 // same way from the last token to the first on the gradient of the state.
 // Few tokens (SEQ_MAX) are walked by one thread per channel pair instead.
 #include <algorithm>
+#include <type_traits>
 
 #include "block_internal.h"
 
@@ -179,13 +180,19 @@ __device__ __forceinline__ uint64_t slot_get(const uint64_t *p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state handed to this lane's V channels by the tiles behind slot pointer
-// `at` (the neighbour's slots); `step` slots further back per tile, `count` tiles
-// in all, the last of which publishes a state at once. B tiles are read ahead.
-template <int V>
+// The state handed to this lane's V channels by the `count` tiles behind slot
+// pointer `at` (the neighbour's slots), each `step` slots further back, the last
+// of which publishes a state at once. The block's waves take runs of LB tiles
+// side by side (one trip to memory covers NW LB tiles), reduce each run to one
+// map, and every wave composes the runs' maps from LDS. Called by the whole
+// block; all waves get the same state.
+constexpr int LB = 4;
+
+template <int V, int NW>
 __device__ __forceinline__ void look_back(const uint64_t *at, int64_t step, int count,
+                                          float (&mapA)[NW][64 * V], float (&mapB)[NW][64 * V],
                                           float (&state)[V]) {
-  constexpr int B = 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float A[V], S[V];
   bool done[V];
 #pragma unroll
@@ -194,45 +201,62 @@ __device__ __forceinline__ void look_back(const uint64_t *at, int64_t step, int 
     S[e] = 0.f;
     done[e] = false;
   }
-  int left = count, polls = 0;
-  while (left > 0) {
-    uint64_t w[B][V];
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[b][e] = slot_get(at - min(b, left - 1) * step + e);
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      if (b >= left) break;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        while (w[b][e] == kEmpty && polls < kMaxPolls) {
-          __builtin_amdgcn_s_sleep(1);
-          w[b][e] = slot_get(at - b * step + e);
-          ++polls;
-        }
-        const float a = __builtin_bit_cast(float, (uint32_t)w[b][e]);
-        const float s = __builtin_bit_cast(float, (uint32_t)(w[b][e] >> 32));
-        if (!done[e]) {
-          S[e] = fmaf(A[e], s, S[e]);
-          if (a == -1.f)
-            done[e] = true;
-          else
-            A[e] *= a;
-        }
-      }
-      bool all = true;
-#pragma unroll
-      for (int e = 0; e < V; ++e) all = all && done[e];
-      if (__all(all)) {
-        left = 0;
-        break;
-      }
+  int polls = 0;
+  const auto compose = [&](float (&p)[V], float (&q)[V], bool (&end)[V], int e, float x, float y) {
+    if (!end[e]) {
+      q[e] = fmaf(p[e], y, q[e]);
+      if (x == -1.f)
+        end[e] = true;
+      else
+        p[e] *= x;
     }
+  };
+  for (int o = 0; o < count; o += NW * LB) {
+    float a[V], b[V];
+    bool end[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      a[e] = 1.f;
+      b[e] = 0.f;
+      end[e] = false;
+    }
+    const int first = o + wave * LB, left = count - first;
     if (left > 0) {
-      left -= min(B, left);
-      at -= B * step;
+      const uint64_t *p = at - first * step;
+      uint64_t w[LB][V];
+#pragma unroll
+      for (int k = 0; k < LB; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[k][e] = slot_get(p - min(k, left - 1) * step + e);
+#pragma unroll
+      for (int k = 0; k < LB; ++k)
+        if (k < left) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            while (w[k][e] == kEmpty && polls < kMaxPolls) {
+              __builtin_amdgcn_s_sleep(1);
+              w[k][e] = slot_get(p - k * step + e);
+              ++polls;
+            }
+            compose(a, b, end, e, __builtin_bit_cast(float, (uint32_t)w[k][e]),
+                    __builtin_bit_cast(float, (uint32_t)(w[k][e] >> 32)));
+          }
+        }
     }
+    if (o > 0) __syncthreads();  // the last round's maps have been read
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      mapA[wave][V * lane + e] = end[e] ? -1.f : a[e];
+      mapB[wave][V * lane + e] = b[e];
+    }
+    __syncthreads();
+    bool all = true;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      for (int q = 0; q < NW; ++q) compose(A, S, done, e, mapA[q][V * lane + e], mapB[q][V * lane + e]);
+      all = all && done[e];
+    }
+    if (__all(all)) break;  // the same in every wave: they read the same maps
   }
 #pragma unroll
   for (int e = 0; e < V; ++e) state[e] = S[e];
@@ -246,6 +270,20 @@ __device__ __forceinline__ Pack<T, V> load_raw(const T *row, int c, int d) {
 #pragma unroll
   for (int e = 0; e < V; ++e) p.v[e] = c + e < d ? row[c + e] : (T)0.f;
   return p;
+}
+
+// The same for the byte offset of a channel that is known to hold a whole pack:
+// one load from a wave-uniform row, with no branch around it.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_at(const T *row, uint32_t bytes) {
+  return *(const Pack<T, V> *)((const char *)row + bytes);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_at(T *row, uint32_t bytes, const float (&v)[V]) {
+  Pack<T, V> p;
+#pragma unroll
+  for (int e = 0; e < V; ++e) p.v[e] = (T)v[e];
+  *(Pack<T, V> *)((char *)row + bytes) = p;
 }
 
 // Where a block's tile is. `ord`: position in its chain (0 runs first).
@@ -264,6 +302,7 @@ __device__ __forceinline__ Tile next_tile(const RecArgs &a, int nt) {
     id = ticket;
   }
   const unsigned cbs = (a.d + 64 * V - 1) / (64 * V), per = cbs * a.n;
+  id = __builtin_amdgcn_readfirstlane(id);
   return {(int)((id % per) / cbs), (int)(id % cbs), (int64_t)(id / per)};
 }
 
@@ -281,7 +320,7 @@ constexpr int64_t kSlotBase = 256;  // bytes in front of the slots: the tile cou
 template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
-  __shared__ float sA[NW][CH], sB[NW][CH], sIn[CH];
+  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW][CH], lB[NW][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   const int lane = threadIdx.x & 63, n = tl.n;
@@ -301,17 +340,27 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
       store_ch<float, V>(a.h_last + (int64_t)n * d, c, d, s);
     return;
   }
-  // the wave's tokens as local states hl (from a zero state) and products P
+  // the wave's tokens as local states hl (from a zero state) and products P.
+  // FAST: all R tokens, whole packs (d a multiple of V) and no document start,
+  // as most waves have it: straight code.
   float P[R][V], hl[R][V];
   const uint64_t cuts = start_bits<R>(a, n, tb, tb + cnt);
-  {
+  const bool fast = cnt == R && d % V == 0 && cuts == 0;
+  const uint32_t at = (c < d ? c : 0) * (uint32_t)sizeof(T);
+  const auto local = [&](auto tag) __attribute__((always_inline)) {
+    constexpr bool FAST = decltype(tag)::value;
     const T *g = seq_of<T>(a.g, n), *v = seq_of<T>(a.v, n);
     Pack<T, V> gr[R], vr[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t t = min(tb + r, len - 1);
-      gr[r] = load_raw<T, V>(g + t * a.g.tok_stride, c, d);
-      vr[r] = load_raw<T, V>(v + t * a.v.tok_stride, c, d);
+      const int64_t t = FAST ? tb + r : min(tb + r, len - 1);
+      if constexpr (FAST) {
+        gr[r] = load_at<T, V>(g + t * a.g.tok_stride, at);
+        vr[r] = load_at<T, V>(v + t * a.v.tok_stride, at);
+      } else {
+        gr[r] = load_raw<T, V>(g + t * a.g.tok_stride, c, d);
+        vr[r] = load_raw<T, V>(v + t * a.v.tok_stride, c, d);
+      }
     }
     float p[V], q[V];
 #pragma unroll
@@ -321,8 +370,8 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (r < cnt) {
-        const bool cut = cuts >> r & 1;
+      if (FAST || r < cnt) {
+        const bool cut = !FAST && (cuts >> r & 1);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float f, i;
@@ -338,7 +387,11 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
         hl[r][e] = q[e];
       }
     }
-  }
+  };
+  if (fast)
+    local(std::true_type());
+  else
+    local(std::false_type());
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     sA[wave][V * lane + e] = P[R - 1][e];
@@ -346,7 +399,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   }
   if (lane == 0) sCut[wave] = cuts != 0;
   __syncthreads();
-  // the map of the waves in front of this one; wave 0 takes the whole tile's
+  // the map of the waves in front of this one, and wave 0's of the whole tile
   const int upto = wave == 0 ? NW : wave;
   float A[V], B[V];
   bool cut = false;
@@ -365,44 +418,44 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
     }
     cut = cut || k;
   }
-  if (wave == 0) {
-    uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) +
-                     ((int64_t)tl.ord * a.n + n) * (int64_t)((d + CH - 1) / CH) * CH +
-                     (int64_t)tl.cb * CH + V * lane;
-    const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
-    const bool more = t0 + TT < len;  // a tile behind this one reads the slots
-    if (tl.ord > 0) {
-      if (more) {
+  const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
+  uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) + tl.ord * step +
+                   (int64_t)n * ((d + CH - 1) / CH) * CH + (int64_t)tl.cb * CH + V * lane;
+  const bool more = wave == 0 && t0 + TT < len;  // a tile behind this one reads the slots
+  if (tl.ord > 0) {
+    if (more) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
-      }
-      look_back<V>(mine - step, step, (int)tl.ord, s);
+      for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
     }
-    if (more && !(cut && tl.ord > 0)) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sIn[V * lane + e] = s[e];
+    look_back<V, NW>(mine - step, step, (int)tl.ord, lA, lB, s);
   }
-  __syncthreads();
+  if (more && !(cut && tl.ord > 0)) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
+  }
   if (wave > 0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      s[e] = sIn[V * lane + e];
-      s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
-    }
+    for (int e = 0; e < V; ++e) s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
   }
   if (c >= d) return;
   float o[V] = {};
+  if (fast) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (r < cnt) {
-      const bool k = (cuts & ((uint64_t)2 << r) - 1) != 0;
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = k ? hl[r][e] : fmaf(P[r][e], s[e], hl[r][e]);
-      store_ch<T, V>(h + (tb + r) * a.h.tok_stride, c, d, o);
+      for (int e = 0; e < V; ++e) o[e] = fmaf(P[r][e], s[e], hl[r][e]);
+      store_at<T, V>(h + (tb + r) * a.h.tok_stride, at, o);
     }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < cnt) {
+        const bool k = (cuts & ((uint64_t)2 << r) - 1) != 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = k ? hl[r][e] : fmaf(P[r][e], s[e], hl[r][e]);
+        store_ch<T, V>(h + (tb + r) * a.h.tok_stride, c, d, o);
+      }
+  }
   if (a.h_last && cnt > 0 && tb + cnt == len) store_ch<float, V>(a.h_last + (int64_t)n * d, c, d, o);
 }
 
@@ -411,7 +464,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
 template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
-  __shared__ float sA[NW][CH], sB[NW][CH], sIn[CH];
+  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW][CH], lB[NW][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   const int lane = threadIdx.x & 63, n = tl.n;
@@ -436,41 +489,59 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
     return;
   }
   const uint64_t cuts = start_bits<R>(a, n, tb, tb + cnt);
+  const bool fast = cnt == R && d % V == 0 && cuts == 0 && tb > 0;
+  const uint32_t at = (c < d ? c : 0) * (uint32_t)sizeof(T);
   Pack<T, V> gr[R], dr[R], vr[R], pr[R];
-  {
-    const T *g = seq_of<T>(a.g, n), *dh = seq_of<T>(a.dh, n);
-    const T *v = seq_of<T>(a.v, n), *h = seq_of<T>(a.h, n);
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-      const int64_t t = min(tb + r, len - 1);
-      gr[r] = load_raw<T, V>(g + t * a.g.tok_stride, c, d);
-      dr[r] = load_raw<T, V>(dh + t * a.dh.tok_stride, c, d);
-    }
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r) {  // used after the wait
-      const int64_t t = min(tb + r, len - 1);
-      vr[r] = load_raw<T, V>(v + t * a.v.tok_stride, c, d);
-      pr[r] = load_raw<T, V>(h + max(t - 1, (int64_t)0) * a.h.tok_stride, c, d);
-    }
-  }
   float A[V], B[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     A[e] = 1.f;
     B[e] = 0.f;
   }
+  // FAST: all R tokens with a token before them, whole packs, no document start
+  const auto local = [&](auto tag) __attribute__((always_inline)) {
+    constexpr bool FAST = decltype(tag)::value;
+    const T *g = seq_of<T>(a.g, n), *dh = seq_of<T>(a.dh, n);
+    const T *v = seq_of<T>(a.v, n), *h = seq_of<T>(a.h, n);
 #pragma unroll
-  for (int r = R - 1; r >= 0; --r)
-    if (r < cnt) {
-      const bool k = cuts >> r & 1;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float f, i;
-        gate((float)gr[r].v[e], f, i);
-        B[e] = k ? 0.f : f * ((float)dr[r].v[e] + B[e]);
-        A[e] *= f;
+    for (int r = R - 1; r >= 0; --r) {
+      const int64_t t = FAST ? tb + r : min(tb + r, len - 1);
+      if constexpr (FAST) {
+        gr[r] = load_at<T, V>(g + t * a.g.tok_stride, at);
+        dr[r] = load_at<T, V>(dh + t * a.dh.tok_stride, at);
+      } else {
+        gr[r] = load_raw<T, V>(g + t * a.g.tok_stride, c, d);
+        dr[r] = load_raw<T, V>(dh + t * a.dh.tok_stride, c, d);
       }
     }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {  // used after the wait
+      const int64_t t = FAST ? tb + r : min(tb + r, len - 1);
+      if constexpr (FAST) {
+        vr[r] = load_at<T, V>(v + t * a.v.tok_stride, at);
+        pr[r] = load_at<T, V>(h + (t - 1) * a.h.tok_stride, at);
+      } else {
+        vr[r] = load_raw<T, V>(v + t * a.v.tok_stride, c, d);
+        pr[r] = load_raw<T, V>(h + max(t - 1, (int64_t)0) * a.h.tok_stride, c, d);
+      }
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r)
+      if (FAST || r < cnt) {
+        const bool k = !FAST && (cuts >> r & 1);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float f, i;
+          gate((float)gr[r].v[e], f, i);
+          B[e] = k ? 0.f : f * ((float)dr[r].v[e] + B[e]);
+          A[e] *= f;
+        }
+      }
+  };
+  if (fast)
+    local(std::true_type());
+  else
+    local(std::false_type());
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     sA[wave][V * lane + e] = A[e];
@@ -478,7 +549,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
   }
   if (lane == 0) sCut[wave] = cuts != 0;
   __syncthreads();
-  // the map of the waves behind this one; the last wave takes the whole tile's
+  // the map of the waves behind this one, and the last wave's of the whole tile
   const int down = wave == NW - 1 ? 0 : wave + 1;
   bool cut = false;
 #pragma unroll
@@ -496,60 +567,65 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
     }
     cut = cut || k;
   }
-  if (wave == NW - 1) {
-    const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
-    uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) + tl.ord * step +
-                     (int64_t)n * ((d + CH - 1) / CH) * CH + (int64_t)tl.cb * CH + V * lane;
-    const bool more = tile > 0;
-    if (!first) {
-      if (more) {
+  const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
+  uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) + tl.ord * step +
+                   (int64_t)n * ((d + CH - 1) / CH) * CH + (int64_t)tl.cb * CH + V * lane;
+  const bool more = wave == NW - 1 && tile > 0;
+  if (!first) {
+    if (more) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
-      }
-      // tiles between this one and the sequence's last
-      look_back<V>(mine - step, step, (int)((len - 1) / TT - tile), s);
+      for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
     }
-    if (more && !(cut && !first)) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sIn[V * lane + e] = s[e];
+    // the tiles between this one and the sequence's last
+    look_back<V, NW>(mine - step, step, (int)((len - 1) / TT - tile), lA, lB, s);
   }
-  __syncthreads();
+  if (more && !(cut && !first)) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
+  }
   if (wave < NW - 1) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      s[e] = sIn[V * lane + e];
-      s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
-    }
+    for (int e = 0; e < V; ++e) s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
   }
   if (c >= d) return;
+  const auto finish = [&](auto tag) __attribute__((always_inline)) {
+    constexpr bool FAST = decltype(tag)::value;
 #pragma unroll
-  for (int r = R - 1; r >= 0; --r)
-    if (r < cnt) {
-      const bool k = cuts >> r & 1;
-      float prev[V], og[V], ov[V];
-      if (tb + r == 0) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) prev[e] = 0.f;
-        if (a.h0) load_ch<float, V>(a.h0 + (int64_t)n * d, c, d, prev);
-      } else {
+    for (int r = R - 1; r >= 0; --r)
+      if (FAST || r < cnt) {
+        const bool k = !FAST && (cuts >> r & 1);
+        float prev[V], og[V], ov[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) prev[e] = (float)pr[r].v[e];
-      }
+        if constexpr (!FAST) {
+          if (tb + r == 0) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float f, i;
-        gate((float)gr[r].v[e], f, i);
-        const float delta = (float)dr[r].v[e] + s[e];
-        ov[e] = i * delta;
-        og[e] = delta * ((k ? 0.f : prev[e]) - (float)vr[r].v[e]) * (f * i);
-        s[e] = k ? 0.f : f * delta;
+            for (int e = 0; e < V; ++e) prev[e] = 0.f;
+            if (a.h0) load_ch<float, V>(a.h0 + (int64_t)n * d, c, d, prev);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float f, i;
+          gate((float)gr[r].v[e], f, i);
+          const float delta = (float)dr[r].v[e] + s[e];
+          ov[e] = i * delta;
+          og[e] = delta * ((k ? 0.f : prev[e]) - (float)vr[r].v[e]) * (f * i);
+          s[e] = k ? 0.f : f * delta;
+        }
+        if constexpr (FAST) {
+          store_at<T, V>(dg + (tb + r) * a.dg.tok_stride, at, og);
+          store_at<T, V>(dv + (tb + r) * a.dv.tok_stride, at, ov);
+        } else {
+          store_ch<T, V>(dg + (tb + r) * a.dg.tok_stride, c, d, og);
+          store_ch<T, V>(dv + (tb + r) * a.dv.tok_stride, c, d, ov);
+        }
       }
-      store_ch<T, V>(dg + (tb + r) * a.dg.tok_stride, c, d, og);
-      store_ch<T, V>(dv + (tb + r) * a.dv.tok_stride, c, d, ov);
-    }
+  };
+  if (fast)
+    finish(std::true_type());
+  else
+    finish(std::false_type());
   if (a.dh0 && tb == 0) store_ch<float, V>(a.dh0 + (int64_t)n * d, c, d, s);
 }
 
@@ -568,7 +644,7 @@ constexpr int64_t SEQ_MAX = 16;
 
 template <typename T>
 struct Shape {  // channels per lane, tokens per wave (forward, backward), waves
-  static constexpr int V = 2, RF = 16, RB = sizeof(T) == 2 ? 16 : 8, NW = 8;
+  static constexpr int V = 2, RF = 16, RB = 8, NW = 8;
 };
 
 int64_t tile_slots(int n, int d, int64_t nt, int v) { return nt * n * round_up(d, 64 * v); }

@@ -165,44 +165,45 @@ def _invalid(msg: str) -> IptttError:
 
 
 def _dtype_of(t):
-    if t.dtype not in _DT:
+    dt = _DT.get(t.dtype)
+    if dt is None:
         raise IptttError(IPTTT_E_UNSUPPORTED, f"IPTTT_E_UNSUPPORTED: dtype {t.dtype}")
-    return _DT[t.dtype]
+    return dt
 
 
-def _like(name, t, shape, dtype, device):
-    """Checks a tensor's shape, type and device."""
-    if tuple(t.shape) != tuple(shape):
-        raise _invalid(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+def _is(name, t, dtype, device):
+    """Checks a tensor's type and device."""
+    if t.dtype is not dtype:
         raise _invalid(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise _invalid(f"{name} is on {t.device}, expected {device}")
-    return t
 
 
 def _dense(name, t, shape, dtype, device):
-    _like(name, t, shape, dtype, device)
+    if t.shape != shape:
+        raise _invalid(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _is(name, t, dtype, device)
     if not t.is_contiguous():
         raise _invalid(f"{name} must be contiguous")
     return t
 
 
-def _rows(name, t, d, dtype=None, device=None, n=None):
-    """(row stride) of a tensor of rows [..., d]: [n, d] of any row stride, or any
+def _rows(name, t, d, dtype, device, n=None):
+    """The row stride of a tensor of rows [..., d]: [n, d] of any row stride, or any
     number of leading dimensions laid out as equally spaced rows."""
-    if t.dim() < 1 or t.shape[-1] != d:
-        raise _invalid(f"{name} has shape {tuple(t.shape)}, expected rows of {d}")
-    if dtype is not None:
-        _like(name, t, t.shape, dtype, device)
+    shape = t.shape
+    if not shape or shape[-1] != d:
+        raise _invalid(f"{name} has shape {tuple(shape)}, expected rows of {d}")
+    _is(name, t, dtype, device)
     rows = t.numel() // d
     if n is not None and rows != n:
         raise _invalid(f"{name} has {rows} rows, expected {n}")
+    if t.is_contiguous():
+        return d
     if rows > 0 and d > 1 and t.stride(-1) != 1:
         raise _invalid(f"{name} must have its last dimension contiguous")
-    stride, span = d, 1
-    first = True
-    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    stride, span, first = d, 1, True
+    for size, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if first:
@@ -213,17 +214,33 @@ def _rows(name, t, d, dtype=None, device=None, n=None):
     return stride
 
 
+# The current stream's handle without building a torch.cuda.Stream for it, which
+# takes about as long as a small kernel.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, device):
+    """The HIP stream of a call whose tensors are on `device`."""
+    if device.type != "cuda":
+        raise _invalid(f"tensors are on {device}, not on a GPU")
+    if device.index != torch.cuda.current_device():
+        raise _invalid(f"tensors are on {device}, the current device is cuda:"
+                       f"{torch.cuda.current_device()}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
 def _temp(nbytes, device, stream):
     """Workspace from torch's allocator. On a stream other than the current one the
     allocator is told, so the memory is not handed out again while the call runs."""
     t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _used_on(stream, t)
+    if stream is not None:
+        _used_on(stream, t)
     return t
 
 
 def _used_on(stream, *tensors):
-    if stream is None:
-        return
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     if stream != torch.cuda.current_stream(stream.device):
@@ -248,66 +265,75 @@ class Norm:
     def forward(self, x, res=None, stream=None):
         """Returns (y, h, mean, rstd): h = x + res (x itself without res), y its norm,
         and the rows' statistics for the backward. x, res: [..., d]."""
-        xs = _rows("x", x, self.d, self.dtype, self.device)
-        lead = x.shape[:-1]
-        n = x.numel() // self.d
-        y = torch.empty(x.shape, dtype=self.dtype, device=self.device)
-        stats = torch.empty((2,) + tuple(lead), dtype=torch.float32, device=self.device)
-        mean, rstd = stats[0], stats[1]
+        d, dtype, dev = self.d, self.dtype, self.device
+        xs = _rows("x", x, d, dtype, dev)
+        st = _on(stream, dev)
+        shape = x.shape
+        n = x.numel() // d
+        y = torch.empty(shape, dtype=dtype, device=dev)
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         rs, h = 0, None
         if res is not None:
-            rs = _rows("res", res, self.d, self.dtype, self.device, n)
-            h = torch.empty(x.shape, dtype=self.dtype, device=self.device)
-        ipttt_norm_forward(self.desc, x, xs, res, rs, n, h, y, mean, rstd, stream)
-        _used_on(stream, x, res, h, y, stats, self.gamma, self.beta)
+            rs = _rows("res", res, d, dtype, dev, n)
+            h = torch.empty(shape, dtype=dtype, device=dev)
+        ipttt_norm_forward(self.desc, x, xs, res, rs, n, h, y, mean, rstd, st)
+        if stream is not None:
+            _used_on(stream, x, res, h, y, mean, rstd, self.gamma, self.beta)
         return y, (x if h is None else h), mean, rstd
 
     def backward(self, h, mean, rstd, dy, dh=None, stream=None):
         """Returns {"dx", "dgamma", "dbeta"}: the gradient of x and res ([..., d], the
         activations' dtype) and the fp32 weight gradients, from dL/dy and dL/dh."""
-        hs = _rows("h", h, self.d, self.dtype, self.device)
-        n = h.numel() // self.d
-        ds = _rows("dy", dy, self.d, self.dtype, self.device, n)
-        hh = 0 if dh is None else _rows("dh", dh, self.d, self.dtype, self.device, n)
+        d, dtype, dev = self.d, self.dtype, self.device
+        hs = _rows("h", h, d, dtype, dev)
+        st = _on(stream, dev)
+        n = h.numel() // d
+        ds = _rows("dy", dy, d, dtype, dev, n)
+        hh = 0 if dh is None else _rows("dh", dh, d, dtype, dev, n)
         for name, t in (("mean", mean), ("rstd", rstd)):
             if t.numel() != n:
                 raise _invalid(f"{name} has {t.numel()} values, expected {n}")
-            _dense(name, t, t.shape, torch.float32, self.device)
-        dx = torch.empty(h.shape, dtype=self.dtype, device=self.device)
-        sums = torch.empty((2, self.d), dtype=torch.float32, device=self.device)
+            _dense(name, t, t.shape, torch.float32, dev)
+        dx = torch.empty(h.shape, dtype=dtype, device=dev)
+        dgamma = torch.empty(d, dtype=torch.float32, device=dev)
+        dbeta = torch.empty(d, dtype=torch.float32, device=dev)
         need = ipttt_norm_backward_workspace_bytes(self.desc, n)
-        ws = _temp(need, self.device, stream)
-        ipttt_norm_backward(self.desc, h, hs, mean, rstd, dy, ds, dh, hh, n, dx, sums[0], sums[1],
-                            ws, need, stream)
-        _used_on(stream, h, mean, rstd, dy, dh, dx, sums, self.gamma)
-        return {"dx": dx, "dgamma": sums[0], "dbeta": sums[1]}
+        ws = _temp(need, dev, stream)
+        ipttt_norm_backward(self.desc, h, hs, mean, rstd, dy, ds, dh, hh, n, dx, dgamma, dbeta, ws,
+                            need, st)
+        if stream is not None:
+            _used_on(stream, h, mean, rstd, dy, dh, dx, dgamma, dbeta, self.gamma)
+        return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
 
 
 def _view(name, t, shape, dtype, device):
-    _like(name, t, shape, dtype, device)
-    if t.numel() and shape[2] > 1 and t.stride(2) != 1:
+    """A View of a [batch, seq_len, d] tensor, or of [batch, d] as one token each."""
+    if t.shape != shape:
+        raise _invalid(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _is(name, t, dtype, device)
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] > 1 and t.numel():
         raise _invalid(f"{name} must have its channels contiguous")
-    return View(p=t.data_ptr(), seq_stride=t.stride(0), tok_stride=t.stride(1))
+    return View(t.data_ptr(), stride[0], stride[-2])
 
 
-def _recurrence(g, v, h, h0, starts, lens):
-    if g.dim() != 3:
-        raise _invalid("g must be [batch, seq_len, d]")
-    n, length, d = g.shape
-    dev = g.device
-    r = RecurrenceDesc(batch=n, d=d, seq_len=length, dtype=_dtype_of(g))
-    r.g = _view("g", g, g.shape, g.dtype, dev)
-    r.v = _view("v", v, g.shape, g.dtype, dev)
-    r.h = _view("h", h, g.shape, g.dtype, dev)
+def _recurrence(g, v, h, h0, starts=None, lens=None):
+    shape, dtype, dev = g.shape, g.dtype, g.device
+    n, d = shape[0], shape[-1]
+    length = shape[1] if len(shape) == 3 else 1
+    dt = _dtype_of(g)
     if h0 is not None:
-        r.h0 = _p(_dense("h0", h0, (n, d), torch.float32, dev))
+        h0 = _dense("h0", h0, (n, d), torch.float32, dev).data_ptr()
     if starts is not None:
-        if starts.dtype == torch.bool:
+        if starts.dtype is torch.bool:
             starts = starts.view(torch.uint8)
-        r.starts = _p(_dense("starts", starts, (n, length), torch.uint8, dev))
+        starts = _dense("starts", starts, (n, length), torch.uint8, dev).data_ptr()
     if lens is not None:
-        r.lens = _p(_dense("lens", lens, (n,), torch.int32, dev))
-    return r
+        lens = _dense("lens", lens, (n,), torch.int32, dev).data_ptr()
+    return RecurrenceDesc(n, d, length, dt, _view("g", g, shape, dtype, dev),
+                          _view("v", v, shape, dtype, dev), _view("h", h, shape, dtype, dev), starts,
+                          lens, h0)
 
 
 def recurrence_forward(g, v, h0=None, starts=None, lens=None, stream=None):
@@ -315,13 +341,18 @@ def recurrence_forward(g, v, h0=None, starts=None, lens=None, stream=None):
     (slices of a wider tensor will do). h0: fp32 [batch, d]; starts: bool or uint8
     [batch, seq_len], nonzero where a packed document begins; lens: int32 [batch].
     Returns (h, h_last): h like g, h_last fp32 [batch, d], the state for the next call."""
-    h = torch.empty(g.shape, dtype=g.dtype, device=g.device)
+    if g.dim() != 3:
+        raise _invalid("g must be [batch, seq_len, d]")
+    dev = g.device
+    st = _on(stream, dev)
+    h = torch.empty(g.shape, dtype=g.dtype, device=dev)
     r = _recurrence(g, v, h, h0, starts, lens)
-    last = torch.empty((r.batch, r.d), dtype=torch.float32, device=g.device)
+    last = torch.empty((r.batch, r.d), dtype=torch.float32, device=dev)
     need = ipttt_recurrence_workspace_bytes(r)
-    ws = _temp(need, g.device, stream)
-    ipttt_recurrence_forward(r, last, ws, need, stream)
-    _used_on(stream, g, v, h0, starts, lens, h, last)
+    ws = _temp(need, dev, stream)
+    ipttt_recurrence_forward(r, last, ws, need, st)
+    if stream is not None:
+        _used_on(stream, g, v, h0, starts, lens, h, last)
     return h, last
 
 
@@ -330,14 +361,17 @@ def recurrence_step(g, v, state, out=None, stream=None):
     Returns (h [batch, d], the new state); pass out=state to update it in place."""
     if g.dim() != 2:
         raise _invalid("g must be [batch, d]")
-    h = torch.empty(g.shape, dtype=g.dtype, device=g.device)
-    r = _recurrence(g.unsqueeze(1), v.unsqueeze(1), h.unsqueeze(1), state, None, None)
+    dev = g.device
+    st = _on(stream, dev)
+    h = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    r = _recurrence(g, v, h, state)
     if out is None:
-        out = torch.empty(g.shape, dtype=torch.float32, device=g.device)
+        out = torch.empty(g.shape, dtype=torch.float32, device=dev)
     else:
-        _dense("out", out, g.shape, torch.float32, g.device)
-    ipttt_recurrence_step(r, out, stream)
-    _used_on(stream, g, v, state, h, out)
+        _dense("out", out, g.shape, torch.float32, dev)
+    ipttt_recurrence_step(r, out, st)
+    if stream is not None:
+        _used_on(stream, g, v, state, h, out)
     return h, out
 
 
@@ -346,19 +380,23 @@ def recurrence_backward(g, v, h, dh, h0=None, dh_last=None, starts=None, lens=No
     """Gradients of recurrence_forward from its output h, dL/dh and dL/dh_last (fp32
     [batch, d] or None): {"dg", "dv", "dh0"}. dg and dv may be passed in (for
     example the two halves of one projection's gradient)."""
+    if g.dim() != 3:
+        raise _invalid("g must be [batch, seq_len, d]")
+    shape, dtype, dev = g.shape, g.dtype, g.device
+    st = _on(stream, dev)
     r = _recurrence(g, v, h, h0, starts, lens)
-    dev = g.device
-    dg = torch.empty(g.shape, dtype=g.dtype, device=dev) if dg is None else dg
-    dv = torch.empty(g.shape, dtype=g.dtype, device=dev) if dv is None else dv
+    dg = torch.empty(shape, dtype=dtype, device=dev) if dg is None else dg
+    dv = torch.empty(shape, dtype=dtype, device=dev) if dv is None else dv
     dh0 = torch.empty((r.batch, r.d), dtype=torch.float32, device=dev)
     if dh_last is not None:
         _dense("dh_last", dh_last, (r.batch, r.d), torch.float32, dev)
     need = ipttt_recurrence_workspace_bytes(r)
     ws = _temp(need, dev, stream)
-    ipttt_recurrence_backward(r, _view("dh", dh, g.shape, g.dtype, dev), dh_last,
-                              _view("dg", dg, g.shape, g.dtype, dev),
-                              _view("dv", dv, g.shape, g.dtype, dev), dh0, ws, need, stream)
-    _used_on(stream, g, v, h, dh, h0, dh_last, starts, lens, dg, dv, dh0)
+    ipttt_recurrence_backward(r, _view("dh", dh, shape, dtype, dev), dh_last,
+                              _view("dg", dg, shape, dtype, dev), _view("dv", dv, shape, dtype, dev),
+                              dh0, ws, need, st)
+    if stream is not None:
+        _used_on(stream, g, v, h, dh, h0, dh_last, starts, lens, dg, dv, dh0)
     return {"dg": dg, "dv": dv, "dh0": dh0}
 
 
@@ -379,34 +417,39 @@ class FeedForward:
 
     def forward(self, x, save: bool = False, stream=None):
         """x: [..., d]. Returns y, or (y, a, u) with the pre-activations for the backward."""
-        xs = _rows("x", x, self.d, self.dtype, self.device)
-        n = x.numel() // self.d
-        y = torch.empty(x.shape, dtype=self.dtype, device=self.device)
+        d, dtype, dev = self.d, self.dtype, self.device
+        xs = _rows("x", x, d, dtype, dev)
+        st = _on(stream, dev)
+        n = x.numel() // d
+        y = torch.empty(x.shape, dtype=dtype, device=dev)
         a = u = None
         if save:
-            a = torch.empty(x.shape[:-1] + (self.d_ff,), dtype=self.dtype, device=self.device)
+            a = torch.empty(x.shape[:-1] + (self.d_ff,), dtype=dtype, device=dev)
             u = torch.empty_like(a)
         need = ipttt_ff_workspace_bytes(self.desc, n)
-        ws = _temp(need, self.device, stream)
-        ipttt_ff_forward(self.desc, x, xs, n, y, self.d, a, u, ws, need, stream)
-        _used_on(stream, x, y, a, u, self.w_gate, self.w_up, self.w_down)
+        ws = _temp(need, dev, stream)
+        ipttt_ff_forward(self.desc, x, xs, n, y, d, a, u, ws, need, st)
+        if stream is not None:
+            _used_on(stream, x, y, a, u, self.w_gate, self.w_up, self.w_down)
         return (y, a, u) if save else y
 
     def backward(self, x, a, u, dy, stream=None):
         """Gradients from dL/dy and the saved pre-activations: {"dx", "dw_gate", "dw_up",
         "dw_down"}, all in the weights' dtype."""
-        xs = _rows("x", x, self.d, self.dtype, self.device)
-        n = x.numel() // self.d
-        ds = _rows("dy", dy, self.d, self.dtype, self.device, n)
+        d, f, dtype, dev = self.d, self.d_ff, self.dtype, self.device
+        xs = _rows("x", x, d, dtype, dev)
+        st = _on(stream, dev)
+        n = x.numel() // d
+        ds = _rows("dy", dy, d, dtype, dev, n)
         for name, t in (("a", a), ("u", u)):
-            _dense(name, t, x.shape[:-1] + (self.d_ff,), self.dtype, self.device)
-        new = lambda s: torch.empty(s, dtype=self.dtype, device=self.device)  # noqa: E731
-        g = {"dx": new(x.shape), "dw_gate": new((self.d_ff, self.d)), "dw_up": new((self.d_ff, self.d)),
-             "dw_down": new((self.d, self.d_ff))}
+            _dense(name, t, x.shape[:-1] + (f,), dtype, dev)
+        new = lambda *s: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
+        g = {"dx": new(*x.shape), "dw_gate": new(f, d), "dw_up": new(f, d), "dw_down": new(d, f)}
         need = ipttt_ff_backward_workspace_bytes(self.desc, n)
-        ws = _temp(need, self.device, stream)
+        ws = _temp(need, dev, stream)
         ipttt_ff_backward(self.desc, x, xs, a, u, dy, ds, n,
-                          FFGrads(dx_stride=self.d, **{k: _p(t) for k, t in g.items()}), ws, need,
-                          stream)
-        _used_on(stream, x, a, u, dy, self.w_gate, self.w_up, self.w_down, *g.values())
+                          FFGrads(_p(g["dx"]), d, _p(g["dw_gate"]), _p(g["dw_up"]), _p(g["dw_down"])),
+                          ws, need, st)
+        if stream is not None:
+            _used_on(stream, x, a, u, dy, self.w_gate, self.w_up, self.w_down, *g.values())
         return g

@@ -186,7 +186,7 @@ __device__ __forceinline__ uint64_t slot_get(const uint64_t *p) {
 // side by side (one trip to memory covers NW LB tiles), reduce each run to one
 // map, and every wave composes the runs' maps from LDS. Called by the whole
 // block; all waves get the same state.
-constexpr int LB = 4;
+constexpr int LB = 2;
 
 template <int V, int NW>
 __device__ __forceinline__ void look_back(const uint64_t *at, int64_t step, int count,
@@ -642,16 +642,21 @@ __global__ __launch_bounds__(256) void k_rec_clear(uint64_t *ws, int64_t slots) 
 
 constexpr int64_t SEQ_MAX = 16;
 
-template <typename T>
-struct Shape {  // channels per lane, tokens per wave (forward, backward), waves
-  static constexpr int V = 2, RF = 16, RB = 8, NW = 8;
-};
+// Channels per lane, tokens per wave in the forward and the backward, waves.
+// Measured (128k x 2560 forward / 8 x 16k x 2048 backward, bf16): 16 tokens, 8
+// waves 485 / 609 us; 8 tokens 688 / 686; 32 tokens (forward) 476; 4 waves of 16
+// 572 / 640; 16 waves of 8 (backward) 760; 4 channels a lane 725 / 899 and up
+// (registers). Look-back runs of 1, 2, 4, 8 tiles a wave: 501, 485, 492, 526.
+constexpr int kV = 2, kFwdTokens = 16, kBwdTokens = 16, kWaves = 8;
+constexpr int kFwdTile = kFwdTokens * kWaves, kBwdTile = kBwdTokens * kWaves;
+constexpr int kMinTile = kFwdTile < kBwdTile ? kFwdTile : kBwdTile;  // what the workspace holds
 
-int64_t tile_slots(int n, int d, int64_t nt, int v) { return nt * n * round_up(d, 64 * v); }
+int64_t channel_blocks(int d) { return (d + 64 * kV - 1) / (64 * kV); }
+int64_t tile_slots(int n, int d, int64_t nt) { return nt * n * channel_blocks(d) * 64 * kV; }
 
-hipError_t clear_slots(const RecArgs &a, int64_t nt, int v, hipStream_t st) {
+hipError_t clear_slots(const RecArgs &a, int64_t nt, hipStream_t st) {
   if (nt <= 1) return hipSuccess;
-  const int64_t slots = tile_slots(a.n, a.d, nt, v);
+  const int64_t slots = tile_slots(a.n, a.d, nt);
   hipLaunchKernelGGL(k_rec_clear, dim3((unsigned)std::min<int64_t>((slots + 511) / 512, 2048)),
                      dim3(256), 0, st, (uint64_t *)a.ws, slots);
   return hipGetLastError();
@@ -659,17 +664,14 @@ hipError_t clear_slots(const RecArgs &a, int64_t nt, int v, hipStream_t st) {
 
 }  // namespace
 
-// the smallest tile of any type's forward and backward
-constexpr int kMinTile = Shape<float>::RB * Shape<float>::NW;
-
 bool rec_size_ok(int n, int d, int64_t L) {
-  const int64_t nt = (L + kMinTile - 1) / kMinTile, cb = (d + 64 * Shape<float>::V - 1) / (64 * Shape<float>::V);
-  return nt * n <= INT32_MAX && nt * n * cb <= INT32_MAX;
+  const int64_t nt = (L + kMinTile - 1) / kMinTile;
+  return nt * n <= INT32_MAX && nt * n * channel_blocks(d) <= INT32_MAX;
 }
 
 size_t rec_workspace(int n, int d, int64_t L) {
   const int64_t nt = (L + kMinTile - 1) / kMinTile;
-  return (size_t)kSlotBase + (L <= SEQ_MAX || nt <= 1 ? 0 : 8 * tile_slots(n, d, nt, Shape<float>::V));
+  return (size_t)kSlotBase + (L <= SEQ_MAX || nt <= 1 ? 0 : 8 * tile_slots(n, d, nt));
 }
 
 template <typename T>
@@ -682,30 +684,28 @@ hipError_t rec_step(const RecArgs &a, hipStream_t st) {
 template <typename T>
 hipError_t rec_forward(const RecArgs &a, hipStream_t st) {
   if (a.L <= SEQ_MAX) return rec_step<T>(a, st);
-  using S = Shape<T>;
-  const int64_t nt = (a.L + S::RF * S::NW - 1) / (S::RF * S::NW);
-  const hipError_t e = clear_slots(a, nt, S::V, st);
+  const int64_t nt = (a.L + kFwdTile - 1) / kFwdTile;
+  const hipError_t e = clear_slots(a, nt, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_rec_fwd<T, S::V, S::RF, S::NW>),
-                     dim3((unsigned)(nt * a.n * ((a.d + 64 * S::V - 1) / (64 * S::V)))),
-                     dim3(64 * S::NW), 0, st, a, (int)nt);
+  hipLaunchKernelGGL((k_rec_fwd<T, kV, kFwdTokens, kWaves>),
+                     dim3((unsigned)(nt * a.n * channel_blocks(a.d))), dim3(64 * kWaves), 0, st, a,
+                     (int)nt);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t rec_backward(const RecArgs &a, hipStream_t st) {
-  using S = Shape<T>;
   if (a.L <= SEQ_MAX) {
     hipLaunchKernelGGL(k_rec_seq_bwd<T>, dim3((a.d + 64 * SEQ_V - 1) / (64 * SEQ_V), a.n), dim3(64),
                        0, st, a);
     return hipGetLastError();
   }
-  const int64_t nt = (a.L + S::RB * S::NW - 1) / (S::RB * S::NW);
-  const hipError_t e = clear_slots(a, nt, S::V, st);
+  const int64_t nt = (a.L + kBwdTile - 1) / kBwdTile;
+  const hipError_t e = clear_slots(a, nt, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_rec_bwd<T, S::V, S::RB, S::NW>),
-                     dim3((unsigned)(nt * a.n * ((a.d + 64 * S::V - 1) / (64 * S::V)))),
-                     dim3(64 * S::NW), 0, st, a, (int)nt);
+  hipLaunchKernelGGL((k_rec_bwd<T, kV, kBwdTokens, kWaves>),
+                     dim3((unsigned)(nt * a.n * channel_blocks(a.d))), dim3(64 * kWaves), 0, st, a,
+                     (int)nt);
   return hipGetLastError();
 }
 

@@ -18,6 +18,7 @@
 // 2^-24 of a product: fp32 accuracy at six times the bf16 work, against
 // 1/16 of the bf16 rate for the fp32 MFMA.
 #include <algorithm>
+#include <type_traits>
 
 #include "block_internal.h"
 #include "mfma_common.h"
@@ -78,10 +79,18 @@ struct FfProb {
   int M, N, nk;
   int splits;  // parts of K, each its own blocks (epilogue: partial sums)
 };
+// Independent products of one launch: problem p has the blocks start[p] ..
+// start[p + 1], a multiple of 8, so that its tiles keep their XCDs.
+template <class Epi, int G>
+struct FfGroup {
+  FfProb prob[G];
+  Epi epi[G];
+  int start[G + 1];
+};
 
-template <class C, int NP, bool DUAL, class Epi>
+template <class C, int NP, bool DUAL, class Epi, int G>
 __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_ff_gemm(
-    FfProb g, Epi epi) {
+    FfGroup<Epi, G> grp) {
   static_assert(C::SMEM_ELEMS * 2 <= 160 * 1024, "LDS overflow");
   __shared__ __attribute__((aligned(1024))) __bf16 smem[C::SMEM_ELEMS];
   using M = typename C::M;
@@ -89,8 +98,15 @@ __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC)
   constexpr int MT = DUAL ? C::BM / 2 : C::BM;    // output rows per block
   constexpr int WT = DUAL ? C::WTM / 2 : C::WTM;  // and per wave
   constexpr int HI = DUAL ? C::MI / 2 : C::MI;
+  int which = 0;
+#pragma unroll
+  for (int p = 1; p < G; ++p) which += (int)blockIdx.x >= grp.start[p];
+  const FfProb g = grp.prob[which];
+  const Epi epi = grp.epi[which];
   const int nm = (g.M + MT - 1) / MT, nn = (g.N + C::BN - 1) / C::BN;
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int blocks = nm * nn * g.splits, bid = blockIdx.x - grp.start[which];
+  if (bid >= blocks) return;
+  const int id = xcd_remap(bid, blocks);
   const int sp = id / (nm * nn);
   int tm, tn;
   tile_of<C::GM>(id % (nm * nn), nm, nn, tm, tn);
@@ -118,10 +134,10 @@ __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC)
   // this block's steps of the (plane pair, K step) sequence
   constexpr int PAIRS = NP == 1 ? 1 : 6;
   const int total = PAIRS * g.nk, per = (total + g.splits - 1) / g.splits;
-  const int first = sp * per, count = min(per, total - first);
+  const int first = sp * per;
   int pair = NP == 1 ? 0 : first / g.nk, ks = NP == 1 ? first : first % g.nk;
   kloop_dma_pl<C, 2, true, C::MI + C::NJ>(
-      smem, la, lb, count, wave, acc,
+      smem, la, lb, min(per, total - first), wave, acc,
       [&](const __bf16 *As, const __bf16 *Bs, int u, Frags<C> &f) __attribute__((always_inline)) {
         const int r = M::orow(lane), kq = M::okoff(lane);
 #pragma unroll
@@ -161,35 +177,46 @@ __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC)
       v[4 + r] = __builtin_bit_cast(float, (unsigned)s[1]);
     }
   };
+  const auto write = [&](auto tag) __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(tag)::value;
 #pragma unroll
-  for (int i = 0; i < HI; i += 2) {
-    const int m = m0 + wm * WT + C::FM * i + 8 * (gq >> 1) + C::FM * (gq & 1);
-    typename Epi::In in[C::NJ];
+    for (int i = 0; i < HI; i += 2) {
+      const int m = m0 + wm * WT + C::FM * i + 8 * (gq >> 1) + C::FM * (gq & 1);
+      typename Epi::In in[C::NJ];
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j)  // all loads of these tiles before their stores
-      in[j] = epi.load(m, min(n0 + brow[j] + M::rcol(lane), g.N - 1));
+      for (int j = 0; j < C::NJ; ++j) {  // all loads of these tiles before their stores
+        const int n = n0 + brow[j] + M::rcol(lane);
+        in[j] = epi.template load<FULL>(m, FULL ? n : min(n, g.N - 1));
+      }
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) {
-      const int n = n0 + brow[j] + M::rcol(lane);
-      float v[8];
-      rows8(acc[i][j], acc[i + 1][j], v);
-      if constexpr (DUAL) {
-        float w[8];
-        rows8(acc[i + HI][j], acc[i + HI + 1][j], w);
-        if (n < g.N) epi.store(m, n, v, w);
-      } else {
-        if (n < g.N) epi.store(m, n, v, in[j], sp);
+      for (int j = 0; j < C::NJ; ++j) {
+        const int n = n0 + brow[j] + M::rcol(lane);
+        float v[8];
+        rows8(acc[i][j], acc[i + 1][j], v);
+        if constexpr (DUAL) {
+          float w[8];
+          rows8(acc[i + HI][j], acc[i + HI + 1][j], w);
+          if (FULL || n < g.N) epi.template store<FULL>(m, n, v, w);
+        } else {
+          if (FULL || n < g.N) epi.template store<FULL>(m, n, v, in[j], sp);
+        }
       }
     }
-  }
+  };
+  // whole tiles store without predicates: each would make every later memory
+  // operation of the wave wait (16384 tokens of the 4B-shaped forward 2.50 -> 2.02 ms)
+  if (m0 + MT <= g.M && n0 + C::BN <= g.N && epi.whole())
+    write(std::true_type());
+  else
+    write(std::false_type());
 }
 
 struct NoIn {};
 
 // 8 outputs m .. m + 7 of a row of M
-template <typename T>
+template <typename T, bool FULL = false>
 __device__ __forceinline__ void store8(T *row, int m, int M, const float (&v)[8]) {
-  if (m + 8 <= M) {
+  if (FULL || m + 8 <= M) {
     blk::store_pack<T, 8>(row + m, v);
   } else {
 #pragma unroll
@@ -207,6 +234,16 @@ __device__ __forceinline__ void load8(const T *row, int m, int M, float (&v)[8])
   }
 }
 
+// 8 values m .. m + 7 of a row of M as they are stored, zero past it
+template <typename T, bool FULL>
+__device__ __forceinline__ Pack<T, 8> pack8(const T *row, int m, int M) {
+  if (FULL || m + 8 <= M) return *(const Pack<T, 8> *)(row + m);
+  Pack<T, 8> p;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p.v[e] = m + e < M ? row[m + e] : (T)0.f;
+  return p;
+}
+
 // z = SiLU(a) u as the next product's operand (padded with zeros to Fp), and a,
 // u themselves when saved.
 template <typename T>
@@ -216,44 +253,53 @@ struct EpiZ {
   int64_t plane;
   int F, Fp;
   T *a, *u;
-  __device__ In load(int, int) const { return {}; }
+  template <bool FULL>
+  __device__ In load(int, int) const {
+    return {};
+  }
+  __device__ bool whole() const { return true; }
+  template <bool FULL>
   __device__ void store(int m, int n, const float (&av)[8], const float (&uv)[8]) const {
-    if (m >= Fp) return;
+    if (!FULL && m >= Fp) return;
     float zv[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      zv[e] = m + e < F ? av[e] * fast_sigmoid(av[e]) * uv[e] : 0.f;
+      zv[e] = FULL || m + e < F ? av[e] * fast_sigmoid(av[e]) * uv[e] : 0.f;
     store8_planes<planes_of<T>()>(z + (int64_t)n * Fp + m, plane, zv);
     if (a) {
-      store8<T>(a + (int64_t)n * F, m, F, av);
-      store8<T>(u + (int64_t)n * F, m, F, uv);
+      store8<T, FULL>(a + (int64_t)n * F, m, F, av);
+      store8<T, FULL>(u + (int64_t)n * F, m, F, uv);
     }
   }
 };
 
-// out[n][m], rows ld apart; columns n >= cut go to out2 (n - cut).
+// out[n][m], rows ld apart; columns n >= cut go to out2 (n - cut). With part: the
+// sums of one part of K instead, fp32 [part][n][part_ld].
 template <typename T>
 struct EpiOut {
   using In = NoIn;
   T *out, *out2;
   int64_t ld;
   int M, N, cut;  // N: rows of each output
-  __device__ In load(int, int) const { return {}; }
-  __device__ void store(int m, int n, const float (&v)[8], In, int) const {
+  float *part;
+  int64_t part_stride, part_ld;
+  template <bool FULL>
+  __device__ In load(int, int) const {
+    return {};
+  }
+  // a tile may hold columns between the two outputs
+  __device__ bool whole() const { return part || !out2 || cut == N; }
+  template <bool FULL>
+  __device__ void store(int m, int n, const float (&v)[8], In, int sp) const {
+    if (part) {
+      if (FULL || m < part_ld)
+        blk::store_pack<float, 8>(part + sp * part_stride + (int64_t)n * part_ld + m, v);
+      return;
+    }
     const bool second = n >= cut;
     const int row = second ? n - cut : n;
-    if (m < M && row < N) store8<T>((second ? out2 : out) + (int64_t)row * ld, m, M, v);
-  }
-};
-
-// Partial sums of one part of K: fp32 [part][n][ld], ld a multiple of 8.
-struct EpiPart {
-  using In = NoIn;
-  float *out;
-  int64_t stride, ld;
-  __device__ In load(int, int) const { return {}; }
-  __device__ void store(int m, int n, const float (&v)[8], In, int sp) const {
-    if (m < ld) blk::store_pack<float, 8>(out + sp * stride + (int64_t)n * ld + m, v);
+    if (FULL || (m < M && row < N))
+      store8<T, FULL>((second ? out2 : out) + (int64_t)row * ld, m, M, v);
   }
 };
 
@@ -262,28 +308,29 @@ struct EpiPart {
 template <typename T>
 struct EpiDz {
   struct In {
-    float a[8], u[8];
+    Pack<T, 8> a, u;
   };
   const T *a, *u;
   __bf16 *dau, *z;  // [n][2 Fp]: dA then dU; [n][Fp]
   int64_t dau_plane, z_plane;
   int F, Fp;
+  __device__ bool whole() const { return true; }
+  template <bool FULL>
   __device__ In load(int m, int n) const {
-    In in;
-    load8<T>(a + (int64_t)n * F, m, F, in.a);
-    load8<T>(u + (int64_t)n * F, m, F, in.u);
-    return in;
+    return {pack8<T, FULL>(a + (int64_t)n * F, m, F), pack8<T, FULL>(u + (int64_t)n * F, m, F)};
   }
+  template <bool FULL>
   __device__ void store(int m, int n, const float (&v)[8], const In &in, int) const {
-    if (m >= Fp) return;
+    if (!FULL && m >= Fp) return;
     float da[8], du[8], zv[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const bool real = m + e < F;
-      const float s = fast_sigmoid(in.a[e]), h = in.a[e] * s;
-      da[e] = real ? v[e] * in.u[e] * (s + h * (1.f - s)) : 0.f;
+      const bool real = FULL || m + e < F;
+      const float av = (float)in.a.v[e], uv = (float)in.u.v[e];
+      const float s = fast_sigmoid(av), h = av * s;
+      da[e] = real ? v[e] * uv * (s + h * (1.f - s)) : 0.f;
       du[e] = real ? v[e] * h : 0.f;
-      zv[e] = real ? h * in.u[e] : 0.f;
+      zv[e] = real ? h * uv : 0.f;
     }
     constexpr int NP = planes_of<T>();
     __bf16 *row = dau + (int64_t)n * 2 * Fp + m;
@@ -293,74 +340,95 @@ struct EpiDz {
   }
 };
 
-// out[n][m] = sum of the parts, in order
+// out[n][m] = sum of the parts, in order, for up to G products (gridDim.y)
 template <typename T>
-__global__ __launch_bounds__(256) void k_ff_join(const float *__restrict__ part, int parts,
-                                                 int64_t stride, int64_t ld, int64_t n, int M,
-                                                 T *__restrict__ out, int64_t out_ld) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t per = ld / 8;
-  if (i >= n * per) return;
-  const int64_t row = i / per;
-  const int m = 8 * (int)(i % per);
-  float s[8] = {};
-  for (int p = 0; p < parts; ++p) {
-    float v[8];
-    blk::load_pack<float, 8>(part + p * stride + row * ld + m, v);
+struct FfJoin {
+  EpiOut<T> e;
+  int parts, n;  // n: columns of the product
+};
+template <typename T, int G>
+struct FfJoins {
+  FfJoin<T> j[G];
+};
+template <typename T, int G>
+__global__ __launch_bounds__(256) void k_ff_join(FfJoins<T, G> js) {
+  const FfJoin<T> j = js.j[blockIdx.y];
+  const int64_t per = j.e.part_ld / 8, count = per * j.n;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
+    const int n = (int)(i / per), m = 8 * (int)(i % per);
+    float s[8] = {};
+    for (int p = 0; p < j.parts; ++p) {
+      float v[8];
+      blk::load_pack<float, 8>(j.e.part + p * j.e.part_stride + (int64_t)n * j.e.part_ld + m, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] += v[e];
+      for (int e = 0; e < 8; ++e) s[e] += v[e];
+    }
+    const bool second = n >= j.e.cut;
+    const int row = second ? n - j.e.cut : n;
+    if (row < j.e.N) store8<T>((second ? j.e.out2 : j.e.out) + (int64_t)row * j.e.ld, m, j.e.M, s);
   }
-  store8<T>(out + row * out_ld, m, M, s);
 }
 
 // ---- operand layouts -------------------------------------------------------------------
 
-// src [R][C] (rows src_ld apart) -> planes [R][ld], columns C .. ld zero; ld a multiple of 8
-template <typename T>
-__global__ __launch_bounds__(256) void k_ff_rows(const T *__restrict__ src, int64_t src_ld,
-                                                 int64_t R, int C, __bf16 *__restrict__ out,
-                                                 int64_t ld, int64_t plane) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = ld / 8;
-  if (i >= R * per) return;
-  const int64_t r = i / per;
-  const int c = 8 * (int)(i % per);
-  float v[8];
-  load8<T>(src + r * src_ld, c, C, v);
-  store8_planes<planes_of<T>()>(out + r * ld + c, plane, v);
-}
+// One operand to lay out from src [R][C] (rows src_ld apart): its rows, planes
+// [R][ld] with zeros from column C on, or its columns, planes [C][ld] with out[c][r]
+// = src[r][c] and zeros from r = R to the next multiple of 64. An fp32 source is
+// split into its planes; a bf16 source may have `planes` planes of its own.
+struct FfLay {
+  const void *src;
+  int64_t src_ld, src_plane, R, ld, plane;
+  __bf16 *out;
+  int C, planes, cols;  // cols: lay out columns
+  int start;            // first block
+};
+constexpr int kLays = 6;
+struct FfLays {
+  FfLay lay[kLays];
+  int count;
+};
 
-// src [R][C] -> planes [C][ld], out[c][r] = src[r][c] for r < R, zero for R <= r <
-// Rp (a multiple of 64). NP planes from an fp32 source; a bf16 source has NS
-// planes of its own (gridDim.z), each transposed. 64 x 64 tiles through LDS.
+// A block moves one 64 x 64 tile, columns through LDS (pitch 65: its reads and
+// writes touch 64 different banks). Bound by HBM.
 template <typename T>
-__global__ __launch_bounds__(256) void k_ff_trans(const T *__restrict__ src, int64_t src_ld,
-                                                  int64_t src_plane, int64_t R, int C,
-                                                  __bf16 *__restrict__ out, int64_t ld,
-                                                  int64_t plane) {
+__global__ __launch_bounds__(256) void k_ff_lay(FfLays ls) {
   __shared__ float tile[64][65];
   constexpr int NP = planes_of<T>();
-  src += blockIdx.z * src_plane;
-  out += blockIdx.z * plane;
-  const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 64;
-  const int tid = threadIdx.x;
+  int which = 0;
+#pragma unroll
+  for (int k = 1; k < kLays; ++k) which += k < ls.count && (int)blockIdx.x >= ls.lay[k].start;
+  const FfLay l = ls.lay[which];
+  int id = blockIdx.x - l.start;
+  // columns of tiles: of the source; a row operand also covers its padding
+  const int across = l.cols ? (l.C + 63) / 64 : (int)(l.ld / 64);
+  const int per = across * (int)((l.R + 63) / 64), p = id / per;
+  id %= per;
+  const int64_t r0 = (int64_t)(id / across) * 64;
+  const int c0 = (id % across) * 64, tid = threadIdx.x;
+  const T *src = (const T *)l.src + p * l.src_plane;
+  __bf16 *out = l.out + p * l.plane;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int r = (tid >> 3) + 32 * k, c = 8 * (tid & 7);
     float v[8] = {};
-    if (r0 + r < R && c0 + c < C) load8<T>(src + (r0 + r) * src_ld, c0 + c, C, v);
+    if (r0 + r < l.R && c0 + c < l.C) load8<T>(src + (r0 + r) * l.src_ld, c0 + c, l.C, v);
+    if (!l.cols) {
+      if (r0 + r < l.R) store8_planes<NP>(out + (r0 + r) * l.ld + c0 + c, l.plane, v);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile[r][c + e] = v[e];
+      for (int e = 0; e < 8; ++e) tile[r][c + e] = v[e];
+    }
   }
+  if (!l.cols) return;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int c = (tid >> 3) + 32 * k, r = 8 * (tid & 7);
-    if (c0 + c < C) {
+    if (c0 + c < l.C) {
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = tile[r + e][c];
-      store8_planes<NP>(out + (int64_t)(c0 + c) * ld + r0 + r, plane, v);
+      store8_planes<NP>(out + (int64_t)(c0 + c) * l.ld + r0 + r, l.plane, v);
     }
   }
 }
@@ -531,35 +599,87 @@ hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n
 
 // ---- launches ------------------------------------------------------------------------------
 
-using FfBig = Cfg<2, 4, 64, 16, 0, 8>;    // 256 x 256 tiles, 8 waves
-using FfMid = Cfg<1, 2, 64, 16, 0, 8>;    // 128 x 128 tiles, 2 waves
+constexpr int kCUs = 256;
+using FfBig = Cfg<2, 4, 64, 16, 0, 8>;  // 256 x 256 tiles, 8 waves, one block per CU
+using FfMid = Cfg<1, 2, 64, 16, 0, 8>;  // 128 x 128 tiles, 2 waves, two blocks per CU
 
-template <class C, int NP, bool DUAL, class Epi>
-hipError_t launch_tiles(FfProb g, const Epi &epi, hipStream_t st) {
-  constexpr int MT = DUAL ? C::BM / 2 : C::BM;
-  const int64_t nb = (int64_t)((g.M + MT - 1) / MT) * ((g.N + C::BN - 1) / C::BN) * g.splits;
-  hipLaunchKernelGGL((k_ff_gemm<C, NP, DUAL, Epi>), dim3((unsigned)nb), dim3(C::NTHR), 0, st, g, epi);
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t tiles_of(const FfProb &g, int edge, bool dual) {
+  return ceil_div(g.M, dual ? edge / 2 : edge) * ceil_div(g.N, edge);
+}
+
+template <class C, int NP, bool DUAL, class Epi, int G>
+hipError_t launch_tiles(FfGroup<Epi, G> grp, hipStream_t st) {
+  int at = 0;
+  for (int p = 0; p < G; ++p) {
+    grp.start[p] = at;
+    at += (int)round_up(tiles_of(grp.prob[p], C::BM, DUAL) * grp.prob[p].splits, 8);
+  }
+  grp.start[G] = at;
+  hipLaunchKernelGGL((k_ff_gemm<C, NP, DUAL, Epi, G>), dim3((unsigned)at), dim3(C::NTHR), 0, st,
+                     grp);
   return hipGetLastError();
 }
-int64_t big_tiles(int64_t M, int64_t N, bool dual) {
-  return ((M + (dual ? 127 : 255)) / (dual ? 128 : 256)) * ((N + 255) / 256);
-}
-// Large tiles once they fill three quarters of the CUs, small ones below.
-template <int NP, bool DUAL, class Epi>
-hipError_t launch_product(const FfProb &g, const Epi &epi, hipStream_t st) {
-  if (big_tiles(g.M, g.N, DUAL) >= 192) return launch_tiles<FfBig, NP, DUAL>(g, epi, st);
-  return launch_tiles<FfMid, NP, DUAL>(g, epi, st);
+
+// 256 x 256 tiles once they fill three quarters of the CUs, 128 x 128 ones below
+// (4B-shaped, 1024 tokens forward: 187 us so, 192 with small tiles up to the point
+// where a model of whole rounds favours large ones; with four stages of copies
+// in flight instead of two, hence one small block per CU, 267).
+template <class Epi, int G>
+bool use_big(const FfGroup<Epi, G> &grp, bool dual) {
+  int64_t tiles = 0;
+  for (int p = 0; p < G; ++p) tiles += tiles_of(grp.prob[p], 256, dual);
+  return tiles >= kCUs * 3 / 4;
 }
 
-// Parts of K of a product [M][N] with `steps` steps whose tiles do not fill the
-// GPU: enough for two blocks per CU, each with at least 8 steps.
-int split_parts(int64_t M, int64_t N, int64_t steps) {
-  if (big_tiles(M, N, false) >= 192) return 1;
-  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-  int64_t s = std::min<int64_t>({512 / std::max<int64_t>(tiles, 1), steps / 8, 16});
+// Parts of K for a product whose small tiles do not fill the GPU: two blocks per
+// CU in all, each with at least 8 steps (below that the copies' latency is most
+// of a block's time).
+int parts_of(const FfProb &g, int64_t steps) {
+  const int64_t tiles = tiles_of(g, 128, false);
+  const int64_t s = std::min<int64_t>({2 * kCUs / std::max<int64_t>(tiles, 1), steps / 8, 32});
   if (s < 2) return 1;
-  const int64_t per = (steps + s - 1) / s;
-  return (int)((steps + per - 1) / per);  // no empty part
+  return (int)ceil_div(steps, ceil_div(steps, s));  // no empty part
+}
+int64_t part_bytes(const FfProb &g, int parts) {
+  return parts > 1 ? 4 * (int64_t)parts * g.N * round_up(g.M, 8) : 0;
+}
+
+// Up to G independent products written out, each split over K by its `splits`
+// (its partial sums then in epi.part), and the joins.
+template <typename T, int G>
+hipError_t products_out(FfGroup<EpiOut<T>, G> grp, hipStream_t st) {
+  constexpr int NP = planes_of<T>();
+  bool split = false;
+  for (int p = 0; p < G; ++p) {
+    EpiOut<T> &e = grp.epi[p];
+    e.part_ld = round_up(grp.prob[p].M, 8);
+    e.part_stride = grp.prob[p].N * e.part_ld;
+    if (grp.prob[p].splits == 1) e.part = nullptr;
+    split = split || e.part;
+  }
+  if (!split && use_big(grp, false)) return launch_tiles<FfBig, NP, false>(grp, st);
+  hipError_t err = launch_tiles<FfMid, NP, false>(grp, st);
+  if (err != hipSuccess || !split) return err;
+  FfJoins<T, G> js{};
+  int used = 0;
+  int64_t most = 0;
+  for (int p = 0; p < G; ++p)
+    if (grp.prob[p].splits > 1) {
+      js.j[used++] = {grp.epi[p], grp.prob[p].splits, grp.prob[p].N};
+      most = std::max(most, grp.epi[p].part_stride / 8);
+    }
+  hipLaunchKernelGGL((k_ff_join<T, G>), dim3((unsigned)std::min<int64_t>(ceil_div(most, 256), 2048), used),
+                     dim3(256), 0, st, js);
+  return hipGetLastError();
+}
+
+// One product with an epilogue of its own.
+template <int NP, bool DUAL, class Epi>
+hipError_t product_with(const FfProb &g, const Epi &epi, hipStream_t st) {
+  const FfGroup<Epi, 1> grp{{g}, {epi}, {}};
+  if (use_big(grp, DUAL)) return launch_tiles<FfBig, NP, DUAL>(grp, st);
+  return launch_tiles<FfMid, NP, DUAL>(grp, st);
 }
 
 struct Area {
@@ -579,35 +699,34 @@ struct Opnd {
   int64_t ld, plane;
 };
 
-bool in_place(const void *p, int64_t cols, int64_t ld) {
-  return cols % kStep == 0 && ld % 8 == 0 && ((uintptr_t)p & 15) == 0;
-}
-
-// src's rows as an operand: in place, or laid out in buf.
+// Collects the operands to lay out and launches them together.
 template <typename T>
-hipError_t rows_operand(const T *src, int64_t src_ld, int64_t R, int C, __bf16 *buf, Opnd &o,
-                        hipStream_t st) {
-  if constexpr (sizeof(T) == 2) {
-    if (in_place(src, C, src_ld)) {
-      o = Opnd{(const __bf16 *)src, src_ld, 0};
-      return hipSuccess;
-    }
+struct Layouts {
+  FfLays ls{};
+  int64_t blocks = 0;
+  void add(const void *src, int64_t src_ld, int64_t src_plane, int planes, int64_t R, int C,
+           __bf16 *out, int64_t ld, int64_t plane, bool cols) {
+    FfLay &l = ls.lay[ls.count++];
+    l = FfLay{src, src_ld, src_plane, R, ld, plane, out, C, planes, cols, (int)blocks};
+    blocks += planes * ceil_div(R, 64) * (cols ? ceil_div(C, 64) : ld / 64);
   }
-  const int64_t ld = kpad(C), plane = R * ld;
-  o = Opnd{buf, ld, plane};
-  hipLaunchKernelGGL(k_ff_rows<T>, dim3((unsigned)((R * (ld / 8) + 255) / 256)), dim3(256), 0, st, src,
-                     src_ld, R, C, buf, ld, plane);
-  return hipGetLastError();
-}
-
-// src's columns as an operand: out[c][r], rows ld apart, zero past R to a whole step.
-template <typename T>
-hipError_t trans_operand(const T *src, int64_t src_ld, int64_t src_plane, int planes, int64_t R, int C,
-                         __bf16 *out, int64_t ld, int64_t plane, hipStream_t st) {
-  hipLaunchKernelGGL(k_ff_trans<T>, dim3((unsigned)(kpad(R) / 64), (C + 63) / 64, planes), dim3(256),
-                     0, st, src, src_ld, src_plane, R, C, out, ld, plane);
-  return hipGetLastError();
-}
+  // the rows of src: used in place if they are an operand already
+  Opnd rows(const T *src, int64_t src_ld, int64_t R, int C, __bf16 *buf) {
+    if (sizeof(T) == 2 && C % kStep == 0 && src_ld % 8 == 0 && ((uintptr_t)src & 15) == 0)
+      return {(const __bf16 *)src, src_ld, 0};
+    const int64_t ld = kpad(C);
+    add(src, src_ld, 0, 1, R, C, buf, ld, R * ld, false);
+    return {buf, ld, R * ld};
+  }
+  void cols(const T *src, int64_t src_ld, int64_t R, int C, __bf16 *out, int64_t ld, int64_t plane) {
+    add(src, src_ld, 0, 1, R, C, out, ld, plane, true);
+  }
+  hipError_t launch(hipStream_t st) const {
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_ff_lay<T>, dim3((unsigned)blocks), dim3(256), 0, st, ls);
+    return hipGetLastError();
+  }
+};
 
 #define TRYH(expr)                       \
   do {                                   \
@@ -615,12 +734,12 @@ hipError_t trans_operand(const T *src, int64_t src_ld, int64_t src_plane, int pl
     if (_e != hipSuccess) return _e;     \
   } while (0)
 
-struct FwdWs {
+struct FwdPlan {
   __bf16 *x, *wg, *wu, *wd, *z;
   float *part;
-  int parts;
+  FfProb down;  // sizes and parts; operands are set by the call
   size_t bytes;
-  FwdWs(void *base, int np, int d, int F, int64_t n) {
+  FwdPlan(void *base, int np, int d, int F, int64_t n) {
     Area w{(char *)base};
     const int64_t dp = kpad(d), Fp = kpad(F);
     const bool copy_d = np > 1 || d != dp, copy_f = np > 1 || F != Fp;
@@ -629,18 +748,22 @@ struct FwdWs {
     wu = w.planes(np, copy_d ? F : 0, dp);
     wd = w.planes(np, copy_f ? d : 0, Fp);
     z = w.planes(np, n, Fp);
-    parts = split_parts(d, n, (np == 1 ? 1 : 6) * (Fp / kStep));
-    part = (float *)w.take(parts > 1 ? 4 * parts * n * round_up(d, 8) : 0);
+    down = FfProb{};
+    down.M = d;
+    down.N = (int)n;
+    down.nk = (int)(Fp / kStep);
+    down.splits = parts_of(down, (np == 1 ? 1 : 6) * down.nk);
+    part = (float *)w.take(part_bytes(down, down.splits));
     bytes = w.off;
   }
 };
 
-struct BwdWs {
+struct BwdPlan {
   __bf16 *dy, *wdt, *dau, *z, *wgut, *xt, *dyt, *daut, *zt;
-  float *part;
-  int parts;
+  FfProb out[3];  // dx, [dW_g dW_u], dW_d: sizes and parts
+  float *part[3];
   size_t bytes;
-  BwdWs(void *base, int np, int d, int F, int64_t n) {
+  BwdPlan(void *base, int np, int d, int F, int64_t n) {
     Area w{(char *)base};
     const int64_t dp = kpad(d), Fp = kpad(F), Tp = kpad(n);
     dy = w.planes(np, n, dp);
@@ -652,26 +775,27 @@ struct BwdWs {
     dyt = w.planes(np, d, Tp);
     daut = w.planes(np, 2 * Fp, Tp);
     zt = w.planes(np, Fp, Tp);
-    parts = split_parts(d, n, (np == 1 ? 1 : 6) * (2 * Fp / kStep));
-    part = (float *)w.take(parts > 1 ? 4 * parts * n * round_up(d, 8) : 0);
+    const int64_t M[3] = {d, d, F}, N[3] = {n, 2 * Fp, d}, K[3] = {2 * Fp, Tp, Tp};
+    for (int p = 0; p < 3; ++p) {
+      out[p] = FfProb{};
+      out[p].M = (int)M[p];
+      out[p].N = (int)N[p];
+      out[p].nk = (int)(K[p] / kStep);
+      out[p].splits = parts_of(out[p], (np == 1 ? 1 : 6) * out[p].nk);
+      part[p] = (float *)w.take(part_bytes(out[p], out[p].splits));
+    }
     bytes = w.off;
   }
 };
 
-// out[n][m] = A rows times B rows with K split when the tiles are few.
-template <typename T>
-hipError_t product_out(FfProb g, int parts, float *part, T *out, int64_t out_ld, hipStream_t st) {
-  constexpr int NP = planes_of<T>();
-  if (parts == 1) {
-    g.splits = 1;
-    return launch_product<NP, false>(g, EpiOut<T>{out, nullptr, out_ld, g.M, g.N, 1 << 30}, st);
-  }
-  g.splits = parts;
-  const int64_t ld = round_up(g.M, 8), stride = (int64_t)g.N * ld;
-  TRYH((launch_product<NP, false>(g, EpiPart{part, stride, ld}, st)));
-  hipLaunchKernelGGL(k_ff_join<T>, dim3((unsigned)((stride / 8 + 255) / 256)), dim3(256), 0, st, part,
-                     parts, stride, ld, (int64_t)g.N, g.M, out, out_ld);
-  return hipGetLastError();
+FfProb with_operands(FfProb g, const Opnd &a, const Opnd &b) {
+  g.a = a.p;
+  g.lda = a.ld;
+  g.pa = a.plane;
+  g.b = b.p;
+  g.ldb = b.ld;
+  g.pb = b.plane;
+  return g;
 }
 
 }  // namespace
@@ -681,10 +805,10 @@ using namespace mfma;
 
 size_t ff_forward_workspace(int elem, int d, int F, int64_t n) {
   if (n <= kSmallTokens) return (size_t)round_up(std::max<int64_t>(n, 1) * F * elem, 256);
-  return FwdWs(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes;
+  return FwdPlan(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes;
 }
 size_t ff_backward_workspace(int elem, int d, int F, int64_t n) {
-  return std::max<size_t>(256, BwdWs(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes);
+  return std::max<size_t>(256, BwdPlan(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes);
 }
 
 template <typename T>
@@ -699,18 +823,20 @@ hipError_t ff_forward(const FfArgs &p, hipStream_t st) {
                                       nullptr, st);
   }
   constexpr int NP = planes_of<T>();
-  const FwdWs w(p.ws, NP, d, F, n);
+  const FwdPlan w(p.ws, NP, d, F, n);
   const int64_t Fp = kpad(F);
-  Opnd x, g, u, o;
-  TRYH(rows_operand((const T *)p.x, p.x_stride, n, d, w.x, x, st));
-  TRYH(rows_operand(wg, (int64_t)d, F, d, w.wg, g, st));
-  TRYH(rows_operand(wu, (int64_t)d, F, d, w.wu, u, st));
-  TRYH(rows_operand(wd, (int64_t)F, d, F, w.wd, o, st));
-  FfProb q{g.p, u.p, x.p, g.ld, x.ld, g.plane, x.plane, F, n, (int)(kpad(d) / kStep), 1};
-  TRYH((launch_product<NP, true>(
-      q, EpiZ<T>{w.z, n * Fp, F, (int)Fp, (T *)p.a, (T *)p.u}, st)));
-  FfProb r{o.p, nullptr, w.z, o.ld, Fp, o.plane, n * Fp, d, n, (int)(Fp / kStep), 1};
-  return product_out<T>(r, w.parts, w.part, (T *)p.y, p.y_stride, st);
+  Layouts<T> lay;
+  const Opnd x = lay.rows((const T *)p.x, p.x_stride, n, d, w.x);
+  const Opnd g = lay.rows(wg, d, F, d, w.wg);
+  const Opnd u = lay.rows(wu, d, F, d, w.wu);
+  const Opnd o = lay.rows(wd, F, d, F, w.wd);
+  TRYH(lay.launch(st));
+  const FfProb q{g.p, u.p, x.p, g.ld, x.ld, g.plane, x.plane, F, n, (int)(kpad(d) / kStep), 1};
+  TRYH((product_with<NP, true>(q, EpiZ<T>{w.z, n * Fp, F, (int)Fp, (T *)p.a, (T *)p.u}, st)));
+  const FfGroup<EpiOut<T>, 1> y{{with_operands(w.down, o, {w.z, Fp, n * Fp})},
+                                {EpiOut<T>{(T *)p.y, nullptr, p.y_stride, d, n, 1 << 30, w.part, 0, 0}},
+                                {}};
+  return products_out<T, 1>(y, st);
 }
 
 template <typename T>
@@ -724,35 +850,37 @@ hipError_t ff_backward(const FfArgs &p, hipStream_t st) {
     return hipGetLastError();
   }
   constexpr int NP = planes_of<T>();
-  const BwdWs w(p.ws, NP, d, F, n);
+  const BwdPlan w(p.ws, NP, d, F, n);
   const int64_t dp = kpad(d), Fp = kpad(F), Tp = kpad(n);
-  Opnd dy;
-  TRYH(rows_operand((const T *)p.dy, p.dy_stride, n, d, w.dy, dy, st));
   // W_d^T [F][dp]; W_g^T and W_u^T side by side [d][2 Fp]; x^T and dy^T [d][Tp]
-  TRYH(trans_operand((const T *)p.w_down, (int64_t)F, 0, 1, d, F, w.wdt, dp, F * dp, st));
-  TRYH(trans_operand((const T *)p.w_gate, (int64_t)d, 0, 1, F, d, w.wgut, 2 * Fp, d * 2 * Fp, st));
-  TRYH(trans_operand((const T *)p.w_up, (int64_t)d, 0, 1, F, d, w.wgut + Fp, 2 * Fp, d * 2 * Fp, st));
-  TRYH(trans_operand((const T *)p.x, p.x_stride, 0, 1, n, d, w.xt, Tp, d * Tp, st));
-  TRYH(trans_operand((const T *)p.dy, p.dy_stride, 0, 1, n, d, w.dyt, Tp, d * Tp, st));
+  Layouts<T> lay;
+  const Opnd dy = lay.rows((const T *)p.dy, p.dy_stride, n, d, w.dy);
+  lay.cols((const T *)p.w_down, F, d, F, w.wdt, dp, F * dp);
+  lay.cols((const T *)p.w_gate, d, F, d, w.wgut, 2 * Fp, d * 2 * Fp);
+  lay.cols((const T *)p.w_up, d, F, d, w.wgut + Fp, 2 * Fp, d * 2 * Fp);
+  lay.cols((const T *)p.x, p.x_stride, n, d, w.xt, Tp, d * Tp);
+  lay.cols((const T *)p.dy, p.dy_stride, n, d, w.dyt, Tp, d * Tp);
+  TRYH(lay.launch(st));
   // dz, and from it dA, dU and z
-  FfProb q{w.wdt, nullptr, dy.p, dp, dy.ld, F * dp, dy.plane, F, n, (int)(dp / kStep), 1};
-  TRYH((launch_product<NP, false>(q,
-                                  EpiDz<T>{(const T *)p.a, (const T *)p.u, w.dau, w.z, n * 2 * Fp,
-                                           n * Fp, F, (int)Fp},
-                                  st)));
-  TRYH(trans_operand(w.dau, 2 * Fp, n * 2 * Fp, NP, n, (int)(2 * Fp), w.daut, Tp, 2 * Fp * Tp, st));
-  TRYH(trans_operand(w.z, Fp, n * Fp, NP, n, (int)Fp, w.zt, Tp, Fp * Tp, st));
-  // dx = [dA dU] [W_g; W_u]
-  FfProb r{w.wgut, nullptr, w.dau, 2 * Fp, 2 * Fp, d * 2 * Fp, n * 2 * Fp, d, n,
-           (int)(2 * Fp / kStep), 1};
-  TRYH(product_out<T>(r, w.parts, w.part, (T *)p.dx, p.dx_stride, st));
-  // dW_g, dW_u (rows f < F of [dA dU]^T and from Fp on) and dW_d
-  FfProb s{w.xt, nullptr, w.daut, Tp, Tp, d * Tp, 2 * Fp * Tp, d, (int)(2 * Fp), (int)(Tp / kStep), 1};
-  TRYH((launch_product<NP, false>(
-      s, EpiOut<T>{(T *)p.dw_gate, (T *)p.dw_up, (int64_t)d, d, F, (int)Fp}, st)));
-  FfProb t{w.zt, nullptr, w.dyt, Tp, Tp, Fp * Tp, d * Tp, F, d, (int)(Tp / kStep), 1};
-  return launch_product<NP, false>(
-      t, EpiOut<T>{(T *)p.dw_down, nullptr, (int64_t)F, F, d, 1 << 30}, st);
+  const FfProb q{w.wdt, nullptr, dy.p, dp, dy.ld, F * dp, dy.plane, F, n, (int)(dp / kStep), 1};
+  TRYH((product_with<NP, false>(q,
+                                EpiDz<T>{(const T *)p.a, (const T *)p.u, w.dau, w.z, n * 2 * Fp,
+                                         n * Fp, F, (int)Fp},
+                                st)));
+  Layouts<__bf16> turn;
+  turn.add(w.dau, 2 * Fp, n * 2 * Fp, NP, n, (int)(2 * Fp), w.daut, Tp, 2 * Fp * Tp, true);
+  turn.add(w.z, Fp, n * Fp, NP, n, (int)Fp, w.zt, Tp, Fp * Tp, true);
+  TRYH(turn.launch(st));
+  // dx = [dA dU] [W_g; W_u]; dW_g, dW_u (rows f < F of [dA dU]^T and from Fp on); dW_d
+  const Opnd xt{w.xt, Tp, d * Tp}, dyt{w.dyt, Tp, d * Tp}, daut{w.daut, Tp, 2 * Fp * Tp};
+  const FfGroup<EpiOut<T>, 3> out{
+      {with_operands(w.out[0], {w.wgut, 2 * Fp, d * 2 * Fp}, {w.dau, 2 * Fp, n * 2 * Fp}),
+       with_operands(w.out[1], xt, daut), with_operands(w.out[2], {w.zt, Tp, Fp * Tp}, dyt)},
+      {EpiOut<T>{(T *)p.dx, nullptr, p.dx_stride, d, n, 1 << 30, w.part[0], 0, 0},
+       EpiOut<T>{(T *)p.dw_gate, (T *)p.dw_up, (int64_t)d, d, F, (int)Fp, w.part[1], 0, 0},
+       EpiOut<T>{(T *)p.dw_down, nullptr, (int64_t)F, F, d, 1 << 30, w.part[2], 0, 0}},
+      {}};
+  return products_out<T, 3>(out, st);
 }
 
 template hipError_t ff_forward<float>(const FfArgs &, hipStream_t);

@@ -440,12 +440,18 @@ __global__ __launch_bounds__(256) void k_ff_zero(uint16_t *__restrict__ p, int64
 
 // ---- few tokens -------------------------------------------------------------------------
 // Up to 64 tokens every weight is read once and little else moves, so the weights
-// go straight from memory into MFMA operands: a block owns 16 weight rows (of both
-// W_g and W_u in the first product), its WV waves take interleaved pieces of K,
-// and their sums meet in LDS. A lane's 16 bytes of row l % 16 are one operand
-// register set: 8 bf16 values of one 16x16x32 MFMA, or 4 fp32 values of four
-// 16x16x4 ones (any assignment of K values to lanes gives the same sum as long
-// as both operands share it). NT: groups of 16 tokens.
+// go straight from memory into MFMA operands: 16 bytes of a weight row per lane
+// are 8 bf16 values of one 16x16x32 MFMA, or 4 fp32 values of four 16x16x4 ones
+// (any assignment of K values to lanes gives the same sum as long as both operands
+// share it). The MFMA's 16 operand rows would be 16 weight rows, whose 16-byte
+// pieces lie a row apart: 64 cache lines a load, and the loads' address work, not
+// memory, sets the time (n = 16: 46 us, 64: 95). So an operand row is a weight row
+// i and one of KF neighbouring pieces of K, s: rows i KF + s, and columns j KF + s
+// of the other operand for token j. Lanes next to each other then read pieces
+// next to each other; of the products, those whose two s agree are summed.
+// A block owns RG groups of 16 / KF weight rows (of both W_g and W_u in the first
+// product), so that the tokens' operands serve several weight rows; its WV waves
+// take interleaved steps of K and meet in LDS. NT: groups of 16 / KF tokens.
 
 template <typename T>
 struct Quad;  // 16 bytes of one operand row
@@ -475,124 +481,183 @@ __device__ __forceinline__ Quad<T> quad_at(const T *p) {
   const Pack<T, Quad<T>::E> k = *(const Pack<T, Quad<T>::E> *)p;
   return __builtin_bit_cast(Quad<T>, k);
 }
-// the same with zeros at and past the row's end
+// the same with zeros at and past `end`
 template <typename T>
-__device__ __forceinline__ Quad<T> quad_end(const T *row, int k, int K) {
-  if (k + Quad<T>::E <= K) return quad_at<T>(row + k);
+__device__ __forceinline__ Quad<T> quad_end(const T *row, int k, int end) {
+  if (k + Quad<T>::E <= end) return quad_at<T>(row + k);
   Quad<T> q;
 #pragma unroll
-  for (int e = 0; e < Quad<T>::E; ++e) q.set(e, k + e < K ? (float)row[k + e] : 0.f);
+  for (int e = 0; e < Quad<T>::E; ++e) q.set(e, k + e < end ? (float)row[k + e] : 0.f);
   return q;
-}
-
-// acc[t] (and acc2[t]) += the block's 16 weight rows times token group t over this
-// wave's pieces of K. U MFMA steps per piece.
-template <typename T, int NT, int WV, bool DUAL>
-__device__ __forceinline__ void small_dot(const T *wrow, const T *w2row, const T *const (&xrow)[NT],
-                                          int K, int wave, int lane, f32x4 (&acc)[NT],
-                                          f32x4 (&acc2)[NT]) {
-  constexpr int U = DUAL ? 4 : 8;
-  constexpr int S = 4 * Quad<T>::E;  // K values of one step (64 bytes of a row)
-  constexpr int P = U * S;
-  const int kl = Quad<T>::E * (lane >> 4);
-  int k0 = wave * P;
-  for (; k0 + P <= K; k0 += WV * P) {
-    Quad<T> w[U], w2[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      w[u] = quad_at<T>(wrow + k0 + S * u + kl);
-      if constexpr (DUAL) w2[u] = quad_at<T>(w2row + k0 + S * u + kl);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const Quad<T> x = quad_at<T>(xrow[t] + k0 + S * u + kl);
-        acc[t] = Quad<T>::mma(w[u], x, acc[t]);
-        if constexpr (DUAL) acc2[t] = Quad<T>::mma(w2[u], x, acc2[t]);
-      }
-  }
-  if (k0 < K)  // the row's last, partial piece (one wave)
-    for (int k = k0; k < K; k += S) {
-      const Quad<T> w = quad_end<T>(wrow, k + kl, K);
-      Quad<T> w2{};
-      if constexpr (DUAL) w2 = quad_end<T>(w2row, k + kl, K);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const Quad<T> x = quad_end<T>(xrow[t], k + kl, K);
-        acc[t] = Quad<T>::mma(w, x, acc[t]);
-        if constexpr (DUAL) acc2[t] = Quad<T>::mma(w2, x, acc2[t]);
-      }
-    }
 }
 
 // DUAL: out = SiLU(W x) (W2 x), with W x and W2 x saved to a, u when given.
 // Otherwise out = W x. W [M][K] dense, x rows x_ld apart, out rows out_ld apart.
-template <typename T, int NT, int WV, bool DUAL>
+template <typename T, int NT, int RG, int WV, int KF, bool DUAL>
 __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
                                                       const T *__restrict__ w2,
                                                       const T *__restrict__ x, int64_t x_ld, int n,
                                                       int M, int K, T *__restrict__ out,
                                                       int64_t out_ld, T *__restrict__ a,
                                                       T *__restrict__ u) {
-  __shared__ f32x4 sum[WV][DUAL ? 2 : 1][NT][64];
+  constexpr int RB = 16 / KF;  // weight rows, tokens of a group
+  constexpr int D = DUAL ? 2 : 1;
+  constexpr int E = Quad<T>::E, S = 4 * KF * E;  // K values of a lane, of a step
+  // steps whose loads go together: about 8 KB of weights a wave, fewer where the
+  // tokens' operands fill the registers
+  constexpr int U = NT >= 8 || RG * D >= 8 ? 1 : RG * D >= 4 ? 2 : 4;
+  constexpr int P = U * S;
+  __shared__ float sum[WV][D][RG * NT][RB * RB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int m0 = 16 * blockIdx.x;
-  const int64_t row = (int64_t)min(m0 + (lane & 15), M - 1) * K;
-  const T *xrow[NT];
+  const int m0 = RG * RB * blockIdx.x;
+  const int r = lane & 15, kl = E * (r % KF + KF * (lane >> 4));
+  const T *wrow[D][RG], *xrow[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) xrow[t] = x + (int64_t)min(16 * t + (lane & 15), n - 1) * x_ld;
-  f32x4 acc[NT] = {}, acc2[NT] = {};
-  small_dot<T, NT, WV, DUAL>(w + row, DUAL ? w2 + row : nullptr, xrow, K, wave, lane, acc, acc2);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    sum[wave][0][t][lane] = acc[t];
-    if constexpr (DUAL) sum[wave][1][t][lane] = acc2[t];
+  for (int g = 0; g < RG; ++g) {
+    const int64_t at = (int64_t)min(m0 + RB * g + r / KF, M - 1) * K;
+    wrow[0][g] = w + at;
+    if constexpr (DUAL) wrow[1][g] = w2 + at;
   }
-  __syncthreads();
-  // lane holds rows 4 (l / 16) .. + 3 at token l % 16
-  for (int t = wave; t < NT; t += WV) {
-    const int tok = 16 * t + (lane & 15), m = m0 + 4 * (lane >> 4);
-    f32x4 s{}, s2{};
 #pragma unroll
-    for (int q = 0; q < WV; ++q) {
-      s += sum[q][0][t][lane];
-      if constexpr (DUAL) s2 += sum[q][1][t][lane];
+  for (int t = 0; t < NT; ++t) xrow[t] = x + (int64_t)min(RB * t + r / KF, n - 1) * x_ld;
+  f32x4 acc[D][RG][NT] = {};
+  Quad<T> cur[U][D][RG], next[U][D][RG];
+  const auto load = [&](Quad<T> (&q)[U][D][RG], int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+#pragma unroll
+      for (int i = 0; i < D; ++i)
+#pragma unroll
+        for (int g = 0; g < RG; ++g) q[s][i][g] = quad_at<T>(wrow[i][g] + kl + k0 + S * s);
+  };
+  int k0 = wave * P;
+  if (k0 + P <= K) load(cur, k0);
+  for (; k0 + P <= K; k0 += WV * P) {
+    // this piece's tokens, then the next piece's weights: loads return in order,
+    // so the MFMAs wait for the tokens (from L2) and not for memory
+    Quad<T> xv[U][NT];
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) xv[s][t] = quad_at<T>(xrow[t] + kl + k0 + S * s);
+    const bool more = k0 + WV * P + P <= K;
+    if (more) load(next, k0 + WV * P);
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+#pragma unroll
+          for (int g = 0; g < RG; ++g)
+            acc[i][g][t] = Quad<T>::mma(cur[s][i][g], xv[s][t], acc[i][g][t]);
+    if (more) {
+#pragma unroll
+      for (int s = 0; s < U; ++s)
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+#pragma unroll
+          for (int g = 0; g < RG; ++g) cur[s][i][g] = next[s][i][g];
     }
-    if (tok < n) {
+  }
+  // the rows' last, partial piece, by the wave whose turn it is
+  const int whole = K / P * P;
+  if (wave == whole / P % WV)
+    for (int k = whole; k < K; k += S) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (m + r < M) {
-          if constexpr (DUAL) {
-            if (a) {
-              a[(int64_t)tok * M + m + r] = (T)s[r];
-              u[(int64_t)tok * M + m + r] = (T)s2[r];
-            }
-            out[tok * out_ld + m + r] = (T)(s[r] * fast_sigmoid(s[r]) * s2[r]);
-          } else {
-            out[tok * out_ld + m + r] = (T)s[r];
+      for (int t = 0; t < NT; ++t) {
+        const Quad<T> xe = quad_end<T>(xrow[t], kl + k, K);
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+#pragma unroll
+          for (int g = 0; g < RG; ++g)
+            acc[i][g][t] = Quad<T>::mma(quad_end<T>(wrow[i][g], kl + k, K), xe, acc[i][g][t]);
+      }
+    }
+  // Lane l holds operand rows 4 (l / 16) + q, q = 0 .. 3, of column l % 16: its
+  // column's piece s = l % KF matches q = s, s + KF, ..: weight rows
+  // (4 / KF) (l / 16) + q / KF. The KF lanes of a token then add up.
+  const int s = r % KF, tok = r / KF;
+#pragma unroll
+  for (int i = 0; i < D; ++i)
+#pragma unroll
+    for (int g = 0; g < RG; ++g)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 4 / KF; ++h) {
+          float v = 0.f;
+#pragma unroll
+          for (int q = 0; q < KF; ++q) {
+            const float p = acc[i][g][t][h * KF + q];
+            v = q == s ? p : v;
           }
+#pragma unroll
+          for (int q = 1; q < KF; q *= 2) v += __shfl_xor(v, q, 64);
+          if (s == 0) sum[wave][i][g * NT + t][((4 / KF) * (lane >> 4) + h) * RB + tok] = v;
         }
+  __syncthreads();
+  for (int o = tid; o < RG * NT * RB * RB; o += 64 * WV) {
+    // neighbouring threads take neighbouring weight rows of one token
+    const int row = o % (RG * RB), col = o / (RG * RB), g = row / RB, t = col / RB;
+    const int m = m0 + row;
+    float v[D] = {};
+#pragma unroll
+    for (int q = 0; q < WV; ++q)
+#pragma unroll
+      for (int i = 0; i < D; ++i) v[i] += sum[q][i][g * NT + t][row % RB * RB + col % RB];
+    if (m < M && col < n) {
+      if constexpr (DUAL) {
+        if (a) {
+          a[(int64_t)col * M + m] = (T)v[0];
+          u[(int64_t)col * M + m] = (T)v[1];
+        }
+        out[col * out_ld + m] = (T)(v[0] * fast_sigmoid(v[0]) * v[1]);
+      } else {
+        out[col * out_ld + m] = (T)v[0];
+      }
     }
   }
 }
 
-constexpr int kSmallTokens = 64;
+// Whether a call streams its weights (k_ff_small) or runs on tiles: up to 16
+// tokens always, up to 64 in fp32, whose tiles do six times the work (1024 x 2048:
+// 32 and 115 us at 64 tokens), or where the weights are few (bf16, 32 and 64
+// tokens: 1024 x 1024 13 us against 30 on tiles, 1999 x 3001 32 and 62 against 66,
+// 2560 x 9728 77 and 98 against 70).
+bool few_tokens(int elem, int d, int F, int64_t n) {
+  return n <= 16 || (n <= 64 && (elem == 4 || (int64_t)d * F <= 6 << 20));
+}
 
-template <typename T, int WV, bool DUAL>
-hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n, int M, int K,
-                        T *out, int64_t out_ld, T *a, T *u, hipStream_t st) {
-  const dim3 grid((M + 15) / 16), block(64 * WV);
-#define SMALL(NT) \
-  hipLaunchKernelGGL((k_ff_small<T, NT, WV, DUAL>), grid, block, 0, st, w, w2, x, x_ld, n, M, K, \
-                     out, out_ld, a, u)
-  if (n <= 16)
-    SMALL(1);
-  else if (n <= 32)
-    SMALL(2);
-  else
-    SMALL(4);
+// Row groups of a block of four waves: two where that makes two blocks a CU, else
+// one (2560 x 9728, one token: 29 us with 2 groups in the first product and 1 in
+// the second, 31 with 4 and 1, 32 with 4 and 2; with eight waves 34).
+template <typename T, bool DUAL>
+hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n, int M, int K, T *out,
+                        int64_t out_ld, T *a, T *u, hipStream_t st) {
+  constexpr int WV = 4;
+#define SMALL(NT, RG, KF)                                                                       \
+  hipLaunchKernelGGL((k_ff_small<T, NT, RG, WV, KF, DUAL>),                                     \
+                     dim3((M + RG * (16 / KF) - 1) / (RG * (16 / KF))), dim3(64 * WV), 0, st, w, w2, \
+                     x, x_ld, n, M, K, out, out_ld, a, u)
+#define SMALL_TOKENS(RG) \
+  if (n <= 4)            \
+    SMALL(1, RG, 4);     \
+  else if (n <= 8)       \
+    SMALL(2, RG, 4);     \
+  else if (n <= 16)      \
+    SMALL(4, RG, 4);     \
+  else if (n <= 32)      \
+    SMALL(8, RG, 4);     \
+  else                   \
+    SMALL(8, RG, 2)
+  if (M >= 16 * 2 * 256) {
+    SMALL_TOKENS(2);
+  } else {
+    SMALL_TOKENS(1);
+  }
+#undef SMALL_TOKENS
 #undef SMALL
   return hipGetLastError();
 }
@@ -804,7 +869,7 @@ FfProb with_operands(FfProb g, const Opnd &a, const Opnd &b) {
 using namespace mfma;
 
 size_t ff_forward_workspace(int elem, int d, int F, int64_t n) {
-  if (n <= kSmallTokens) return (size_t)round_up(std::max<int64_t>(n, 1) * F * elem, 256);
+  if (few_tokens(elem, d, F, n)) return (size_t)round_up(std::max<int64_t>(n, 1) * F * elem, 256);
   return FwdPlan(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes;
 }
 size_t ff_backward_workspace(int elem, int d, int F, int64_t n) {
@@ -815,12 +880,12 @@ template <typename T>
 hipError_t ff_forward(const FfArgs &p, hipStream_t st) {
   const int d = p.d, F = p.F, n = (int)p.n;
   const T *wg = (const T *)p.w_gate, *wu = (const T *)p.w_up, *wd = (const T *)p.w_down;
-  if (n <= kSmallTokens) {
+  if (few_tokens((int)sizeof(T), d, F, n)) {
     T *z = (T *)p.ws;
-    TRYH((launch_small<T, 4, true>(wg, wu, (const T *)p.x, p.x_stride, n, F, d, z, F, (T *)p.a,
-                                   (T *)p.u, st)));
-    return launch_small<T, 16, false>(wd, nullptr, z, F, n, d, F, (T *)p.y, p.y_stride, nullptr,
-                                      nullptr, st);
+    TRYH((launch_small<T, true>(wg, wu, (const T *)p.x, p.x_stride, n, F, d, z, F, (T *)p.a,
+                                (T *)p.u, st)));
+    return launch_small<T, false>(wd, nullptr, z, F, n, d, F, (T *)p.y, p.y_stride, nullptr, nullptr,
+                                  st);
   }
   constexpr int NP = planes_of<T>();
   const FwdPlan w(p.ws, NP, d, F, n);

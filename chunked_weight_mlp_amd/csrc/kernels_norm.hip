@@ -13,6 +13,7 @@ namespace ipttt {
 namespace {
 
 using blk::load_pack;
+using blk::Pack;
 using blk::store_pack;
 using blk::wave_sum;
 
@@ -29,6 +30,26 @@ __device__ __forceinline__ float row_sum(float v, float *slot) {
     for (int w = 0; w < WPR; ++w) v += slot[w];
   }
   return v;
+}
+
+// Two sums at once, one barrier.
+template <int WPR>
+__device__ __forceinline__ void row_sum2(float &a, float &b, float (*slot)[2]) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) {
+      slot[threadIdx.x >> 6][0] = a;
+      slot[threadIdx.x >> 6][1] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      a += slot[w][0];
+      b += slot[w][1];
+    }
+  }
 }
 
 // 8 elements from column c of a row of d; zero at and past d. W: d is a
@@ -127,73 +148,105 @@ __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
   }
 }
 
+// 8 columns as they are stored, from column c of a row of d; zero at and past d.
+template <typename T, bool W>
+__device__ __forceinline__ Pack<T, 8> raw_cols(const T *row, int c, int d) {
+  if constexpr (W) {
+    Pack<T, 8> p = *(const Pack<T, 8> *)(row + (c < d ? c : 0));
+    if (c >= d) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p.v[e] = (T)0.f;
+    }
+    return p;
+  } else {
+    if (c + 8 <= d) return *(const Pack<T, 8> *)(row + c);
+    Pack<T, 8> p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p.v[e] = c + e < d ? row[c + e] : (T)0.f;
+    return p;
+  }
+}
+
+// One row of the backward as it is stored.
+template <typename T, int NP>
+struct BwdRow {
+  Pack<T, 8> h[NP], dy[NP], dh[NP];
+  float mean, rstd;
+};
+template <typename T, int TPR, int NP, bool W>
+__device__ __forceinline__ void load_row(const NormArgs &a, int64_t row, int tr, BwdRow<T, NP> &r) {
+  const T *h = (const T *)a.x + row * a.x_stride, *dy = (const T *)a.dy + row * a.dy_stride;
+  const T *dh = (const T *)a.r + row * a.r_stride;
+  r.mean = a.mean[row];
+  r.rstd = a.rstd[row];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    r.h[p] = raw_cols<T, W>(h, 8 * (TPR * p + tr), a.d);
+    r.dy[p] = raw_cols<T, W>(dy, 8 * (TPR * p + tr), a.d);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) r.dh[p] = raw_cols<T, W>(dh, 8 * (TPR * p + tr), a.d);
+  }
+}
+
 // A block walks rows blockIdx, blockIdx + gridDim, ... (RB at a time) and keeps
 // its columns' sums of dy xh and dy in registers; its waves' sums meet in LDS
 // once at the end and go to part[block], which k_norm_sums adds in a fixed order.
+// All of a row's loads are issued together, dh's too, which is used last: 131072
+// x 2048 bf16 in 412 us, 5.2 TB/s (686 us with dh loaded where it is used).
 template <typename T, int WPR, int NP, bool W>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void k_norm_bwd(NormArgs a) {
   constexpr int RB = WPR > 4 ? 1 : 4 / WPR;
   constexpr int TPR = 64 * WPR;
-  __shared__ float red[2][2][WPR];
-  __shared__ float comb[RB > 1 ? (RB - 1) * 64 * 8 : 1];
-  const int tr = threadIdx.x % TPR, rb = threadIdx.x / TPR;
+  __shared__ float red[2][WPR][2];
+  __shared__ float comb[RB > 1 ? (RB - 1) * TPR * 8 : 1];
+  const int tr = threadIdx.x % TPR;
+  const int rb = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   const int d = a.d;
   float dg[NP][8], db[NP][8];
+  Pack<T, 8> gamma[NP];
 #pragma unroll
-  for (int p = 0; p < NP; ++p)
+  for (int p = 0; p < NP; ++p) {
+    if (a.gamma) gamma[p] = raw_cols<T, W>((const T *)a.gamma, 8 * (TPR * p + tr), d);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg[p][e] = db[p][e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      dg[p][e] = db[p][e] = 0.f;
+      if (!a.gamma) gamma[p].v[e] = (T)1.f;
+    }
+  }
   int par = 0;
   for (int64_t row = (int64_t)blockIdx.x * RB + rb; row < a.n; row += (int64_t)gridDim.x * RB) {
-    const T *h = (const T *)a.x + row * a.x_stride;
-    const T *dy = (const T *)a.dy + row * a.dy_stride;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float xh[NP][8], q[NP][8];
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      load_cols<T, W>(h, 8 * (TPR * p + tr), d, xh[p]);
-      load_cols<T, W>(dy, 8 * (TPR * p + tr), d, q[p]);
-    }
+    BwdRow<T, NP> cur;
+    load_row<T, TPR, NP, W>(a, row, tr, cur);
+    const float mean = cur.mean, rstd = cur.rstd;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int c = 8 * (TPR * p + tr);
-      float g[8];
-      if (a.gamma) {
-        load_cols<T, W>((const T *)a.gamma, c, d, g);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = 1.f;
-      }
+    for (int p = 0; p < NP; ++p)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        xh[p][e] = (xh[p][e] - mean) * rstd;
-        if (c + e < d) {  // past the row q is zero, xh is not
-          dg[p][e] = fmaf(q[p][e], xh[p][e], dg[p][e]);
-          db[p][e] += q[p][e];
-          q[p][e] *= g[e];
-          s0 += q[p][e];
-          s1 = fmaf(q[p][e], xh[p][e], s1);
-        }
+        // past the row dy is zero (xh is not)
+        const float y = (float)cur.dy[p].v[e], xh = ((float)cur.h[p].v[e] - mean) * rstd;
+        dg[p][e] = fmaf(y, xh, dg[p][e]);
+        db[p][e] += y;
+        const float q = y * (float)gamma[p].v[e];
+        s0 += q;
+        s1 = fmaf(q, xh, s1);
       }
-    }
-    const float c0 = row_sum<WPR>(s0, red[par][0]) / (float)d;
-    const float c1 = row_sum<WPR>(s1, red[par][1]) / (float)d;
+    row_sum2<WPR>(s0, s1, red[par]);
+    const float c0 = s0 / (float)d, c1 = s1 / (float)d;
     par ^= 1;
     T *dx = (T *)a.y + row * d;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      const int c = 8 * (TPR * p + tr);
       float o[8];
-      if (a.r) {
-        load_cols<T, W>((const T *)a.r + row * a.r_stride, c, d, o);
-      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+      for (int e = 0; e < 8; ++e) {
+        const float q = (float)cur.dy[p].v[e] * (float)gamma[p].v[e];
+        const float xh = ((float)cur.h[p].v[e] - mean) * rstd;
+        o[e] = fmaf(q - c0 - xh * c1, rstd, a.r ? (float)cur.dh[p].v[e] : 0.f);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(q[p][e] - c0 - xh[p][e] * c1, rstd, o[e]);
-      store_cols<T, W>(dx, c, d, o);
+      store_cols<T, W>(dx, 8 * (TPR * p + tr), d, o);
     }
   }
   if (!a.part) return;
@@ -205,14 +258,14 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void k_norm_bwd(NormArgs 
         __syncthreads();
         if (rb > 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) comb[((rb - 1) * 8 + e) * 64 + tr] = v[p][e];
+          for (int e = 0; e < 8; ++e) comb[((rb - 1) * 8 + e) * TPR + tr] = v[p][e];
         }
         __syncthreads();
         if (rb == 0) {
 #pragma unroll
           for (int w = 0; w < RB - 1; ++w)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[p][e] += comb[(w * 8 + e) * 64 + tr];
+            for (int e = 0; e < 8; ++e) v[p][e] += comb[(w * 8 + e) * TPR + tr];
         }
       }
       if (rb == 0) {
@@ -250,10 +303,17 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const float *__restrict__ pa
 }
 
 // Waves a row is spread over. Forward: one wave to 4096 columns, four beyond;
-// with too few rows to fill the GPU a row takes four waves from 1024 columns
-// on. Backward: the sums of dgamma and dbeta take registers too.
+// with too few rows to fill the GPU a row takes four waves from 1024 columns on.
 int fwd_waves(int d, int64_t n) { return d > 4096 || (d >= 1024 && n <= 2048) ? 4 : 1; }
-int bwd_waves(int d) { return d > 8192 ? 16 : d > 2560 ? 4 : 1; }
+// Backward: a lane also holds its columns' sums, so a wave takes 2560 columns at
+// most, and each wave should walk several rows per sum it writes (one wave a row
+// against four: 131072 x 2048 412 and 419 us, 65536 x 2560 276 and 318, 4096 x
+// 2560 44 and 27). Rows of odd width, whose tails take branches, run better on
+// four (32768 x 2047: 177 and 146 us).
+int bwd_waves(int d, int64_t n) {
+  if (d > 8192) return 8;
+  return d > 2560 || (d > 512 && (n < 16384 || d % 8)) ? 4 : 1;
+}
 
 template <typename T, int WPR, int NP>
 hipError_t fwd_launch(const NormArgs &a, hipStream_t st) {
@@ -280,8 +340,7 @@ hipError_t bwd_launch(const NormArgs &a, hipStream_t st) {
 }  // namespace
 
 int norm_bwd_blocks(int d, int64_t n) {
-  const int rb = bwd_waves(d) == 1 ? 4 : 1;
-  const int most = bwd_waves(d) == 16 ? 512 : 1024;
+  const int w = bwd_waves(d, n), rb = w == 1 ? 4 : 1, most = w == 8 ? 512 : 1024;
   return (int)std::max<int64_t>(1, std::min<int64_t>((n + rb - 1) / rb, most));
 }
 
@@ -313,7 +372,7 @@ hipError_t norm_forward(const NormArgs &a, hipStream_t st) {
 
 template <typename T>
 hipError_t norm_backward(const NormArgs &a, hipStream_t st) {
-  const int wpr = bwd_waves(a.d), np = (a.d + 512 * wpr - 1) / (512 * wpr);
+  const int wpr = bwd_waves(a.d, a.n), np = (a.d + 512 * wpr - 1) / (512 * wpr);
   const auto main_pass = [&]() -> hipError_t {
     if (wpr == 1) {
       PIECES(1, bwd_launch)
@@ -325,7 +384,7 @@ hipError_t norm_backward(const NormArgs &a, hipStream_t st) {
         default: return hipErrorInvalidValue;
       }
     }
-    return bwd_launch<T, 16, 2>(a, st);
+    return np <= 3 ? bwd_launch<T, 8, 3>(a, st) : bwd_launch<T, 8, 4>(a, st);
   };
   hipError_t e = main_pass();
   if (e != hipSuccess || !a.part) return e;

@@ -416,7 +416,8 @@ class FeedForward:
         self.desc = FFDesc(d=d, d_ff=f, dtype=dt, w_gate=_p(w_gate), w_up=_p(w_up), w_down=_p(w_down))
 
     def forward(self, x, save: bool = False, stream=None):
-        """x: [..., d]. Returns y, or (y, a, u) with the pre-activations for the backward."""
+        """x: [..., d]. Returns y, or (y, a, u) with the pre-activations (fp32) for the
+        backward."""
         d, dtype, dev = self.d, self.dtype, self.device
         xs = _rows("x", x, d, dtype, dev)
         st = _on(stream, dev)
@@ -424,7 +425,7 @@ class FeedForward:
         y = torch.empty(x.shape, dtype=dtype, device=dev)
         a = u = None
         if save:
-            a = torch.empty(x.shape[:-1] + (self.d_ff,), dtype=dtype, device=dev)
+            a = torch.empty(x.shape[:-1] + (self.d_ff,), dtype=torch.float32, device=dev)
             u = torch.empty_like(a)
         need = ipttt_ff_workspace_bytes(self.desc, n)
         ws = _temp(need, dev, stream)
@@ -442,7 +443,7 @@ class FeedForward:
         n = x.numel() // d
         ds = _rows("dy", dy, d, dtype, dev, n)
         for name, t in (("a", a), ("u", u)):
-            _dense(name, t, x.shape[:-1] + (f,), dtype, dev)
+            _dense(name, t, x.shape[:-1] + (f,), torch.float32, dev)
         new = lambda *s: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
         g = {"dx": new(*x.shape), "dw_gate": new(f, d), "dw_up": new(f, d), "dw_down": new(d, f)}
         need = ipttt_ff_backward_workspace_bytes(self.desc, n)

@@ -191,7 +191,7 @@ size_t ipttt_ff_workspace_bytes(const ipttt_ff_desc *desc, int64_t n) {
 }
 
 ipttt_status ipttt_ff_forward(const ipttt_ff_desc *desc, const void *x, int64_t x_stride,
-                              int64_t n, void *y, int64_t y_stride, void *a, void *u,
+                              int64_t n, void *y, int64_t y_stride, float *a, float *u,
                               void *workspace, size_t workspace_bytes, void *hip_stream) {
   TRY(check_ff(desc, n));
   const size_t el = size_of(desc->dtype);
@@ -223,7 +223,7 @@ size_t ipttt_ff_backward_workspace_bytes(const ipttt_ff_desc *desc, int64_t n) {
 }
 
 ipttt_status ipttt_ff_backward(const ipttt_ff_desc *desc, const void *x, int64_t x_stride,
-                               const void *a, const void *u, const void *dy, int64_t dy_stride,
+                               const float *a, const float *u, const void *dy, int64_t dy_stride,
                                int64_t n, const ipttt_ff_grads *grads, void *workspace,
                                size_t workspace_bytes, void *hip_stream) {
   TRY(check_ff(desc, n));
@@ -246,8 +246,8 @@ ipttt_status ipttt_ff_backward(const ipttt_ff_desc *desc, const void *x, int64_t
   FfArgs p = ff_args(desc, n);
   p.x = x;
   p.x_stride = x_stride;
-  p.a = const_cast<void *>(a);
-  p.u = const_cast<void *>(u);
+  p.a = const_cast<float *>(a);
+  p.u = const_cast<float *>(u);
   p.dy = dy;
   p.dy_stride = dy_stride;
   p.dx = grads->dx;

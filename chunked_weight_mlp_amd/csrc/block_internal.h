@@ -65,7 +65,7 @@ struct FfArgs {
   int64_t x_stride;
   void *y;  // forward
   int64_t y_stride;
-  void *a, *u;     // pre-activations [n][F]: written by the forward (or null), read by the backward
+  float *a, *u;    // pre-activations [n][F]: written by the forward (or null), read by the backward
   const void *dy;  // backward
   int64_t dy_stride;
   void *dx;

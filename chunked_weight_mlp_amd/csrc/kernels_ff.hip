@@ -179,9 +179,13 @@ __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC)
   };
   const auto write = [&](auto tag) __attribute__((always_inline)) {
     constexpr bool FULL = decltype(tag)::value;
+    constexpr int TURN = Epi::TURN, PT = 40;  // pitch of a turned tile's rows (32 values)
+    static_assert(TURN * C::WM * C::WN * C::WTN * PT <= C::SMEM_ELEMS, "turned tiles fit the stages");
+    // this wave's own part of the stages, which every wave has left
+    __bf16 *const mine = smem + wave * (TURN * C::WTN * PT);
 #pragma unroll
     for (int i = 0; i < HI; i += 2) {
-      const int m = m0 + wm * WT + C::FM * i + 8 * (gq >> 1) + C::FM * (gq & 1);
+      const int mw = m0 + wm * WT + C::FM * i, ml = 8 * (gq >> 1) + C::FM * (gq & 1), m = mw + ml;
       typename Epi::In in[C::NJ];
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j) {  // all loads of these tiles before their stores
@@ -197,9 +201,30 @@ __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC)
           float w[8];
           rows8(acc[i + HI][j], acc[i + HI + 1][j], w);
           if (FULL || n < g.N) epi.template store<FULL>(m, n, v, w);
+        } else if constexpr (TURN > 0) {
+          bf16x8 t[TURN] = {};  // columns past the last are zero
+          if (FULL || n < g.N) epi.template store<FULL>(m, n, v, in[j], sp, t);
+#pragma unroll
+          for (int k = 0; k < TURN; ++k)
+            *(bf16x8 *)(mine + (k * C::WTN + C::FM * j + M::rcol(lane)) * PT + ml) = t[k];
         } else {
-          if (FULL || n < g.N) epi.template store<FULL>(m, n, v, in[j], sp);
+          if (FULL || n < g.N) epi.template store<FULL>(m, n, v, in[j], sp, nullptr);
         }
+      }
+      if constexpr (TURN > 0) {  // 32 rows x 64 columns, read back 8 columns of a row a lane
+#pragma unroll
+        for (int k = 0; k < TURN; ++k)
+#pragma unroll
+          for (int u = 0; u < C::WTN / 32; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const __bf16 *p = mine + (k * C::WTN + 32 * u + M::tr_row(lane)) * PT + C::FM * h +
+                                M::tr_col(lane);
+              const v4i16 lo = ds_read_tr16(p), hi = ds_read_tr16(p + 4 * PT);
+              epi.template turned<FULL>(
+                  k, mw + C::FM * h + (lane & 15), n0 + wn * C::WTN + 32 * u + 8 * gq,
+                  __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
+            }
       }
     }
   };
@@ -245,14 +270,17 @@ __device__ __forceinline__ Pack<T, 8> pack8(const T *row, int m, int M) {
 }
 
 // z = SiLU(a) u as the next product's operand (padded with zeros to Fp), and a,
-// u themselves when saved.
+// u themselves when saved: in fp32, so that the backward's only roundings are
+// those of its products' operands (with a and u in bf16 its errors against 64 bits
+// double, 1.7e-3 of rounding the result alone to 3.5e-3, for 4% of a training step).
 template <typename T>
 struct EpiZ {
   using In = NoIn;
+  static constexpr int TURN = 0;
   __bf16 *z;
   int64_t plane;
   int F, Fp;
-  T *a, *u;
+  float *a, *u;
   template <bool FULL>
   __device__ In load(int, int) const {
     return {};
@@ -267,8 +295,8 @@ struct EpiZ {
       zv[e] = FULL || m + e < F ? av[e] * fast_sigmoid(av[e]) * uv[e] : 0.f;
     store8_planes<planes_of<T>()>(z + (int64_t)n * Fp + m, plane, zv);
     if (a) {
-      store8<T, FULL>(a + (int64_t)n * F, m, F, av);
-      store8<T, FULL>(u + (int64_t)n * F, m, F, uv);
+      store8<float, FULL>(a + (int64_t)n * F, m, F, av);
+      store8<float, FULL>(u + (int64_t)n * F, m, F, uv);
     }
   }
 };
@@ -278,6 +306,7 @@ struct EpiZ {
 template <typename T>
 struct EpiOut {
   using In = NoIn;
+  static constexpr int TURN = 0;
   T *out, *out2;
   int64_t ld;
   int M, N, cut;  // N: rows of each output
@@ -290,7 +319,7 @@ struct EpiOut {
   // a tile may hold columns between the two outputs
   __device__ bool whole() const { return part || !out2 || cut == N; }
   template <bool FULL>
-  __device__ void store(int m, int n, const float (&v)[8], In, int sp) const {
+  __device__ void store(int m, int n, const float (&v)[8], In, int sp, bf16x8 *) const {
     if (part) {
       if (FULL || m < part_ld)
         blk::store_pack<float, 8>(part + sp * part_stride + (int64_t)n * part_ld + m, v);
@@ -303,40 +332,61 @@ struct EpiOut {
   }
 };
 
-// dz -> dA = dz u SiLU'(a), dU = dz SiLU(a), z = SiLU(a) u, operands padded with
-// zeros to Fp; a and u come from the forward in the block's type.
+// dz -> dA = dz u SiLU'(a), dU = dz SiLU(a), z = SiLU(a) u as operands: dA and dU
+// by token for dx, [n][2 Fp] padded with zeros to Fp; and all three by feature for
+// the weights' gradients. In bf16 the block turns its tile in LDS for that (TURN
+// results of store(), written by turned()); in fp32, three planes each, z is
+// written by token too and k_ff_lay turns them afterwards.
 template <typename T>
 struct EpiDz {
+  static constexpr int NP = planes_of<T>();
+  static constexpr int TURN = NP == 1 ? 3 : 0;
   struct In {
-    Pack<T, 8> a, u;
+    Pack<float, 8> a, u;
   };
-  const T *a, *u;
-  __bf16 *dau, *z;  // [n][2 Fp]: dA then dU; [n][Fp]
+  const float *a, *u;
+  __bf16 *dau, *z;  // z: fp32 only
   int64_t dau_plane, z_plane;
+  __bf16 *daut, *zt;  // bf16 only: [2 Fp][Tp], [Fp][Tp], zero past the last token
+  int64_t Tp;
   int F, Fp;
   __device__ bool whole() const { return true; }
   template <bool FULL>
   __device__ In load(int m, int n) const {
-    return {pack8<T, FULL>(a + (int64_t)n * F, m, F), pack8<T, FULL>(u + (int64_t)n * F, m, F)};
+    return {pack8<float, FULL>(a + (int64_t)n * F, m, F), pack8<float, FULL>(u + (int64_t)n * F, m, F)};
   }
   template <bool FULL>
-  __device__ void store(int m, int n, const float (&v)[8], const In &in, int) const {
+  __device__ void store(int m, int n, const float (&v)[8], const In &in, int, bf16x8 *turn) const {
     if (!FULL && m >= Fp) return;
     float da[8], du[8], zv[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const bool real = FULL || m + e < F;
-      const float av = (float)in.a.v[e], uv = (float)in.u.v[e];
+      const float av = in.a.v[e], uv = in.u.v[e];
       const float s = fast_sigmoid(av), h = av * s;
       da[e] = real ? v[e] * uv * (s + h * (1.f - s)) : 0.f;
       du[e] = real ? v[e] * h : 0.f;
       zv[e] = real ? h * uv : 0.f;
     }
-    constexpr int NP = planes_of<T>();
     __bf16 *row = dau + (int64_t)n * 2 * Fp + m;
     store8_planes<NP>(row, dau_plane, da);
     store8_planes<NP>(row + Fp, dau_plane, du);
-    store8_planes<NP>(z + (int64_t)n * Fp + m, z_plane, zv);
+    if constexpr (NP > 1) {
+      store8_planes<NP>(z + (int64_t)n * Fp + m, z_plane, zv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        turn[0][e] = (__bf16)da[e];
+        turn[1][e] = (__bf16)du[e];
+        turn[2][e] = (__bf16)zv[e];
+      }
+    }
+  }
+  // tokens n .. n + 7 of feature m of result k
+  template <bool FULL>
+  __device__ void turned(int k, int m, int n, bf16x8 v) const {
+    if (FULL || (m < Fp && n < Tp))
+      *(bf16x8 *)((k == 2 ? zt + (int64_t)m * Tp : daut + ((int64_t)k * Fp + m) * Tp) + n) = v;
   }
 };
 
@@ -498,8 +548,8 @@ __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
                                                       const T *__restrict__ w2,
                                                       const T *__restrict__ x, int64_t x_ld, int n,
                                                       int M, int K, T *__restrict__ out,
-                                                      int64_t out_ld, T *__restrict__ a,
-                                                      T *__restrict__ u) {
+                                                      int64_t out_ld, float *__restrict__ a,
+                                                      float *__restrict__ u) {
   constexpr int RB = 16 / KF;  // weight rows, tokens of a group
   constexpr int D = DUAL ? 2 : 1;
   constexpr int E = Quad<T>::E, S = 4 * KF * E;  // K values of a lane, of a step
@@ -610,8 +660,8 @@ __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
     if (m < M && col < n) {
       if constexpr (DUAL) {
         if (a) {
-          a[(int64_t)col * M + m] = (T)v[0];
-          u[(int64_t)col * M + m] = (T)v[1];
+          a[(int64_t)col * M + m] = v[0];
+          u[(int64_t)col * M + m] = v[1];
         }
         out[col * out_ld + m] = (T)(v[0] * fast_sigmoid(v[0]) * v[1]);
       } else {
@@ -635,7 +685,7 @@ bool few_tokens(int elem, int d, int F, int64_t n) {
 // the second, 31 with 4 and 1, 32 with 4 and 2; with eight waves 34).
 template <typename T, bool DUAL>
 hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n, int M, int K, T *out,
-                        int64_t out_ld, T *a, T *u, hipStream_t st) {
+                        int64_t out_ld, float *a, float *u, hipStream_t st) {
   constexpr int WV = 4;
 #define SMALL(NT, RG, KF)                                                                       \
   hipLaunchKernelGGL((k_ff_small<T, NT, RG, WV, KF, DUAL>),                                     \
@@ -834,7 +884,7 @@ struct BwdPlan {
     dy = w.planes(np, n, dp);
     wdt = w.planes(np, F, dp);
     dau = w.planes(np, n, 2 * Fp);
-    z = w.planes(np, n, Fp);
+    z = w.planes(np, np > 1 ? n : 0, Fp);
     wgut = w.planes(np, d, 2 * Fp);
     xt = w.planes(np, d, Tp);
     dyt = w.planes(np, d, Tp);
@@ -882,8 +932,7 @@ hipError_t ff_forward(const FfArgs &p, hipStream_t st) {
   const T *wg = (const T *)p.w_gate, *wu = (const T *)p.w_up, *wd = (const T *)p.w_down;
   if (few_tokens((int)sizeof(T), d, F, n)) {
     T *z = (T *)p.ws;
-    TRYH((launch_small<T, true>(wg, wu, (const T *)p.x, p.x_stride, n, F, d, z, F, (T *)p.a,
-                                (T *)p.u, st)));
+    TRYH((launch_small<T, true>(wg, wu, (const T *)p.x, p.x_stride, n, F, d, z, F, p.a, p.u, st)));
     return launch_small<T, false>(wd, nullptr, z, F, n, d, F, (T *)p.y, p.y_stride, nullptr, nullptr,
                                   st);
   }
@@ -897,7 +946,7 @@ hipError_t ff_forward(const FfArgs &p, hipStream_t st) {
   const Opnd o = lay.rows(wd, F, d, F, w.wd);
   TRYH(lay.launch(st));
   const FfProb q{g.p, u.p, x.p, g.ld, x.ld, g.plane, x.plane, F, n, (int)(kpad(d) / kStep), 1};
-  TRYH((product_with<NP, true>(q, EpiZ<T>{w.z, n * Fp, F, (int)Fp, (T *)p.a, (T *)p.u}, st)));
+  TRYH((product_with<NP, true>(q, EpiZ<T>{w.z, n * Fp, F, (int)Fp, p.a, p.u}, st)));
   const FfGroup<EpiOut<T>, 1> y{{with_operands(w.down, o, {w.z, Fp, n * Fp})},
                                 {EpiOut<T>{(T *)p.y, nullptr, p.y_stride, d, n, 1 << 30, w.part, 0, 0}},
                                 {}};
@@ -929,13 +978,15 @@ hipError_t ff_backward(const FfArgs &p, hipStream_t st) {
   // dz, and from it dA, dU and z
   const FfProb q{w.wdt, nullptr, dy.p, dp, dy.ld, F * dp, dy.plane, F, n, (int)(dp / kStep), 1};
   TRYH((product_with<NP, false>(q,
-                                EpiDz<T>{(const T *)p.a, (const T *)p.u, w.dau, w.z, n * 2 * Fp,
-                                         n * Fp, F, (int)Fp},
+                                EpiDz<T>{p.a, p.u, w.dau, w.z, n * 2 * Fp, n * Fp, w.daut, w.zt, Tp, F,
+                                         (int)Fp},
                                 st)));
-  Layouts<__bf16> turn;
-  turn.add(w.dau, 2 * Fp, n * 2 * Fp, NP, n, (int)(2 * Fp), w.daut, Tp, 2 * Fp * Tp, true);
-  turn.add(w.z, Fp, n * Fp, NP, n, (int)Fp, w.zt, Tp, Fp * Tp, true);
-  TRYH(turn.launch(st));
+  if constexpr (NP > 1) {
+    Layouts<__bf16> turn;
+    turn.add(w.dau, 2 * Fp, n * 2 * Fp, NP, n, (int)(2 * Fp), w.daut, Tp, 2 * Fp * Tp, true);
+    turn.add(w.z, Fp, n * Fp, NP, n, (int)Fp, w.zt, Tp, Fp * Tp, true);
+    TRYH(turn.launch(st));
+  }
   // dx = [dA dU] [W_g; W_u]; dW_g, dW_u (rows f < F of [dA dU]^T and from Fp on); dW_d
   const Opnd xt{w.xt, Tp, d * Tp}, dyt{w.dyt, Tp, d * Tp}, daut{w.daut, Tp, 2 * Fp * Tp};
   const FfGroup<EpiOut<T>, 3> out{

@@ -118,10 +118,12 @@ ipttt_status ipttt_recurrence_backward(const ipttt_recurrence *r, const ipttt_vi
 /* ---- gated feed-forward block -----------------------------------------------
  *   a = x W_g, u = x W_u, z = SiLU(a) * u, y = z W_d
  * for n tokens. Weights are output-major, as the layer's: w_gate, w_up
- * [d_ff][d], w_down [d][d_ff], 16-byte aligned. In bf16, z and (for the
- * backward) a and u are rounded to bf16 as the operands of the next product,
- * which run on bf16 MFMA with fp32 accumulation; in fp32 every product keeps
- * fp32 accuracy. Any d, d_ff; multiples of 64 avoid copies of the operands. */
+ * [d_ff][d], w_down [d][d_ff], 16-byte aligned. In bf16, z and the backward's dA
+ * and dU are rounded to bf16 as operands of the products they enter, which run on
+ * bf16 MFMA with fp32 accumulation; in fp32 every product keeps fp32 accuracy
+ * (a result whose operands are not all finite is not finite, but may be NaN
+ * where the formula has an infinity). Any d, d_ff; multiples of 64 avoid copies
+ * of the operands. */
 typedef struct {
   int32_t d;          /* 1 .. 65536  */
   int32_t d_ff;       /* 1 .. 262144 */
@@ -129,12 +131,12 @@ typedef struct {
   const void *w_gate, *w_up, *w_down;
 } ipttt_ff_desc;
 
-/* a, u: [n][d_ff] dense, both given to save the pre-activations for the
+/* a, u: [n][d_ff] fp32, dense, both given to save the pre-activations for the
  * backward or both NULL; 16-byte aligned. y rows are y_stride apart. n <= 2^24.
  * n == 0 is a successful no-op. The workspace must be 256-byte aligned. */
 size_t ipttt_ff_workspace_bytes(const ipttt_ff_desc *desc, int64_t n);
 ipttt_status ipttt_ff_forward(const ipttt_ff_desc *desc, const void *x, int64_t x_stride,
-                              int64_t n, void *y, int64_t y_stride, void *a, void *u,
+                              int64_t n, void *y, int64_t y_stride, float *a, float *u,
                               void *workspace, size_t workspace_bytes, void *hip_stream);
 
 /* Gradients, all in the descriptor's type, overwritten. dx rows are dx_stride
@@ -148,7 +150,7 @@ typedef struct {
 
 size_t ipttt_ff_backward_workspace_bytes(const ipttt_ff_desc *desc, int64_t n);
 ipttt_status ipttt_ff_backward(const ipttt_ff_desc *desc, const void *x, int64_t x_stride,
-                               const void *a, const void *u, const void *dy, int64_t dy_stride,
+                               const float *a, const float *u, const void *dy, int64_t dy_stride,
                                int64_t n, const ipttt_ff_grads *grads, void *workspace,
                                size_t workspace_bytes, void *hip_stream);
 

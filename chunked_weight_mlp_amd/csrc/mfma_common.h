@@ -71,7 +71,7 @@ __device__ __forceinline__ void set4(f32x16 &a, int g, f32x4 v) {
 }
 
 template <int WM_, int WN_, int BK_, int FM_ = 32, int PAD_ = 16, int PADT_ = 8, int OCC_ = 1,
-          int GM_ = 8, int WTN_ = 64, int MID_ = 0>
+          int GM_ = 8, int WTN_ = 64, int MID_ = 0, int WTM_ = 128>
 struct Cfg {
   static constexpr int WM = WM_, WN = WN_, BK = BK_, FM = FM_;
   // MFMA sub-steps of a K step done before the next step's LDS writes (0: all;
@@ -81,7 +81,7 @@ struct Cfg {
   static constexpr int OCC = OCC_;  // waves per SIMD the register allocation must allow
   using M = Mfma<FM>;
   using acc_t = typename M::acc_t;
-  static constexpr int WTM = 128, WTN = WTN_;  // wave tile
+  static constexpr int WTM = WTM_, WTN = WTN_;  // wave tile
   static constexpr int MI = WTM / FM, NJ = WTN / FM;
   static constexpr int BM = WTM * WM, BN = WTN * WN;
   static constexpr int NTHR = 64 * WM * WN;

@@ -19,6 +19,7 @@ from . import ipttt as _b
 from .ipttt import IPTTT_E_INVALID, IPTTT_E_UNSUPPORTED, IptttError, _check, _stream
 
 _DT = _b._DT
+_DENSE = torch.contiguous_format
 
 EXPORTS = (
     "ipttt_norm_forward", "ipttt_norm_backward_workspace_bytes", "ipttt_norm_backward",
@@ -270,13 +271,13 @@ class Norm:
         st = _on(stream, dev)
         shape = x.shape
         n = x.numel() // d
-        y = torch.empty(shape, dtype=dtype, device=dev)
+        y = torch.empty_like(x, memory_format=_DENSE)
         mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         rs, h = 0, None
         if res is not None:
             rs = _rows("res", res, d, dtype, dev, n)
-            h = torch.empty(shape, dtype=dtype, device=dev)
+            h = torch.empty_like(x, memory_format=_DENSE)
         ipttt_norm_forward(self.desc, x, xs, res, rs, n, h, y, mean, rstd, st)
         if stream is not None:
             _used_on(stream, x, res, h, y, mean, rstd, self.gamma, self.beta)
@@ -295,7 +296,7 @@ class Norm:
             if t.numel() != n:
                 raise _invalid(f"{name} has {t.numel()} values, expected {n}")
             _dense(name, t, t.shape, torch.float32, dev)
-        dx = torch.empty(h.shape, dtype=dtype, device=dev)
+        dx = torch.empty_like(h, memory_format=_DENSE)
         dgamma = torch.empty(d, dtype=torch.float32, device=dev)
         dbeta = torch.empty(d, dtype=torch.float32, device=dev)
         need = ipttt_norm_backward_workspace_bytes(self.desc, n)
@@ -345,7 +346,7 @@ def recurrence_forward(g, v, h0=None, starts=None, lens=None, stream=None):
         raise _invalid("g must be [batch, seq_len, d]")
     dev = g.device
     st = _on(stream, dev)
-    h = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    h = torch.empty_like(g, memory_format=_DENSE)
     r = _recurrence(g, v, h, h0, starts, lens)
     last = torch.empty((r.batch, r.d), dtype=torch.float32, device=dev)
     need = ipttt_recurrence_workspace_bytes(r)
@@ -363,7 +364,7 @@ def recurrence_step(g, v, state, out=None, stream=None):
         raise _invalid("g must be [batch, d]")
     dev = g.device
     st = _on(stream, dev)
-    h = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    h = torch.empty_like(g, memory_format=_DENSE)
     r = _recurrence(g, v, h, state)
     if out is None:
         out = torch.empty(g.shape, dtype=torch.float32, device=dev)
@@ -385,8 +386,8 @@ def recurrence_backward(g, v, h, dh, h0=None, dh_last=None, starts=None, lens=No
     shape, dtype, dev = g.shape, g.dtype, g.device
     st = _on(stream, dev)
     r = _recurrence(g, v, h, h0, starts, lens)
-    dg = torch.empty(shape, dtype=dtype, device=dev) if dg is None else dg
-    dv = torch.empty(shape, dtype=dtype, device=dev) if dv is None else dv
+    dg = torch.empty_like(g, memory_format=_DENSE) if dg is None else dg
+    dv = torch.empty_like(g, memory_format=_DENSE) if dv is None else dv
     dh0 = torch.empty((r.batch, r.d), dtype=torch.float32, device=dev)
     if dh_last is not None:
         _dense("dh_last", dh_last, (r.batch, r.d), torch.float32, dev)
@@ -422,7 +423,7 @@ class FeedForward:
         xs = _rows("x", x, d, dtype, dev)
         st = _on(stream, dev)
         n = x.numel() // d
-        y = torch.empty(x.shape, dtype=dtype, device=dev)
+        y = torch.empty_like(x, memory_format=_DENSE)
         a = u = None
         if save:
             a = torch.empty(x.shape[:-1] + (self.d_ff,), dtype=torch.float32, device=dev)

@@ -561,6 +561,14 @@ __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m0 = RG * RB * blockIdx.x;
+  const int first = NT * RB * blockIdx.y;  // this block's tokens
+  n -= first;
+  x += first * x_ld;
+  out += first * out_ld;
+  if (a) {
+    a += (int64_t)first * M;
+    u += (int64_t)first * M;
+  }
   const int r = lane & 15, kl = E * (r % KF + KF * (lane >> 4));
   const T *wrow[D][RG], *xrow[NT];
 #pragma unroll
@@ -671,13 +679,20 @@ __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
   }
 }
 
-// Whether a call streams its weights (k_ff_small) or runs on tiles: up to 16
-// tokens always, up to 64 in fp32, whose tiles do six times the work (1024 x 2048:
-// 32 and 115 us at 64 tokens), or where the weights are few (bf16, 32 and 64
-// tokens: 1024 x 1024 13 us against 30 on tiles, 1999 x 3001 32 and 62 against 66,
-// 2560 x 9728 77 and 98 against 70).
+// Whether a call streams its weights (k_ff_small, whose blocks of 64 tokens each
+// read them again, from L2 when they are few) or runs on tiles. Streaming costs
+// in proportion to n d F and has two launches; tiles take more, but more work at
+// a time. Both sides measured (us, streaming / tiles), bf16: 256 x 1024 at 512
+// tokens 15.9 / 16.6, at 1024 23 / 17; 512 x 2048 at 256 19.2 / 19.4; 1024 x 4096 at
+// 64 20.7 / 23.4, at 200 41 / 27; 2560 x 9728 at 16 47 / 70, at 32 77 / 70. Rows of odd
+// width: 250 x 671 at 400 20.6 / 20.6, at 1024 34 / 21; 1999 x 3001 at 32 31 / 53. fp32,
+// whose tiles do six times the work: 512 x 2048 at 256 50 / 57, at 400 76 / 62; 1024 x
+// 4096 at 128 81 / 105, at 200 148 / 113.
 bool few_tokens(int elem, int d, int F, int64_t n) {
-  return n <= 16 || (n <= 64 && (elem == 4 || (int64_t)d * F <= 6 << 20));
+  if (n <= 16) return true;
+  const bool odd = d % 8 || F % 8;
+  const int64_t most = elem == 4 ? 1 << 29 : odd && n > 64 ? 1 << 26 : 1 << 28;
+  return n <= most / ((int64_t)d * F);
 }
 
 // Row groups of a block of four waves: two where that makes two blocks a CU, else
@@ -689,8 +704,9 @@ hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n
   constexpr int WV = 4;
 #define SMALL(NT, RG, KF)                                                                       \
   hipLaunchKernelGGL((k_ff_small<T, NT, RG, WV, KF, DUAL>),                                     \
-                     dim3((M + RG * (16 / KF) - 1) / (RG * (16 / KF))), dim3(64 * WV), 0, st, w, w2, \
-                     x, x_ld, n, M, K, out, out_ld, a, u)
+                     dim3((M + RG * (16 / KF) - 1) / (RG * (16 / KF)),                        \
+                          (n + NT * (16 / KF) - 1) / (NT * (16 / KF))),                        \
+                     dim3(64 * WV), 0, st, w, w2, x, x_ld, n, M, K, out, out_ld, a, u)
 #define SMALL_TOKENS(RG) \
   if (n <= 4)            \
     SMALL(1, RG, 4);     \

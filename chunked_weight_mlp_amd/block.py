@@ -45,6 +45,15 @@ class RecurrenceDesc(ctypes.Structure):
                 ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("h0", ctypes.c_void_p)]
 
 
+class _FlatRecurrence(ctypes.Structure):
+    """RecurrenceDesc with its views' fields side by side: the same layout, built in one call."""
+    _fields_ = [("batch", ctypes.c_int32), ("d", ctypes.c_int32), ("seq_len", ctypes.c_int64),
+                ("dtype", ctypes.c_int)] + [
+        (f"{v}_{f}", t) for v in "gvh"
+        for f, t in (("p", ctypes.c_void_p), ("seq", ctypes.c_int64), ("tok", ctypes.c_int64))] + [
+        ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("h0", ctypes.c_void_p)]
+
+
 class FFDesc(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int32), ("d_ff", ctypes.c_int32), ("dtype", ctypes.c_int),
                 ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
@@ -71,9 +80,9 @@ def load() -> ctypes.CDLL:
             "ipttt_norm_forward": [P(NormDesc), vp, i64, vp, i64, i64, vp, vp, vp, vp, vp],
             "ipttt_norm_backward": [P(NormDesc), vp, i64, vp, vp, vp, i64, vp, i64, i64, vp, vp, vp,
                                     vp, sz, vp],
-            "ipttt_recurrence_forward": [P(RecurrenceDesc), vp, vp, sz, vp],
-            "ipttt_recurrence_step": [P(RecurrenceDesc), vp, vp],
-            "ipttt_recurrence_backward": [P(RecurrenceDesc), P(View), vp, P(View), P(View), vp, vp,
+            "ipttt_recurrence_forward": [vp, vp, vp, sz, vp],
+            "ipttt_recurrence_step": [vp, vp, vp],
+            "ipttt_recurrence_backward": [vp, P(View), vp, P(View), P(View), vp, vp,
                                           sz, vp],
             "ipttt_ff_forward": [P(FFDesc), vp, i64, i64, vp, i64, vp, vp, vp, sz, vp],
             "ipttt_ff_backward": [P(FFDesc), vp, i64, vp, vp, vp, i64, i64, P(FFGrads), vp, sz, vp],
@@ -82,7 +91,7 @@ def load() -> ctypes.CDLL:
             f = getattr(lib, name)
             f.argtypes, f.restype = args, ctypes.c_int
         for name, args in {"ipttt_norm_backward_workspace_bytes": [P(NormDesc), i64],
-                           "ipttt_recurrence_workspace_bytes": [P(RecurrenceDesc)],
+                           "ipttt_recurrence_workspace_bytes": [vp],
                            "ipttt_ff_workspace_bytes": [P(FFDesc), i64],
                            "ipttt_ff_backward_workspace_bytes": [P(FFDesc), i64]}.items():
             f = getattr(lib, name)
@@ -193,14 +202,15 @@ def _rows(name, t, d, dtype, device, n=None):
     """The row stride of a tensor of rows [..., d]: [n, d] of any row stride, or any
     number of leading dimensions laid out as equally spaced rows."""
     shape = t.shape
+    if (t.dtype is dtype and t.device == device and shape and shape[-1] == d and t.is_contiguous()
+            and (n is None or t.numel() == n * d)):
+        return d
     if not shape or shape[-1] != d:
         raise _invalid(f"{name} has shape {tuple(shape)}, expected rows of {d}")
     _is(name, t, dtype, device)
     rows = t.numel() // d
     if n is not None and rows != n:
         raise _invalid(f"{name} has {rows} rows, expected {n}")
-    if t.is_contiguous():
-        return d
     if rows > 0 and d > 1 and t.stride(-1) != 1:
         raise _invalid(f"{name} must have its last dimension contiguous")
     stride, span, first = d, 1, True
@@ -222,13 +232,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _on(stream, device):
     """The HIP stream of a call whose tensors are on `device`."""
+    index = device.index
     if device.type != "cuda":
         raise _invalid(f"tensors are on {device}, not on a GPU")
-    if device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise _invalid(f"tensors are on {device}, the current device is cuda:"
                        f"{torch.cuda.current_device()}")
     if stream is None and _raw_stream is not None:
-        return _raw_stream(device.index)
+        return _raw_stream(index)
     return _stream(stream)
 
 
@@ -262,6 +273,7 @@ class Norm:
         self.gamma = _dense("gamma", gamma, (self.d,), self.dtype, self.device)
         self.beta = None if beta is None else _dense("beta", beta, (self.d,), self.dtype, self.device)
         self.desc = NormDesc(d=self.d, dtype=dt, eps=eps, gamma=_p(gamma), beta=_p(beta))
+        self._ref = ctypes.byref(self.desc)
 
     def forward(self, x, res=None, stream=None):
         """Returns (y, h, mean, rstd): h = x + res (x itself without res), y its norm,
@@ -274,11 +286,14 @@ class Norm:
         y = torch.empty_like(x, memory_format=_DENSE)
         mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-        rs, h = 0, None
+        r = hp = h = None
+        rs = 0
         if res is not None:
-            rs = _rows("res", res, d, dtype, dev, n)
+            rs, r = _rows("res", res, d, dtype, dev, n), res.data_ptr()
             h = torch.empty_like(x, memory_format=_DENSE)
-        ipttt_norm_forward(self.desc, x, xs, res, rs, n, h, y, mean, rstd, st)
+            hp = h.data_ptr()
+        _check(load().ipttt_norm_forward(self._ref, x.data_ptr(), xs, r, rs, n, hp, y.data_ptr(),
+                                         mean.data_ptr(), rstd.data_ptr(), st))
         if stream is not None:
             _used_on(stream, x, res, h, y, mean, rstd, self.gamma, self.beta)
         return y, (x if h is None else h), mean, rstd
@@ -308,15 +323,17 @@ class Norm:
         return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
 
 
-def _view(name, t, shape, dtype, device):
-    """A View of a [batch, seq_len, d] tensor, or of [batch, d] as one token each."""
+def _strides(name, t, shape, dtype, device):
+    """(pointer, sequence stride, token stride) of a [batch, seq_len, d] tensor, or of
+    [batch, d] as one token each."""
     if t.shape != shape:
         raise _invalid(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    _is(name, t, dtype, device)
+    if t.dtype is not dtype or t.device != device:
+        _is(name, t, dtype, device)
     stride = t.stride()
     if stride[-1] != 1 and shape[-1] > 1 and t.numel():
         raise _invalid(f"{name} must have its channels contiguous")
-    return View(t.data_ptr(), stride[0], stride[-2])
+    return t.data_ptr(), stride[0], stride[-2]
 
 
 def _recurrence(g, v, h, h0, starts=None, lens=None):
@@ -332,9 +349,9 @@ def _recurrence(g, v, h, h0, starts=None, lens=None):
         starts = _dense("starts", starts, (n, length), torch.uint8, dev).data_ptr()
     if lens is not None:
         lens = _dense("lens", lens, (n,), torch.int32, dev).data_ptr()
-    return RecurrenceDesc(n, d, length, dt, _view("g", g, shape, dtype, dev),
-                          _view("v", v, shape, dtype, dev), _view("h", h, shape, dtype, dev), starts,
-                          lens, h0)
+    return _FlatRecurrence(n, d, length, dt, *_strides("g", g, shape, dtype, dev),
+                           *_strides("v", v, shape, dtype, dev), *_strides("h", h, shape, dtype, dev),
+                           starts, lens, h0)
 
 
 def recurrence_forward(g, v, h0=None, starts=None, lens=None, stream=None):
@@ -367,10 +384,11 @@ def recurrence_step(g, v, state, out=None, stream=None):
     h = torch.empty_like(g, memory_format=_DENSE)
     r = _recurrence(g, v, h, state)
     if out is None:
-        out = torch.empty(g.shape, dtype=torch.float32, device=dev)
+        out = (torch.empty_like(state) if state is not None else
+               torch.empty(g.shape, dtype=torch.float32, device=dev))
     else:
         _dense("out", out, g.shape, torch.float32, dev)
-    ipttt_recurrence_step(r, out, st)
+    _check(load().ipttt_recurrence_step(ctypes.byref(r), out.data_ptr(), st))
     if stream is not None:
         _used_on(stream, g, v, state, h, out)
     return h, out
@@ -393,9 +411,9 @@ def recurrence_backward(g, v, h, dh, h0=None, dh_last=None, starts=None, lens=No
         _dense("dh_last", dh_last, (r.batch, r.d), torch.float32, dev)
     need = ipttt_recurrence_workspace_bytes(r)
     ws = _temp(need, dev, stream)
-    ipttt_recurrence_backward(r, _view("dh", dh, shape, dtype, dev), dh_last,
-                              _view("dg", dg, shape, dtype, dev), _view("dv", dv, shape, dtype, dev),
-                              dh0, ws, need, st)
+    ipttt_recurrence_backward(r, View(*_strides("dh", dh, shape, dtype, dev)), dh_last,
+                              View(*_strides("dg", dg, shape, dtype, dev)),
+                              View(*_strides("dv", dv, shape, dtype, dev)), dh0, ws, need, st)
     if stream is not None:
         _used_on(stream, g, v, h, dh, h0, dh_last, starts, lens, dg, dv, dh0)
     return {"dg": dg, "dv": dv, "dh0": dh0}
@@ -415,6 +433,7 @@ class FeedForward:
         self.w_up = _dense("w_up", w_up, (f, d), self.dtype, self.device)
         self.w_down = _dense("w_down", w_down, (d, f), self.dtype, self.device)
         self.desc = FFDesc(d=d, d_ff=f, dtype=dt, w_gate=_p(w_gate), w_up=_p(w_up), w_down=_p(w_down))
+        self._ref = ctypes.byref(self.desc)
 
     def forward(self, x, save: bool = False, stream=None):
         """x: [..., d]. Returns y, or (y, a, u) with the pre-activations (fp32) for the
@@ -428,9 +447,10 @@ class FeedForward:
         if save:
             a = torch.empty(x.shape[:-1] + (self.d_ff,), dtype=torch.float32, device=dev)
             u = torch.empty_like(a)
-        need = ipttt_ff_workspace_bytes(self.desc, n)
+        need = load().ipttt_ff_workspace_bytes(self._ref, n)
         ws = _temp(need, dev, stream)
-        ipttt_ff_forward(self.desc, x, xs, n, y, d, a, u, ws, need, st)
+        _check(load().ipttt_ff_forward(self._ref, x.data_ptr(), xs, n, y.data_ptr(), d, _p(a), _p(u),
+                                       ws.data_ptr(), need, st))
         if stream is not None:
             _used_on(stream, x, y, a, u, self.w_gate, self.w_up, self.w_down)
         return (y, a, u) if save else y

@@ -54,6 +54,15 @@ def test_structure_layouts_match_c(tmp_path):
                     str(tmp_path / "l")], check=True)
     out = subprocess.run([str(tmp_path / "l")], capture_output=True, text=True, check=True).stdout
     assert [int(v) for v in out.split()] == want
+    # the binding's flat form of the recurrence has the same fields in the same places
+    flat = K._FlatRecurrence
+    assert ctypes.sizeof(flat) == ctypes.sizeof(K.RecurrenceDesc)
+    for v in "gvh":
+        at = getattr(K.RecurrenceDesc, v).offset
+        for f, full in (("p", "p"), ("seq", "seq_stride"), ("tok", "tok_stride")):
+            assert getattr(flat, f"{v}_{f}").offset == at + getattr(K.View, full).offset
+    for f in ("batch", "d", "seq_len", "dtype", "starts", "lens", "h0"):
+        assert getattr(flat, f).offset == getattr(K.RecurrenceDesc, f).offset
 
 
 class FakeMem:

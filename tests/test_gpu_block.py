@@ -420,6 +420,80 @@ def test_ff_gradient_against_differences():
         assert abs(diff - float(got[name][idx])) <= 1e-4 * max(1.0, abs(diff)), name
 
 
+# ---- large offsets, repeatability ---------------------------------------------------------------------
+
+
+def test_norm_offsets_past_32_bits():
+    """1.1 M rows of 2048: the last rows' results equal those of the rows alone."""
+    n, d = 1100000, 2048
+    assert n * d > 1 << 31
+    x = torch.empty((n, d), dtype=torch.bfloat16, device=DEV).normal_()
+    op = K.Norm(torch.ones(d, dtype=torch.bfloat16, device=DEV), torch.zeros(d, dtype=torch.bfloat16, device=DEV))
+    y, h, mean, rstd = op.forward(x, x)
+    tail = slice(n - 5000, n)
+    yt, ht, mt, rt = op.forward(x[tail], x[tail])
+    assert torch.equal(y[tail], yt) and torch.equal(h[tail], ht) and torch.equal(mean[tail], mt)
+    dx = op.backward(h, mean, rstd, y, x)["dx"]
+    want = op.backward(ht, mt, rt, yt, x[tail])["dx"]   # fewer rows: another split of a row's sum
+    assert rel_fro(dx[tail].float().cpu().numpy(), want.float().cpu().numpy()) <= 4e-3
+
+
+def test_recurrence_offsets_past_32_bits():
+    """1.1 M tokens of 2048 channels in one sequence; the last tokens equal a run from
+    the state before them (gates near 1/4: what is 100 tokens old has gone)."""
+    length, d = 1100000, 2048
+    assert length * d > 1 << 31
+    both = torch.empty((1, length, 2 * d), dtype=torch.bfloat16, device=DEV)
+    for at in range(0, length, 100000):   # in pieces: torch's own indexing has its limits
+        both[:, at:at + 100000].normal_()
+    g, v = both[..., :d], both[..., d:]
+    for at in range(0, length, 100000):
+        g[:, at:at + 100000] -= 1
+    h, last = K.recurrence_forward(g, v)
+    cut = length - 3000
+    ht, lt = K.recurrence_forward(g[:, cut:], v[:, cut:])
+    assert rel_fro(h[:, -2000:].float().cpu().numpy(), ht[:, -2000:].float().cpu().numpy()) <= 4e-3
+    assert rel_fro(last.cpu().numpy(), lt.cpu().numpy()) <= 2e-5
+    got = K.recurrence_backward(g, v, h, h)
+    want = K.recurrence_backward(g[:, cut:], v[:, cut:], h[:, cut:], h[:, cut:],
+                                 h0=h[:, cut - 1].float().contiguous())
+    for k in ("dg", "dv"):
+        assert rel_fro(got[k][:, cut:].float().cpu().numpy(), want[k].float().cpu().numpy()) <= 4e-3
+
+
+def test_ff_offsets_past_32_bits():
+    """262144 tokens through d_ff 9728: z, a, u and their gradients pass 2^31 elements."""
+    n, d, f = 262144, 64, 9728
+    assert n * f > 1 << 31
+    op = K.FeedForward(*[w.to(DEV) for w in ff_weights(d, f, torch.bfloat16)])
+    x = torch.empty((n, d), dtype=torch.bfloat16, device=DEV).normal_()
+    dy = torch.empty((n, d), dtype=torch.bfloat16, device=DEV).normal_()
+    y, a, u = op.forward(x, save=True)
+    dx = op.backward(x, a, u, dy)["dx"]
+    tail = slice(n - 300, n)
+    yt, at, ut = op.forward(x[tail], save=True)
+    assert rel_fro(y[tail].float().cpu().numpy(), yt.float().cpu().numpy()) <= 8e-3
+    assert rel_fro(a[tail].cpu().numpy(), at.cpu().numpy()) <= 1e-5
+    dxt = op.backward(x[tail], at, ut, dy[tail])["dx"]
+    assert rel_fro(dx[tail].float().cpu().numpy(), dxt.float().cpu().numpy()) <= 8e-3
+
+
+def test_norm_and_ff_repeat_bit_for_bit():
+    x, dy = rand((3000, 512), 1, torch.bfloat16).to(DEV), rand((3000, 512), 2, torch.bfloat16).to(DEV)
+    norm = K.Norm(torch.ones(512, dtype=torch.bfloat16, device=DEV))
+    ff = K.FeedForward(*[w.to(DEV) for w in ff_weights(512, 640, torch.bfloat16)])
+
+    def run():
+        y, h, m, r = norm.forward(x, dy)
+        z, a, u = ff.forward(y, save=True)
+        return [y, z, *norm.backward(h, m, r, dy).values(), *ff.backward(y, a, u, dy).values()]
+
+    first = run()
+    for _ in range(2):
+        for p, q in zip(first, run()):
+            assert torch.equal(p, q)
+
+
 # ---- streams and graphs ---------------------------------------------------------------------------
 
 

@@ -12,7 +12,6 @@
 namespace ipttt {
 namespace {
 
-using blk::load_pack;
 using blk::Pack;
 using blk::store_pack;
 using blk::wave_sum;
@@ -52,33 +51,49 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, float (*slot)[2]) {
   }
 }
 
-// 8 elements from column c of a row of d; zero at and past d. W: d is a
-// multiple of 8, so a piece is whole or absent.
-template <typename T, bool W>
-__device__ __forceinline__ void load_cols(const T *row, int c, int d, float (&v)[8]) {
-  if constexpr (W) {
-    load_pack<T, 8>(row + (c < d ? c : 0), v);
-    if (c >= d) {
+// Where a lane's NP pieces of a row of d columns are: piece p starts at column
+// 8 (TPR p + lane). All but the last are whole; the last may lie past the row's
+// end, or (W false: d is no multiple of 8) reach over it. A piece that would reach
+// over is taken back to the row's last 8 columns, so that every access stays one
+// wide one; the columns it then shares with its neighbour are computed twice, with
+// the same results, and counted once (own). Rows of fewer than 8 columns go
+// element by element.
+template <int TPR, int NP, bool W>
+struct Cols {
+  int first, d;
+  int at, off;  // last piece: its column, the first of its values that is its own
+  bool in;      // last piece: whether it has any
+  __device__ __forceinline__ Cols(int lane, int d_) : first(8 * lane), d(d_) {
+    const int c = 8 * TPR * (NP - 1) + first;
+    in = c < d;
+    at = W ? (in ? c : 0) : max(min(c, d - 8), 0);
+    off = in ? c - at : 8;
+  }
+  __device__ __forceinline__ int col(int p) const { return p < NP - 1 ? 8 * TPR * p + first : at; }
+  __device__ __forceinline__ bool own(int p, int e) const {
+    if (p < NP - 1) return true;
+    return W ? in : e >= off && at + e < d;
+  }
+  template <typename T>
+  __device__ __forceinline__ Pack<T, 8> load(const T *row, int p) const {
+    if (W || p < NP - 1 || d >= 8) return *(const Pack<T, 8> *)(row + col(p));
+    Pack<T, 8> v;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    for (int e = 0; e < 8; ++e) v.v[e] = e < d ? row[e] : (T)0.f;
+    return v;
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T *row, int p, const float (&v)[8]) const {
+    if (p == NP - 1 && !in) return;
+    if (W || p < NP - 1 || d >= 8) {
+      store_pack<T, 8>(row + col(p), v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < d) row[e] = (T)v[e];
     }
-  } else if (c + 8 <= d) {
-    load_pack<T, 8>(row + c, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < d ? (float)row[c + e] : 0.f;
   }
-}
-template <typename T, bool W>
-__device__ __forceinline__ void store_cols(T *row, int c, int d, const float (&v)[8]) {
-  if (c + 8 <= d) {
-    store_pack<T, 8>(row + c, v);
-  } else if constexpr (!W) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < d) row[c + e] = (T)v[e];
-  }
-}
+};
 
 template <typename T, int WPR, int NP, bool W>
 __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
@@ -89,28 +104,33 @@ __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
   const int64_t row = (int64_t)blockIdx.x * RB + threadIdx.x / TPR;
   if (row >= a.n) return;  // whole rows: with WPR > 1 the block is one row
   const int d = a.d;
+  const Cols<TPR, NP, W> cols(tr, d);
   const T *x = (const T *)a.x + row * a.x_stride;
   float h[NP][8];
 #pragma unroll
-  for (int p = 0; p < NP; ++p) load_cols<T, W>(x, 8 * (TPR * p + tr), d, h[p]);
+  for (int p = 0; p < NP; ++p) {
+    const Pack<T, 8> v = cols.load(x, p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[p][e] = (float)v.v[e];
+  }
   if (a.r) {
     const T *r = (const T *)a.r + row * a.r_stride;
     T *ho = (T *)a.h + row * d;
-    float q[NP][8];
+    Pack<T, 8> q[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) load_cols<T, W>(r, 8 * (TPR * p + tr), d, q[p]);
+    for (int p = 0; p < NP; ++p) q[p] = cols.load(r, p);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[p][e] += q[p][e];
-      store_cols<T, W>(ho, 8 * (TPR * p + tr), d, h[p]);
+      for (int e = 0; e < 8; ++e) h[p][e] += (float)q[p].v[e];
+      cols.store(ho, p, h[p]);
     }
   }
   float s = 0.f;
 #pragma unroll
   for (int p = 0; p < NP; ++p)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += h[p][e];
+    for (int e = 0; e < 8; ++e) s += cols.own(p, e) ? h[p][e] : 0.f;
   const float mean = row_sum<WPR>(s, red[0]) / (float)d;
   s = 0.f;
 #pragma unroll
@@ -118,7 +138,7 @@ __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       h[p][e] -= mean;
-      if (8 * (TPR * p + tr) + e < d) s = fmaf(h[p][e], h[p][e], s);
+      s = cols.own(p, e) ? fmaf(h[p][e], h[p][e], s) : s;
     }
   const float rstd = rsqrtf(row_sum<WPR>(s, red[1]) / (float)d + a.eps);
   if (a.mean && tr == 0) {
@@ -128,42 +148,13 @@ __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
   T *y = (T *)a.y + row * d;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const int c = 8 * (TPR * p + tr);
-    float g[8], b[8];
-    if (a.gamma) {
-      load_cols<T, W>((const T *)a.gamma, c, d, g);
-    } else {
+    Pack<T, 8> g, b;
+    if (a.gamma) g = cols.load((const T *)a.gamma, p);
+    if (a.beta) b = cols.load((const T *)a.beta, p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = 1.f;
-    }
-    if (a.beta) {
-      load_cols<T, W>((const T *)a.beta, c, d, b);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[p][e] = fmaf(h[p][e] * rstd, g[e], b[e]);
-    store_cols<T, W>(y, c, d, h[p]);
-  }
-}
-
-// 8 columns as they are stored, from column c of a row of d; zero at and past d.
-template <typename T, bool W>
-__device__ __forceinline__ Pack<T, 8> raw_cols(const T *row, int c, int d) {
-  if constexpr (W) {
-    Pack<T, 8> p = *(const Pack<T, 8> *)(row + (c < d ? c : 0));
-    if (c >= d) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p.v[e] = (T)0.f;
-    }
-    return p;
-  } else {
-    if (c + 8 <= d) return *(const Pack<T, 8> *)(row + c);
-    Pack<T, 8> p;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p.v[e] = c + e < d ? row[c + e] : (T)0.f;
-    return p;
+    for (int e = 0; e < 8; ++e)
+      h[p][e] = fmaf(h[p][e] * rstd, a.gamma ? (float)g.v[e] : 1.f, a.beta ? (float)b.v[e] : 0.f);
+    cols.store(y, p, h[p]);
   }
 }
 
@@ -173,20 +164,20 @@ struct BwdRow {
   Pack<T, 8> h[NP], dy[NP], dh[NP];
   float mean, rstd;
 };
-template <typename T, int TPR, int NP, bool W>
-__device__ __forceinline__ void load_row(const NormArgs &a, int64_t row, int tr, BwdRow<T, NP> &r) {
+template <typename T, class C, int NP>
+__device__ __forceinline__ void load_row(const NormArgs &a, int64_t row, const C &cols, BwdRow<T, NP> &r) {
   const T *h = (const T *)a.x + row * a.x_stride, *dy = (const T *)a.dy + row * a.dy_stride;
   const T *dh = (const T *)a.r + row * a.r_stride;
   r.mean = a.mean[row];
   r.rstd = a.rstd[row];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    r.h[p] = raw_cols<T, W>(h, 8 * (TPR * p + tr), a.d);
-    r.dy[p] = raw_cols<T, W>(dy, 8 * (TPR * p + tr), a.d);
+    r.h[p] = cols.load(h, p);
+    r.dy[p] = cols.load(dy, p);
   }
   if (a.r) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) r.dh[p] = raw_cols<T, W>(dh, 8 * (TPR * p + tr), a.d);
+    for (int p = 0; p < NP; ++p) r.dh[p] = cols.load(dh, p);
   }
 }
 
@@ -204,11 +195,12 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void k_norm_bwd(NormArgs 
   const int tr = threadIdx.x % TPR;
   const int rb = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   const int d = a.d;
+  const Cols<TPR, NP, W> cols(tr, d);
   float dg[NP][8], db[NP][8];
   Pack<T, 8> gamma[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    if (a.gamma) gamma[p] = raw_cols<T, W>((const T *)a.gamma, 8 * (TPR * p + tr), d);
+    if (a.gamma) gamma[p] = cols.load((const T *)a.gamma, p);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       dg[p][e] = db[p][e] = 0.f;
@@ -218,15 +210,18 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void k_norm_bwd(NormArgs 
   int par = 0;
   for (int64_t row = (int64_t)blockIdx.x * RB + rb; row < a.n; row += (int64_t)gridDim.x * RB) {
     BwdRow<T, NP> cur;
-    load_row<T, TPR, NP, W>(a, row, tr, cur);
+    load_row(a, row, cols, cur);
     const float mean = cur.mean, rstd = cur.rstd;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        // past the row dy is zero (xh is not)
-        const float y = (float)cur.dy[p].v[e], xh = ((float)cur.h[p].v[e] - mean) * rstd;
+        // a value that is not the lane's own counts as dy = 0 (and xh of one that
+        // is past the row's end is still finite or meets that zero in no sum)
+        const bool own = cols.own(p, e);
+        const float y = own ? (float)cur.dy[p].v[e] : 0.f;
+        const float xh = own ? ((float)cur.h[p].v[e] - mean) * rstd : 0.f;
         dg[p][e] = fmaf(y, xh, dg[p][e]);
         db[p][e] += y;
         const float q = y * (float)gamma[p].v[e];
@@ -246,7 +241,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void k_norm_bwd(NormArgs 
         const float xh = ((float)cur.h[p].v[e] - mean) * rstd;
         o[e] = fmaf(q - c0 - xh * c1, rstd, a.r ? (float)cur.dh[p].v[e] : 0.f);
       }
-      store_cols<T, W>(dx, 8 * (TPR * p + tr), d, o);
+      cols.store(dx, p, o);
     }
   }
   if (!a.part) return;
@@ -269,8 +264,13 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void k_norm_bwd(NormArgs 
         }
       }
       if (rb == 0) {
-        const int c = 8 * (TPR * p + tr);
-        store_cols<float, W>(out, c, d, v[p]);
+        if (W || p < NP - 1) {
+          cols.store(out, p, v[p]);
+        } else {  // the columns shared with a neighbour hold its sums, not these
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (cols.own(p, e)) out[cols.col(p) + e] = v[p][e];
+        }
       }
     }
   };

@@ -156,11 +156,13 @@ __global__ __launch_bounds__(64) void k_rec_seq_bwd(RecArgs a) {
 // Tiles of one (sequence, channel block) meet in `slots`, 8 bytes per tile and
 // channel: all ones (empty, written by k_rec_clear), then the tile's own map
 // (A, B) as soon as it is known, then (-1, s), the state after the tile (before
-// it, in the backward). A waits for nothing but its own 8 bytes, so a slot needs
-// no flag and no fence. A tile walks back from its neighbour, composing maps,
-// until it meets a state. Tiles are handed out by a counter in chain order, so
-// every tile a block waits for is held by a block that already runs and, by
-// induction from the first tile of each chain, ends.
+// it, in the backward). A tile waits for nothing but these 8 bytes, so a slot needs
+// no flag and no fence. It looks back over its neighbours to the nearest state and
+// applies the maps in between to it in the chain's order, so that its state is the
+// serial chain's bit for bit, whichever tiles had published theirs. Tiles are
+// handed out by a counter in chain order, so every tile a block waits for is held
+// by a block that already runs and, by induction from the first tile of each
+// chain, ends.
 
 constexpr uint64_t kEmpty = ~(uint64_t)0;
 // Polls of a tile before it gives up and returns NaN (about a second; a chain in
@@ -181,85 +183,65 @@ __device__ __forceinline__ uint64_t slot_get(const uint64_t *p) {
 }
 
 // The state handed to this lane's V channels by the `count` tiles behind slot
-// pointer `at` (the neighbour's slots), each `step` slots further back, the last
-// of which publishes a state at once. The block's waves take runs of LB tiles
-// side by side (one trip to memory covers NW LB tiles), reduce each run to one
-// map, and every wave composes the runs' maps from LDS. Called by the whole
-// block; all waves get the same state.
+// pointer `at` (the neighbour's slots), each `step` slots further back; the last
+// of them publishes a state at once. The block's waves read LB tiles each, one
+// trip to memory for the nearest NW LB; the furthest of these has to be a state,
+// the others may be maps. Called by the whole block; every wave gets the state.
 constexpr int LB = 2;
 
 template <int V, int NW>
 __device__ __forceinline__ void look_back(const uint64_t *at, int64_t step, int count,
-                                          float (&mapA)[NW][64 * V], float (&mapB)[NW][64 * V],
+                                          float (&mapA)[NW * LB][64 * V], float (&mapB)[NW * LB][64 * V],
                                           float (&state)[V]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float A[V], S[V];
-  bool done[V];
+  const int window = min(count, NW * LB);
+  uint64_t w[LB][V];
+#pragma unroll
+  for (int k = 0; k < LB; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      w[k][e] = slot_get(at - min(wave * LB + k, window - 1) * step + e);
+  int polls = 0;
+#pragma unroll
+  for (int k = 0; k < LB; ++k) {
+    const int t = wave * LB + k;
+    if (t < window) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const auto ready = [&]() {
+          return w[k][e] != kEmpty &&
+                 (t < window - 1 || __builtin_bit_cast(float, (uint32_t)w[k][e]) == -1.f);
+        };
+        while (!ready() && polls < kMaxPolls) {
+          __builtin_amdgcn_s_sleep(1);
+          w[k][e] = slot_get(at - t * step + e);
+          ++polls;
+        }
+        mapA[t][V * lane + e] = __builtin_bit_cast(float, (uint32_t)w[k][e]);
+        mapB[t][V * lane + e] = __builtin_bit_cast(float, (uint32_t)(w[k][e] >> 32));
+        if (!ready()) mapA[t][V * lane + e] = mapB[t][V * lane + e] = __builtin_nanf("");
+      }
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    A[e] = 1.f;
-    S[e] = 0.f;
-    done[e] = false;
+    const int ch = V * lane + e;
+    int t = 0;
+    while (t < window - 1 && mapA[t][ch] != -1.f) ++t;
+    float s = mapB[t][ch];
+    for (--t; t >= 0; --t) s = fmaf(mapA[t][ch], s, mapB[t][ch]);
+    state[e] = s;
   }
-  int polls = 0;
-  const auto compose = [&](float (&p)[V], float (&q)[V], bool (&end)[V], int e, float x, float y) {
-    if (!end[e]) {
-      q[e] = fmaf(p[e], y, q[e]);
-      if (x == -1.f)
-        end[e] = true;
-      else
-        p[e] *= x;
-    }
-  };
-  for (int o = 0; o < count; o += NW * LB) {
-    float a[V], b[V];
-    bool end[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      a[e] = 1.f;
-      b[e] = 0.f;
-      end[e] = false;
-    }
-    const int first = o + wave * LB, left = count - first;
-    if (left > 0) {
-      const uint64_t *p = at - first * step;
-      uint64_t w[LB][V];
-#pragma unroll
-      for (int k = 0; k < LB; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) w[k][e] = slot_get(p - min(k, left - 1) * step + e);
-#pragma unroll
-      for (int k = 0; k < LB; ++k)
-        if (k < left) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            while (w[k][e] == kEmpty && polls < kMaxPolls) {
-              __builtin_amdgcn_s_sleep(1);
-              w[k][e] = slot_get(p - k * step + e);
-              ++polls;
-            }
-            compose(a, b, end, e, __builtin_bit_cast(float, (uint32_t)w[k][e]),
-                    __builtin_bit_cast(float, (uint32_t)(w[k][e] >> 32)));
-          }
-        }
-    }
-    if (o > 0) __syncthreads();  // the last round's maps have been read
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      mapA[wave][V * lane + e] = end[e] ? -1.f : a[e];
-      mapB[wave][V * lane + e] = b[e];
-    }
-    __syncthreads();
-    bool all = true;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      for (int q = 0; q < NW; ++q) compose(A, S, done, e, mapA[q][V * lane + e], mapB[q][V * lane + e]);
-      all = all && done[e];
-    }
-    if (__all(all)) break;  // the same in every wave: they read the same maps
-  }
-#pragma unroll
-  for (int e = 0; e < V; ++e) state[e] = S[e];
+}
+
+// The first of the V channels of a lane whose own ones start at channel c: c, or,
+// where those would reach over the row's end, the row's last V. The lane's
+// neighbour then computes some of them too, with the same results; so packs are
+// whole but for rows of fewer than V channels.
+template <int V>
+__device__ __forceinline__ int lane_channel(int c, int d) {
+  return c < d && d >= V ? min(c, d - V) : c;
 }
 
 // A raw pack of V channels; channels at or past d are zero.
@@ -320,13 +302,13 @@ constexpr int64_t kSlotBase = 256;  // bytes in front of the slots: the tile cou
 template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
-  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW][CH], lB[NW][CH];
+  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW * LB][CH], lB[NW * LB][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   const int lane = threadIdx.x & 63, n = tl.n;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t len = seq_length(a, n), t0 = tl.ord * TT;
-  const int c = CH * tl.cb + V * lane, d = a.d;
+  const int d = a.d, c = lane_channel<V>(CH * tl.cb + V * lane, d);
   const int64_t tb = t0 + wave * R;
   const int cnt = (int)min(max(len - tb, (int64_t)0), (int64_t)R);
   T *h = seq_of<T>(a.h, n);
@@ -341,11 +323,11 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
     return;
   }
   // the wave's tokens as local states hl (from a zero state) and products P.
-  // FAST: all R tokens, whole packs (d a multiple of V) and no document start,
-  // as most waves have it: straight code.
+  // FAST: all R tokens, whole packs and no document start, as most waves have it:
+  // straight code.
   float P[R][V], hl[R][V];
   const uint64_t cuts = start_bits<R>(a, n, tb, tb + cnt);
-  const bool fast = cnt == R && d % V == 0 && cuts == 0;
+  const bool fast = cnt == R && d >= V && cuts == 0;
   const uint32_t at = (c < d ? c : 0) * (uint32_t)sizeof(T);
   const auto local = [&](auto tag) __attribute__((always_inline)) {
     constexpr bool FAST = decltype(tag)::value;
@@ -464,13 +446,13 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
 template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
-  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW][CH], lB[NW][CH];
+  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW * LB][CH], lB[NW * LB][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   const int lane = threadIdx.x & 63, n = tl.n;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t len = seq_length(a, n), tile = nt - 1 - tl.ord, t0 = tile * TT;
-  const int c = CH * tl.cb + V * lane, d = a.d;
+  const int d = a.d, c = lane_channel<V>(CH * tl.cb + V * lane, d);
   const int64_t tb = t0 + wave * R;
   const int cnt = (int)min(max(len - tb, (int64_t)0), (int64_t)R);
   T *dg = seq_of<T>(a.dg, n), *dv = seq_of<T>(a.dv, n);
@@ -489,7 +471,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
     return;
   }
   const uint64_t cuts = start_bits<R>(a, n, tb, tb + cnt);
-  const bool fast = cnt == R && d % V == 0 && cuts == 0 && tb > 0;
+  const bool fast = cnt == R && d >= V && cuts == 0 && tb > 0;
   const uint32_t at = (c < d ? c : 0) * (uint32_t)sizeof(T);
   Pack<T, V> gr[R], dr[R], vr[R], pr[R];
   float A[V], B[V];

@@ -307,12 +307,11 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const float *__restrict__ pa
 int fwd_waves(int d, int64_t n) { return d > 4096 || (d >= 1024 && n <= 2048) ? 4 : 1; }
 // Backward: a lane also holds its columns' sums, so a wave takes 2560 columns at
 // most, and each wave should walk several rows per sum it writes (one wave a row
-// against four: 131072 x 2048 412 and 419 us, 65536 x 2560 276 and 318, 4096 x
-// 2560 44 and 27). Rows of odd width, whose tails take branches, run better on
-// four (32768 x 2047: 177 and 146 us).
+// against four: 131072 x 2048 412 and 419 us, 65536 x 2560 276 and 318, 262144 x 639
+// 495 and 737, but 4096 x 2560 44 and 27).
 int bwd_waves(int d, int64_t n) {
   if (d > 8192) return 8;
-  return d > 2560 || (d > 512 && (n < 16384 || d % 8)) ? 4 : 1;
+  return d > 2560 || (d > 512 && n < 16384) ? 4 : 1;
 }
 
 template <typename T, int WPR, int NP>
@@ -340,7 +339,9 @@ hipError_t bwd_launch(const NormArgs &a, hipStream_t st) {
 }  // namespace
 
 int norm_bwd_blocks(int d, int64_t n) {
-  const int w = bwd_waves(d, n), rb = w == 1 ? 4 : 1, most = w == 8 ? 512 : 1024;
+  // two blocks a CU of the wide rows' kernels, whose registers leave room for no more
+  // (13590 x 4672: 109 us, with 1024 blocks 120), four of the others
+  const int w = bwd_waves(d, n), rb = w == 1 ? 4 : 1, most = w == 1 ? 1024 : 512;
   return (int)std::max<int64_t>(1, std::min<int64_t>((n + rb - 1) / rb, most));
 }
 

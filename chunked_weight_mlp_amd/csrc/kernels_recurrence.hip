@@ -153,16 +153,18 @@ __global__ __launch_bounds__(64) void k_rec_seq_bwd(RecArgs a) {
 // A block of NW waves takes TT = NW R tokens of 64 V channels of one sequence;
 // a lane holds V channels, a wave R consecutive tokens.
 //
-// Tiles of one (sequence, channel block) meet in `slots`, 8 bytes per tile and
-// channel: all ones (empty, written by k_rec_clear), then the tile's own map
-// (A, B) as soon as it is known, then (-1, s), the state after the tile (before
-// it, in the backward). A tile waits for nothing but these 8 bytes, so a slot needs
-// no flag and no fence. It looks back over its neighbours to the nearest state and
-// applies the maps in between to it in the chain's order, so that its state is the
-// serial chain's bit for bit, whichever tiles had published theirs. Tiles are
-// handed out by a counter in chain order, so every tile a block waits for is held
-// by a block that already runs and, by induction from the first tile of each
-// chain, ends.
+// Tiles of one (sequence, channel block) form a chain in groups of G. They meet in
+// slots of 8 bytes per channel: all ones (empty, written by k_rec_clear), then a map
+// (A, B), or (-1, s) for one that ignores the state: a value that validates itself,
+// so a slot needs no flag and no fence. A tile publishes its map. The last tile of a
+// group composes the group's maps in order, publishes that map, and then, once it
+// knows the state before the group, the state after it in the same slot. A tile's
+// state is that of its group's start, the nearest published state behind it with the
+// groups' maps in between applied in order, and the maps of the tiles before it in
+// its group, in order: the same operations whichever slots already held states, so
+// results do not depend on timing. Tiles are handed out by a counter in chain order,
+// so every tile a block waits for is held by a block that already runs and, by
+// induction from the first tile of each chain, ends.
 
 constexpr uint64_t kEmpty = ~(uint64_t)0;
 // Polls of a tile before it gives up and returns NaN (about a second; a chain in
@@ -182,57 +184,119 @@ __device__ __forceinline__ uint64_t slot_get(const uint64_t *p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state handed to this lane's V channels by the `count` tiles behind slot
-// pointer `at` (the neighbour's slots), each `step` slots further back; the last
-// of them publishes a state at once. The block's waves read LB tiles each, one
-// trip to memory for the nearest NW LB; the furthest of these has to be a state,
-// the others may be maps. Called by the whole block; every wave gets the state.
-constexpr int LB = 2;
+// One map after another: the state s through map (a, b), and map (a, b) after (p, q).
+__device__ __forceinline__ float through(float a, float b, float s) { return a == -1.f ? b : fmaf(a, s, b); }
+__device__ __forceinline__ void after(float a, float b, float &p, float &q) {
+  q = a == -1.f ? b : fmaf(a, q, b);
+  p = a == -1.f || p == -1.f ? -1.f : a * p;
+}
 
+// A chain's place in the workspace. Tile `ord` of the launch's order and group g of
+// the chain have their channels' slots at tile(ord) and group(g).
+constexpr int LB = 1;  // slots a wave reads of each kind: groups of NW LB tiles
+struct Chain {
+  uint64_t *tiles, *groups;
+  int64_t step;  // slots between tiles, and between groups
+  __device__ uint64_t *tile(int64_t ord) const { return tiles + ord * step; }
+  __device__ uint64_t *group(int64_t g) const { return groups + g * step; }
+};
+
+// Slots t < count of a run, `stride` apart, into LDS as maps, LB of them per wave;
+// w holds what was read ahead. With `state_last` the last one has to be a state.
 template <int V, int NW>
-__device__ __forceinline__ void look_back(const uint64_t *at, int64_t step, int count,
-                                          float (&mapA)[NW * LB][64 * V], float (&mapB)[NW * LB][64 * V],
-                                          float (&state)[V]) {
+__device__ __forceinline__ void take_slots(uint64_t (&w)[LB][V], const uint64_t *at, int64_t stride,
+                                           int count, bool state_last, int &polls,
+                                           float (&mapA)[NW * LB][64 * V], float (&mapB)[NW * LB][64 * V]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int window = min(count, NW * LB);
-  uint64_t w[LB][V];
-#pragma unroll
-  for (int k = 0; k < LB; ++k)
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      w[k][e] = slot_get(at - min(wave * LB + k, window - 1) * step + e);
-  int polls = 0;
 #pragma unroll
   for (int k = 0; k < LB; ++k) {
     const int t = wave * LB + k;
-    if (t < window) {
+    if (t < count) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const auto ready = [&]() {
-          return w[k][e] != kEmpty &&
-                 (t < window - 1 || __builtin_bit_cast(float, (uint32_t)w[k][e]) == -1.f);
+          return w[k][e] != kEmpty && (!state_last || t < count - 1 ||
+                                       __builtin_bit_cast(float, (uint32_t)w[k][e]) == -1.f);
         };
         while (!ready() && polls < kMaxPolls) {
           __builtin_amdgcn_s_sleep(1);
-          w[k][e] = slot_get(at - t * step + e);
+          w[k][e] = slot_get(at + t * stride + e);
           ++polls;
         }
-        mapA[t][V * lane + e] = __builtin_bit_cast(float, (uint32_t)w[k][e]);
-        mapB[t][V * lane + e] = __builtin_bit_cast(float, (uint32_t)(w[k][e] >> 32));
-        if (!ready()) mapA[t][V * lane + e] = mapB[t][V * lane + e] = __builtin_nanf("");
+        const bool ok = ready();
+        mapA[t][V * lane + e] = ok ? __builtin_bit_cast(float, (uint32_t)w[k][e]) : __builtin_nanf("");
+        mapB[t][V * lane + e] =
+            ok ? __builtin_bit_cast(float, (uint32_t)(w[k][e] >> 32)) : __builtin_nanf("");
       }
     }
   }
-  __syncthreads();
+}
+
+// The state before tile `ord`, the ci-th of its chain, whose own map is (A, B); state
+// holds the chain's initial state (used in its first group). `more`: tiles follow.
+// Called by the whole block with A, B valid in wave `pub`; every wave gets the state.
+template <int V, int NW>
+__device__ __forceinline__ void chain_state(const Chain &c, int64_t ord, int ci, bool more, int pub,
+                                            const float (&A)[V], const float (&B)[V],
+                                            float (&mapA)[2][NW * LB][64 * V],
+                                            float (&mapB)[2][NW * LB][64 * V], float (&state)[V]) {
+  constexpr int G = NW * LB;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int idx = ci % G, g = ci / G, window = min(g, G);
+  const bool last = more && idx == G - 1;  // the group's last: it publishes the group
+  if (wave == pub && more && !last) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int ch = V * lane + e;
-    int t = 0;
-    while (t < window - 1 && mapA[t][ch] != -1.f) ++t;
-    float s = mapB[t][ch];
-    for (--t; t >= 0; --t) s = fmaf(mapA[t][ch], s, mapB[t][ch]);
-    state[e] = s;
+    for (int e = 0; e < V; ++e) slot_put(c.tile(ord) + V * lane + e, A[e], B[e]);
   }
+  // read ahead the tiles before this one in its group, first to last, and the
+  // groups before it, nearest first
+  const uint64_t *tiles = c.tile(ord - idx) + V * lane, *groups = c.group(max(g - 1, 0)) + V * lane;
+  uint64_t wt[LB][V], wg[LB][V];
+#pragma unroll
+  for (int k = 0; k < LB; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int t = wave * LB + k;
+      wt[k][e] = t < idx ? slot_get(tiles + t * c.step + e) : 0;
+      wg[k][e] = t < window ? slot_get(groups - t * c.step + e) : 0;
+    }
+  int polls = 0;
+  take_slots<V, NW>(wt, tiles, c.step, idx, false, polls, mapA[0], mapB[0]);
+  __syncthreads();
+  float p[V], q[V];
+  if (wave == pub && last) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      p[e] = mapA[0][0][V * lane + e];
+      q[e] = mapB[0][0][V * lane + e];
+      for (int t = 1; t < G - 1; ++t) after(mapA[0][t][V * lane + e], mapB[0][t][V * lane + e], p[e], q[e]);
+      after(A[e], B[e], p[e], q[e]);
+      if (g > 0) slot_put(c.group(g) + V * lane + e, p[e], q[e]);
+    }
+  }
+  if (g > 0) {
+    take_slots<V, NW>(wg, groups, -c.step, window, true, polls, mapA[1], mapB[1]);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int ch = V * lane + e;
+      int t = 0;
+      while (t < window - 1 && mapA[1][t][ch] != -1.f) ++t;
+      float s = mapB[1][t][ch];
+      for (--t; t >= 0; --t) s = fmaf(mapA[1][t][ch], s, mapB[1][t][ch]);
+      state[e] = s;
+    }
+  }
+  if (wave == pub && last) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (g == 0 || p[e] != -1.f)
+        slot_put(c.group(g) + V * lane + e, -1.f, through(p[e], q[e], state[e]));
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    for (int t = 0; t < idx; ++t)
+      state[e] = through(mapA[0][t][V * lane + e], mapB[0][t][V * lane + e], state[e]);
 }
 
 // The first of the V channels of a lane whose own ones start at channel c: c, or,
@@ -299,10 +363,17 @@ __device__ __forceinline__ uint64_t start_bits(const RecArgs &a, int n, int64_t 
 
 constexpr int64_t kSlotBase = 256;  // bytes in front of the slots: the tile counter
 
+template <int V>
+__device__ __forceinline__ Chain chain_of(const RecArgs &a, const Tile &t, int64_t nt) {
+  const int64_t cbs = (a.d + 64 * V - 1) / (64 * V), step = (int64_t)a.n * cbs * 64 * V;
+  uint64_t *const at = (uint64_t *)((char *)a.ws + kSlotBase) + ((int64_t)t.n * cbs + t.cb) * 64 * V;
+  return {at, at + nt * step, step};
+}
+
 template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
-  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW * LB][CH], lB[NW * LB][CH];
+  __shared__ float sA[NW][CH], sB[NW][CH], lA[2][NW * LB][CH], lB[2][NW * LB][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   const int lane = threadIdx.x & 63, n = tl.n;
@@ -316,7 +387,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   if (c < d)
     for (int r = cnt; r < R && tb + r < a.L; ++r) store_ch<T, V>(h + (tb + r) * a.h.tok_stride, c, d, zero);
   float s[V] = {};
-  if (tl.ord == 0 && a.h0 && c < d) load_ch<float, V>(a.h0 + (int64_t)n * d, c, d, s);
+  if (a.h0 && c < d) load_ch<float, V>(a.h0 + (int64_t)n * d, c, d, s);
   if (t0 >= len) {  // nothing of the sequence here, and nobody waits for it
     if (tl.ord == 0 && wave == 0 && a.h_last && c < d)
       store_ch<float, V>(a.h_last + (int64_t)n * d, c, d, s);
@@ -400,24 +471,15 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
     }
     cut = cut || k;
   }
-  const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
-  uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) + tl.ord * step +
-                   (int64_t)n * ((d + CH - 1) / CH) * CH + (int64_t)tl.cb * CH + V * lane;
-  const bool more = wave == 0 && t0 + TT < len;  // a tile behind this one reads the slots
-  if (tl.ord > 0) {
-    if (more) {
+  if (cut) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
-    }
-    look_back<V, NW>(mine - step, step, (int)tl.ord, lA, lB, s);
+    for (int e = 0; e < V; ++e) A[e] = -1.f;
   }
-  if (more && !(cut && tl.ord > 0)) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
-  }
+  if (nt > 1)
+    chain_state<V, NW>(chain_of<V>(a, tl, nt), tl.ord, (int)tl.ord, t0 + TT < len, 0, A, B, lA, lB, s);
   if (wave > 0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
+    for (int e = 0; e < V; ++e) s[e] = through(A[e], B[e], s[e]);
   }
   if (c >= d) return;
   float o[V] = {};
@@ -446,7 +508,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
 template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
-  __shared__ float sA[NW][CH], sB[NW][CH], lA[NW * LB][CH], lB[NW * LB][CH];
+  __shared__ float sA[NW][CH], sB[NW][CH], lA[2][NW * LB][CH], lB[2][NW * LB][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   const int lane = threadIdx.x & 63, n = tl.n;
@@ -462,9 +524,8 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
       store_ch<T, V>(dg + (tb + r) * a.dg.tok_stride, c, d, zero);
       store_ch<T, V>(dv + (tb + r) * a.dv.tok_stride, c, d, zero);
     }
-  const bool first = t0 + TT >= len;  // the chain's first tile of this sequence
   float s[V] = {};
-  if (first && a.dh_last && c < d) load_ch<float, V>(a.dh_last + (int64_t)n * d, c, d, s);
+  if (a.dh_last && c < d) load_ch<float, V>(a.dh_last + (int64_t)n * d, c, d, s);
   if (t0 >= len) {
     if (tile == 0 && wave == 0 && a.dh0 && c < d)
       store_ch<float, V>(a.dh0 + (int64_t)n * d, c, d, s);
@@ -549,25 +610,16 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
     }
     cut = cut || k;
   }
-  const int64_t step = (int64_t)a.n * ((d + CH - 1) / CH) * CH;
-  uint64_t *mine = (uint64_t *)((char *)a.ws + kSlotBase) + tl.ord * step +
-                   (int64_t)n * ((d + CH - 1) / CH) * CH + (int64_t)tl.cb * CH + V * lane;
-  const bool more = wave == NW - 1 && tile > 0;
-  if (!first) {
-    if (more) {
+  if (cut) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) slot_put(mine + e, cut ? -1.f : A[e], B[e]);
-    }
-    // the tiles between this one and the sequence's last
-    look_back<V, NW>(mine - step, step, (int)((len - 1) / TT - tile), lA, lB, s);
+    for (int e = 0; e < V; ++e) A[e] = -1.f;
   }
-  if (more && !(cut && !first)) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) slot_put(mine + e, -1.f, cut ? B[e] : fmaf(A[e], s[e], B[e]));
-  }
+  if (nt > 1)
+    chain_state<V, NW>(chain_of<V>(a, tl, nt), tl.ord, (int)((len - 1) / TT - tile), tile > 0, NW - 1, A,
+                       B, lA, lB, s);
   if (wave < NW - 1) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = cut ? B[e] : fmaf(A[e], s[e], B[e]);
+    for (int e = 0; e < V; ++e) s[e] = through(A[e], B[e], s[e]);
   }
   if (c >= d) return;
   const auto finish = [&](auto tag) __attribute__((always_inline)) {
@@ -624,17 +676,20 @@ __global__ __launch_bounds__(256) void k_rec_clear(uint64_t *ws, int64_t slots) 
 
 constexpr int64_t SEQ_MAX = 16;
 
-// Channels per lane, tokens per wave in the forward and the backward, waves.
-// Measured (128k x 2560 forward / 8 x 16k x 2048 backward, bf16): 16 tokens, 8
-// waves 485 / 609 us; 8 tokens 688 / 686; 32 tokens (forward) 476; 4 waves of 16
-// 572 / 640; 16 waves of 8 (backward) 760; 4 channels a lane 725 / 899 and up
-// (registers). Look-back runs of 1, 2, 4, 8 tiles a wave: 501, 485, 492, 526.
+// Channels per lane, tokens per wave in the forward and the backward, waves, all
+// measured on 128k x 2560 forward / 8 x 16k x 2048 backward, bf16, where a copy of
+// the same bytes takes 421 / 674 us. As here 483 / 601 us. 8 tokens a wave 688 / 686,
+// 32 (forward) 476 but 28 us against 17 for 5 x 1237 x 331; 4 waves of 16 tokens 572 /
+// 640, 16 waves of 8 (backward) 760; 4 channels a lane 725 / 899 and up (registers).
+// Slots a wave reads (LB) 1, 2, 3: 483, 513, 530 (forward). Bound by HBM.
 constexpr int kV = 2, kFwdTokens = 16, kBwdTokens = 16, kWaves = 8;
 constexpr int kFwdTile = kFwdTokens * kWaves, kBwdTile = kBwdTokens * kWaves;
 constexpr int kMinTile = kFwdTile < kBwdTile ? kFwdTile : kBwdTile;  // what the workspace holds
 
 int64_t channel_blocks(int d) { return (d + 64 * kV - 1) / (64 * kV); }
-int64_t tile_slots(int n, int d, int64_t nt) { return nt * n * channel_blocks(d) * 64 * kV; }
+int64_t tile_slots(int n, int d, int64_t nt) {  // and the groups'
+  return (nt + nt / (kWaves * LB) + 1) * n * channel_blocks(d) * 64 * kV;
+}
 
 hipError_t clear_slots(const RecArgs &a, int64_t nt, hipStream_t st) {
   if (nt <= 1) return hipSuccess;

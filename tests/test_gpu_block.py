@@ -297,12 +297,18 @@ def test_recurrence_gradient_into_a_fused_projection():
         assert abs(diff - got) <= 1e-4 * max(1.0, abs(diff)), (which, idx, diff, got)
 
 
-def test_recurrence_repeats_bit_for_bit():
-    g, v, *_ = mix_inputs(2, 3000, 300, torch.bfloat16, True, True, False)
-    first = K.recurrence_forward(g, v)
-    for _ in range(3):
-        again = K.recurrence_forward(g, v)
+@pytest.mark.parametrize("n,length,d,starts", [(2, 3000, 300, True), (1, 60001, 43, False),
+                                               (9, 5000, 517, False)])
+def test_recurrence_repeats_bit_for_bit(n, length, d, starts):
+    """fp32, whose last bits would show an order that depends on timing."""
+    g, v, _, _, _, _, st, _ = mix_inputs(n, length, d, torch.float32, True, starts, False)
+    first = K.recurrence_forward(g, v, starts=st)
+    grads = K.recurrence_backward(g, v, first[0], first[0], starts=st)
+    for _ in range(4):
+        again = K.recurrence_forward(g, v, starts=st)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        for k, t in K.recurrence_backward(g, v, again[0], again[0], starts=st).items():
+            assert torch.equal(grads[k], t), k
 
 
 # ---- gated feed-forward block -------------------------------------------------------------------

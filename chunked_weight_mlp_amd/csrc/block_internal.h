@@ -81,9 +81,19 @@ hipError_t ff_forward(const FfArgs &a, hipStream_t st);
 template <typename T>
 hipError_t ff_backward(const FfArgs &a, hipStream_t st);
 
-// ---- small device helpers ------------------------------------------------------
+// ---- small helpers -------------------------------------------------------------
 #ifdef __HIPCC__
 namespace blk {
+
+// A grid of at least `blocks` blocks (a launch takes fewer than 2^32 threads along
+// an axis, and rows of a narrow tensor can be more), and a block's place in it.
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t x = blocks < 1 << 20 ? blocks : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ int64_t block_id() {
+  return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
 
 // N consecutive elements at the alignment of one: rows of odd width or stride
 // start anywhere, and the hardware's unaligned access mode serves a wide load

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
   constexpr int RB = 4 / WPR;  // rows per block
   constexpr int TPR = 64 * WPR;
   const int tr = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RB + threadIdx.x / TPR;
+  const int64_t row = blk::block_id() * RB + threadIdx.x / TPR;
   if (row >= a.n) return;  // whole rows: with WPR > 1 the block is one row
   const int d = a.d;
   const Cols<TPR, NP, W> cols(tr, d);
@@ -317,12 +317,11 @@ int bwd_waves(int d, int64_t n) {
 template <typename T, int WPR, int NP>
 hipError_t fwd_launch(const NormArgs &a, hipStream_t st) {
   constexpr int RB = 4 / WPR;
-  const unsigned grid = (unsigned)((a.n + RB - 1) / RB);
-  const dim3 block(256);
+  const dim3 grid = blk::grid_of((a.n + RB - 1) / RB), block(256);
   if (a.d % 8 == 0)
-    hipLaunchKernelGGL((k_norm_fwd<T, WPR, NP, true>), dim3(grid), block, 0, st, a);
+    hipLaunchKernelGGL((k_norm_fwd<T, WPR, NP, true>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((k_norm_fwd<T, WPR, NP, false>), dim3(grid), block, 0, st, a);
+    hipLaunchKernelGGL((k_norm_fwd<T, WPR, NP, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 template <typename T, int WPR, int NP>

@@ -332,7 +332,7 @@ __device__ __forceinline__ void store_at(T *row, uint32_t bytes, const float (&v
   *(Pack<T, V> *)((char *)row + bytes) = p;
 }
 
-// Where a block's tile is. `ord`: position in its chain (0 runs first).
+// Where a block's tile is. `ord`: position in its chain (0 runs first; nt: none).
 struct Tile {
   int n, cb;
   int64_t ord;
@@ -340,7 +340,7 @@ struct Tile {
 template <int V>
 __device__ __forceinline__ Tile next_tile(const RecArgs &a, int nt) {
   __shared__ unsigned ticket;
-  unsigned id = blockIdx.x;
+  unsigned id = (unsigned)blk::block_id();
   if (nt > 1) {
     if (threadIdx.x == 0)
       ticket = __hip_atomic_fetch_add((unsigned *)a.ws, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -376,6 +376,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   __shared__ float sA[NW][CH], sB[NW][CH], lA[2][NW * LB][CH], lB[2][NW * LB][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
+  if (tl.ord >= nt) return;
   const int lane = threadIdx.x & 63, n = tl.n;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t len = seq_length(a, n), t0 = tl.ord * TT;
@@ -511,6 +512,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
   __shared__ float sA[NW][CH], sB[NW][CH], lA[2][NW * LB][CH], lB[2][NW * LB][CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
+  if (tl.ord >= nt) return;
   const int lane = threadIdx.x & 63, n = tl.n;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t len = seq_length(a, n), tile = nt - 1 - tl.ord, t0 = tile * TT;
@@ -725,7 +727,7 @@ hipError_t rec_forward(const RecArgs &a, hipStream_t st) {
   const hipError_t e = clear_slots(a, nt, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_rec_fwd<T, kV, kFwdTokens, kWaves>),
-                     dim3((unsigned)(nt * a.n * channel_blocks(a.d))), dim3(64 * kWaves), 0, st, a,
+                     blk::grid_of(nt * a.n * channel_blocks(a.d)), dim3(64 * kWaves), 0, st, a,
                      (int)nt);
   return hipGetLastError();
 }
@@ -741,7 +743,7 @@ hipError_t rec_backward(const RecArgs &a, hipStream_t st) {
   const hipError_t e = clear_slots(a, nt, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_rec_bwd<T, kV, kBwdTokens, kWaves>),
-                     dim3((unsigned)(nt * a.n * channel_blocks(a.d))), dim3(64 * kWaves), 0, st, a,
+                     blk::grid_of(nt * a.n * channel_blocks(a.d)), dim3(64 * kWaves), 0, st, a,
                      (int)nt);
   return hipGetLastError();
 }

@@ -429,6 +429,45 @@ def test_ff_gradient_against_differences():
 # ---- large offsets, repeatability ---------------------------------------------------------------------
 
 
+def test_more_blocks_than_an_axis_takes():
+    """Narrow rows in numbers that, a few threads each, pass 2^32 threads in a line."""
+    n = (1 << 26) + 9
+    x = torch.empty((n, 3), dtype=torch.bfloat16, device=DEV).normal_()
+    op = K.Norm(torch.ones(3, dtype=torch.bfloat16, device=DEV), None)
+    y, _, mean, rstd = op.forward(x)
+    for at in (0, (1 << 22) - 7, (1 << 25) + 1, n - 5000):
+        part = slice(at, at + 5000)
+        yp, _, mp, rp = op.forward(x[part])
+        assert torch.equal(y[part], yp) and torch.equal(mean[part], mp) and torch.equal(rstd[part], rp)
+    del x, y, mean, rstd
+
+    batch, length = 65535, 128 * 128 + 3   # 129 tiles a sequence
+    g = torch.empty((batch, length, 1), dtype=torch.bfloat16, device=DEV).normal_().add_(3.0)
+    v = torch.empty_like(g).normal_()
+    h, last = K.recurrence_forward(g, v)
+    got = K.recurrence_backward(g, v, h, h)
+    for i in (0, 1, 31000, batch - 1):
+        one = slice(i, i + 1)
+        hp, lp = K.recurrence_forward(g[one], v[one])
+        assert torch.equal(h[one], hp) and torch.equal(last[one], lp)
+        for k, t in K.recurrence_backward(g[one], v[one], hp, hp).items():
+            assert torch.equal(got[k][one], t), (i, k)
+    del g, v, h, last, got
+
+    n = (1 << 20) + 77
+    W = [rand(s, i, torch.bfloat16, s[1] ** -0.5).to(DEV) for i, s in enumerate(((16, 8), (16, 8), (8, 16)))]
+    ff, x = K.FeedForward(*W), torch.empty((n, 8), dtype=torch.bfloat16, device=DEV).normal_()
+    y = ff.forward(x)
+    y20 = ff.forward(x[:1 << 20])
+    for at in (0, 500000, (1 << 20) - 3000, n - 3000):
+        part = slice(at, at + 3000)
+        want = ff.forward(x[part]).float().cpu().numpy()
+        # the same roundings (z, y to bf16) of sums in another order
+        assert rel_fro(y[part].float().cpu().numpy(), want) <= 4e-3, at
+        if part.stop <= 1 << 20:
+            assert rel_fro(y20[part].float().cpu().numpy(), want) <= 4e-3, at
+
+
 def test_norm_offsets_past_32_bits():
     """1.1 M rows of 2048: the last rows' results equal those of the rows alone."""
     n, d = 1100000, 2048

@@ -88,6 +88,20 @@ struct FfGroup {
   int start[G + 1];
 };
 
+// Lane l holds rows 4 (l / 16) .. + 3 of a 16-row tile at column l % 16. Swapping
+// lane groups of two tiles, one below the other, leaves each lane 8 consecutive
+// rows of its column: 8 (l / 32) + 16 (l / 16 % 2) and on.
+__device__ __forceinline__ void rows8(f32x4 a, f32x4 b, float (&v)[8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float x = a[r], y = b[r];
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
+                                                    __builtin_bit_cast(unsigned, y), false, false);
+    v[r] = __builtin_bit_cast(float, (unsigned)s[0]);
+    v[4 + r] = __builtin_bit_cast(float, (unsigned)s[1]);
+  }
+}
+
 template <class C, int NP, bool DUAL, class Epi, int G>
 __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_ff_gemm(
     FfGroup<Epi, G> grp) {
@@ -163,20 +177,7 @@ __global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::OCC)
         }
       },
       [](int) {}, [](int) {});
-  // Lane l holds rows 4 (l / 16) .. + 3 of a 16-row tile at column l % 16.
-  // Swapping lane groups of tiles i and i + 1 leaves each lane 8 consecutive
-  // rows: m .. m + 7 at column n.
   const int gq = lane >> 4;
-  const auto rows8 = [](f32x4 a, f32x4 b, float (&v)[8]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float x = a[r], y = b[r];
-      const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
-                                                      __builtin_bit_cast(unsigned, y), false, false);
-      v[r] = __builtin_bit_cast(float, (unsigned)s[0]);
-      v[4 + r] = __builtin_bit_cast(float, (unsigned)s[1]);
-    }
-  };
   const auto write = [&](auto tag) __attribute__((always_inline)) {
     constexpr bool FULL = decltype(tag)::value;
     constexpr int TURN = Epi::TURN, PT = 40;  // pitch of a turned tile's rows (32 values)
@@ -488,14 +489,15 @@ __global__ __launch_bounds__(256) void k_ff_zero(uint16_t *__restrict__ p, int64
     p[i] = 0;
 }
 
-// ---- few tokens -------------------------------------------------------------------------
-// Up to 64 tokens every weight is read once and little else moves, so the weights
+// ---- single tokens ----------------------------------------------------------------------
+// For up to 32 tokens every weight is read once and little else moves, so the weights
 // go straight from memory into MFMA operands: 16 bytes of a weight row per lane
 // are 8 bf16 values of one 16x16x32 MFMA, or 4 fp32 values of four 16x16x4 ones
 // (any assignment of K values to lanes gives the same sum as long as both operands
 // share it). The MFMA's 16 operand rows would be 16 weight rows, whose 16-byte
 // pieces lie a row apart: 64 cache lines a load, and the loads' address work, not
-// memory, sets the time (n = 16: 46 us, 64: 95). So an operand row is a weight row
+// memory, sets the time (n = 16: 46 us so, 27 as here, 2048 x 8192 in bf16). So an
+// operand row is a weight row
 // i and one of KF neighbouring pieces of K, s: rows i KF + s, and columns j KF + s
 // of the other operand for token j. Lanes next to each other then read pieces
 // next to each other; of the products, those whose two s agree are summed.
@@ -503,6 +505,7 @@ __global__ __launch_bounds__(256) void k_ff_zero(uint16_t *__restrict__ p, int64
 // product), so that the tokens' operands serve several weight rows; its WV waves
 // take interleaved steps of K and meet in LDS. NT: groups of 16 / KF tokens.
 
+typedef unsigned U32x4 __attribute__((ext_vector_type(4)));
 template <typename T>
 struct Quad;  // 16 bytes of one operand row
 template <>
@@ -510,6 +513,11 @@ struct Quad<__bf16> {
   static constexpr int E = 8;
   bf16x8 v;
   __device__ __forceinline__ void set(int e, float x) { v[e] = (__bf16)x; }
+  __device__ __forceinline__ void keep(int e, bool k) {  // zero a value unless k
+    U32x4 w = __builtin_bit_cast(U32x4, v);
+    w[e >> 1] &= k ? 0xffffffff : e & 1 ? 0xffff : 0xffff0000;
+    v = __builtin_bit_cast(bf16x8, w);
+  }
   __device__ static __forceinline__ f32x4 mma(const Quad &a, const Quad &b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
   }
@@ -519,6 +527,7 @@ struct Quad<float> {
   static constexpr int E = 4;
   f32x4 v;
   __device__ __forceinline__ void set(int e, float x) { v[e] = x; }
+  __device__ __forceinline__ void keep(int e, bool k) { v[e] = k ? v[e] : 0.f; }
   __device__ static __forceinline__ f32x4 mma(const Quad &a, const Quad &b, f32x4 c) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
@@ -543,14 +552,14 @@ __device__ __forceinline__ Quad<T> quad_end(const T *row, int k, int end) {
 
 // DUAL: out = SiLU(W x) (W2 x), with W x and W2 x saved to a, u when given.
 // Otherwise out = W x. W [M][K] dense, x rows x_ld apart, out rows out_ld apart.
-template <typename T, int NT, int RG, int WV, int KF, bool DUAL>
+template <typename T, int NT, int RG, int WV, bool DUAL>
 __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
                                                       const T *__restrict__ w2,
                                                       const T *__restrict__ x, int64_t x_ld, int n,
                                                       int M, int K, T *__restrict__ out,
                                                       int64_t out_ld, float *__restrict__ a,
                                                       float *__restrict__ u) {
-  constexpr int RB = 16 / KF;  // weight rows, tokens of a group
+  constexpr int KF = 4, RB = 16 / KF;  // weight rows, tokens of a group
   constexpr int D = DUAL ? 2 : 1;
   constexpr int E = Quad<T>::E, S = 4 * KF * E;  // K values of a lane, of a step
   // steps whose loads go together: about 8 KB of weights a wave, fewer where the
@@ -561,14 +570,6 @@ __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m0 = RG * RB * blockIdx.x;
-  const int first = NT * RB * blockIdx.y;  // this block's tokens
-  n -= first;
-  x += first * x_ld;
-  out += first * out_ld;
-  if (a) {
-    a += (int64_t)first * M;
-    u += (int64_t)first * M;
-  }
   const int r = lane & 15, kl = E * (r % KF + KF * (lane >> 4));
   const T *wrow[D][RG], *xrow[NT];
 #pragma unroll
@@ -679,22 +680,6 @@ __global__ __launch_bounds__(64 * WV) void k_ff_small(const T *__restrict__ w,
   }
 }
 
-// Whether a call streams its weights (k_ff_small, whose blocks of 64 tokens each
-// read them again, from L2 when they are few) or runs on tiles. Streaming costs
-// in proportion to n d F and has two launches; tiles take more, but more work at
-// a time. Both sides measured (us, streaming / tiles), bf16: 256 x 1024 at 512
-// tokens 15.9 / 16.6, at 1024 23 / 17; 512 x 2048 at 256 19.2 / 19.4; 1024 x 4096 at
-// 64 20.7 / 23.4, at 200 41 / 27; 2560 x 9728 at 16 47 / 70, at 32 77 / 70. Rows of odd
-// width: 250 x 671 at 400 20.6 / 20.6, at 1024 34 / 21; 1999 x 3001 at 32 31 / 53. fp32,
-// whose tiles do six times the work: 512 x 2048 at 256 50 / 57, at 400 76 / 62; 1024 x
-// 4096 at 128 81 / 105, at 200 148 / 113.
-bool few_tokens(int elem, int d, int F, int64_t n) {
-  if (n <= 16) return true;
-  const bool odd = d % 8 || F % 8;
-  const int64_t most = elem == 4 ? 1 << 29 : odd && n > 64 ? 1 << 26 : 1 << 28;
-  return n <= most / ((int64_t)d * F);
-}
-
 // Row groups of a block of four waves: two where that makes two blocks a CU, else
 // one (2560 x 9728, one token: 29 us with 2 groups in the first product and 1 in
 // the second, 31 with 4 and 1, 32 with 4 and 2; with eight waves 34).
@@ -702,22 +687,18 @@ template <typename T, bool DUAL>
 hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n, int M, int K, T *out,
                         int64_t out_ld, float *a, float *u, hipStream_t st) {
   constexpr int WV = 4;
-#define SMALL(NT, RG, KF)                                                                       \
-  hipLaunchKernelGGL((k_ff_small<T, NT, RG, WV, KF, DUAL>),                                     \
-                     dim3((M + RG * (16 / KF) - 1) / (RG * (16 / KF)),                        \
-                          (n + NT * (16 / KF) - 1) / (NT * (16 / KF))),                        \
+#define SMALL(NT, RG)                                                                     \
+  hipLaunchKernelGGL((k_ff_small<T, NT, RG, WV, DUAL>), dim3((M + RG * 4 - 1) / (RG * 4)), \
                      dim3(64 * WV), 0, st, w, w2, x, x_ld, n, M, K, out, out_ld, a, u)
 #define SMALL_TOKENS(RG) \
   if (n <= 4)            \
-    SMALL(1, RG, 4);     \
+    SMALL(1, RG);        \
   else if (n <= 8)       \
-    SMALL(2, RG, 4);     \
+    SMALL(2, RG);        \
   else if (n <= 16)      \
-    SMALL(4, RG, 4);     \
-  else if (n <= 32)      \
-    SMALL(8, RG, 4);     \
+    SMALL(4, RG);        \
   else                   \
-    SMALL(8, RG, 2)
+    SMALL(8, RG)
   if (M >= 16 * 2 * 256) {
     SMALL_TOKENS(2);
   } else {
@@ -727,6 +708,269 @@ hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n
 #undef SMALL
   return hipGetLastError();
 }
+
+// ---- few tokens ---------------------------------------------------------------------------
+// With few tokens the operands' layout passes and the 64-wide padded steps cost more
+// than the products. Here a product takes its operands as they lie, of either
+// orientation and any type, stride and width, turns them on their way into LDS and
+// uses the MFMA of their own type (fp32: no planes), in 64 x 64 tiles of which many
+// fit a small matrix. 128 bytes of K a step, two steps' loads in flight in registers
+// while a third is in LDS. Bound by the steps' latency, or by the weights' traffic.
+
+// One operand: element (row, k) is p[row ld + k], or, turned, p[k ld + row]; the second
+// of two runs of K continues in p2.
+template <typename T>
+struct FfSide {
+  const T *p, *p2;
+  int64_t ld;
+};
+template <typename T>
+struct FfDirect {  // out(m, n) = sum over the runs and k of a(m, k) b(n, k)
+  FfSide<T> a, b;
+  bool b_turned;
+  int M, N, K, runs;
+  int splits;
+};
+template <typename T, class Epi, int G>
+struct FfDirects {
+  FfDirect<T> prob[G];
+  Epi epi[G];
+  int start[G + 1];
+};
+constexpr int kDTile = 64;
+template <typename T>
+constexpr int kDStep = 128 / sizeof(T);  // K values of a step
+
+// A side's 64 rows x 128 bytes of K in LDS: the 16-byte piece q of row r is stored at
+// piece q ^ r ^ r / 8, so that neither 16 rows' reads of a piece nor the turned
+// operand's writes, 8 rows apart, meet in a bank.
+__device__ __forceinline__ int dslot(int r, int q) { return r * 8 + (q ^ ((r ^ (r >> 3)) & 7)); }
+
+// A thread's part of a step of one side: two pieces, of E values of K of a row each, or
+// turned, of E rows at a value of K each. No load branches or reaches over its row: a
+// piece at the end moves back. Rows are then stored where they belong (a neighbour's,
+// with the same values, once more); of K, the values the piece before holds are zeroed,
+// on both sides of the product. A pair: 32 rows of p, then the same 32 of p2.
+template <typename T, bool turned, bool pair = false>
+struct DirectLoader {
+  static constexpr int E = Quad<T>::E, S = kDStep<T>;
+  const T *p, *p2;
+  int64_t at[2];  // of its rows
+  int64_t ks;     // distance between values of K
+  int row[2];     // in the tile
+  int pos;        // its place in the step (the first of turned values)
+  // the place in the step of piece i
+  __device__ __forceinline__ int place(int i) const { return turned ? pos + (E == 8 ? i : 16 * i) : pos; }
+  __device__ __forceinline__ DirectLoader(const FfSide<T> &s, int r0, int R) : p(s.p), p2(s.p2) {
+    const int tid = threadIdx.x;
+    ks = turned ? s.ld : 1;
+    pos = turned ? (E == 8 ? 2 * (tid >> 3) : tid >> 4) : E * (tid & 7);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = turned ? min(r0 + E * (tid & (64 / E - 1)), R - E)
+                           : min(r0 + (tid >> 3) + (pair ? 0 : 32 * i), R - 1);
+      at[i] = turned ? r : r * s.ld;
+      // (rows before the tile go to its end, past the matrix's last)
+      row[i] = turned ? r - r0 : (tid >> 3) + 32 * i;
+    }
+  }
+  // where piece i's value (turned) or first value of K is, of a step from k0 on
+  __device__ __forceinline__ int first_k(int i, int k0, int K) const {
+    const int p = place(i), in = p & (E - 1);
+    return min(min(k0 + p - in, max(K - E, 0)) + in, K - 1);
+  }
+  __device__ __forceinline__ void load(Quad<T> (&q)[2], bool second, int k0, int K) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      q[i] = quad_at<T>(((pair ? i == 1 : second) ? p2 : p) + at[i] + first_k(i, k0, K) * ks);
+  }
+  __device__ __forceinline__ void store(Quad<T> (&q)[2], Quad<T> *lds, int k0, int K) const {
+    if (k0 + S > K) {  // the last step
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = place(i), in = p & (E - 1), from = k0 + p - in, at0 = min(from, max(K - E, 0));
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int k = at0 + (turned ? in : e);
+          q[i].keep(e, k >= from && k < K);
+        }
+      }
+    }
+    if constexpr (!turned) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lds[dslot(row[i], pos / E)] = q[i];
+    } else if constexpr (E == 8) {
+      const U32x4 lo = __builtin_bit_cast(U32x4, q[0]), hi = __builtin_bit_cast(U32x4, q[1]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // the e-th halves of both
+        const unsigned h = hi[e >> 1], l = lo[e >> 1];
+        ((unsigned *)(lds + dslot((row[0] + e) & (kDTile - 1), pos >> 3)))[(pos & 7) >> 1] =
+            __builtin_amdgcn_perm(h, l, e & 1 ? 0x07060302 : 0x05040100);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          ((float *)(lds + dslot((row[i] + e) & (kDTile - 1), place(i) >> 2)))[pos & 3] = q[i].v[e];
+    }
+  }
+};
+
+// TURNED: a is (b where its problem says so). DUAL: two products of 32 rows each, of a.p
+// and a.p2, for one epilogue.
+template <typename T, bool TURNED, bool DUAL, class Epi, int G>
+__global__ __launch_bounds__(256) void k_ff_direct(FfDirects<T, Epi, G> grp) {
+  constexpr int S = kDStep<T>, AHEAD = 2, MT = DUAL ? kDTile / 2 : kDTile;
+  __shared__ Quad<T> lds[2][2][kDTile * 8];
+  int which = 0;
+#pragma unroll
+  for (int p = 1; p < G; ++p) which += (int)blockIdx.x >= grp.start[p];
+  const FfDirect<T> g = grp.prob[which];
+  const Epi epi = grp.epi[which];
+  const int nm = (g.M + MT - 1) / MT, nn = (g.N + kDTile - 1) / kDTile;
+  const int blocks = nm * nn * g.splits, bid = blockIdx.x - grp.start[which];
+  if (bid >= blocks) return;
+  const int id = xcd_remap(bid, blocks), sp = id / (nm * nn);
+  int tm, tn;
+  tile_of<8>(id % (nm * nn), nm, nn, tm, tn);
+  const int m0 = tm * MT, n0 = tn * kDTile;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = 32 * (wave & 1), gq = lane >> 4, lr = lane & 15;
+  const int wm = (DUAL ? 16 : 32) * (wave >> 1), wi = DUAL ? 32 : 16;  // its rows: 16 each from wm, wm + wi
+  const int per_run = (g.K + S - 1) / S, steps = g.runs * per_run;
+  const int per = (steps + g.splits - 1) / g.splits, first = sp * per, count = min(per, steps - first);
+  f32x4 acc[2][2] = {};
+  const auto run = [&](auto tag) __attribute__((always_inline)) {
+    const DirectLoader<T, TURNED, DUAL> la(g.a, m0, g.M);
+    const DirectLoader<T, decltype(tag)::value> lb(g.b, n0, g.N);
+    Quad<T> qa[AHEAD][2], qb[AHEAD][2];
+    const auto fetch = [&](int s, int j) __attribute__((always_inline)) {
+      const bool second = first + s >= per_run;
+      const int k0 = S * (first + s - (second ? per_run : 0));
+      la.load(qa[j], second, k0, g.K);
+      lb.load(qb[j], second, k0, g.K);
+    };
+    // Step s, whose loads are in set j. Of the two stages in LDS it fills the one whose
+    // reads, two steps ago, every wave has behind it at the last step's barrier.
+    const auto step = [&](int s, int j, bool more) __attribute__((always_inline)) {
+      Quad<T> *const as = lds[j][0], *const bs = lds[j][1];
+      const int k0 = S * (first + s - (first + s >= per_run ? per_run : 0));
+      la.store(qa[j], as, k0, g.K);
+      lb.store(qb[j], bs, k0, g.K);
+      if (more) fetch(s + AHEAD, j);
+      lds_barrier();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        Quad<T> a[2], b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a[i] = as[dslot(wm + wi * i + lr, 4 * u + gq)];
+          b[i] = bs[dslot(wn + 16 * i + lr, 4 * u + gq)];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) acc[i][k] = Quad<T>::mma(a[i], b[k], acc[i][k]);
+      }
+    };
+    fetch(0, 0);
+    fetch(min(1, count - 1), 1);
+    int s = 0;
+    for (; s + 2 * AHEAD <= count; s += AHEAD) {  // straight: waits count the loads in flight
+      step(s, 0, true);
+      step(s + 1, 1, true);
+    }
+    step(s, 0, s + 2 < count);
+    if (s + 1 < count) step(s + 1, 1, false);
+    if (s + 2 < count) step(s + 2, 0, false);
+  };
+  if (G > 1 && g.b_turned)
+    run(std::true_type());
+  else
+    run(std::false_type());
+  if constexpr (DUAL) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int n = n0 + wn + 16 * j + lr;
+      if (n < g.N) epi.store(m0 + wm + 4 * gq, n, acc[0][j], acc[1][j]);
+    }
+  } else {
+    const int m = m0 + wm + 8 * (gq >> 1) + 16 * (gq & 1);
+    typename Epi::In in[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      in[j] = epi.template load<false>(m, min(n0 + wn + 16 * j + lr, g.N - 1));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int n = n0 + wn + 16 * j + lr;
+      float v[8];
+      rows8(acc[0][j], acc[1][j], v);
+      if (n < g.N) epi.template store<false>(m, n, v, in[j], sp, nullptr);
+    }
+  }
+}
+
+// z = SiLU(a) u, and a and u when saved, for 4 features m .. m + 3 of token n
+template <typename T>
+struct EpiZDirect {
+  T *z;
+  float *a, *u;
+  int F;
+  template <typename O>
+  __device__ void put(O *row, int m, f32x4 v) const {
+    if (m + 4 <= F) {
+      const float w[4] = {v[0], v[1], v[2], v[3]};
+      blk::store_pack<O, 4>(row + m, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < F) row[m + e] = (O)v[e];
+    }
+  }
+  __device__ void store(int m, int n, f32x4 av, f32x4 uv) const {
+    const int64_t row = (int64_t)n * F;
+    f32x4 zv;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) zv[e] = av[e] * fast_sigmoid(av[e]) * uv[e];
+    put(z + row, m, zv);
+    if (a) {
+      put(a + row, m, av);
+      put(u + row, m, uv);
+    }
+  }
+};
+
+// dz -> dA, dU and z by token, as they are.
+template <typename T>
+struct EpiDzDirect {
+  struct In {
+    Pack<float, 8> a, u;
+  };
+  const float *a, *u;
+  T *da, *du, *z;
+  int F;
+  template <bool FULL>
+  __device__ In load(int m, int n) const {
+    return {pack8<float, FULL>(a + (int64_t)n * F, m, F), pack8<float, FULL>(u + (int64_t)n * F, m, F)};
+  }
+  template <bool FULL>
+  __device__ void store(int m, int n, const float (&v)[8], const In &in, int, bf16x8 *) const {
+    float av[8], uv[8], zv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = in.a.v[e], y = in.u.v[e];
+      const float s = fast_sigmoid(x), h = x * s;
+      av[e] = v[e] * y * (s + h * (1.f - s));
+      uv[e] = v[e] * h;
+      zv[e] = h * y;
+    }
+    const int64_t row = (int64_t)n * F;
+    store8<T, FULL>(da + row, m, F, av);
+    store8<T, FULL>(du + row, m, F, uv);
+    store8<T, FULL>(z + row, m, F, zv);
+  }
+};
 
 // ---- launches ------------------------------------------------------------------------------
 
@@ -776,6 +1020,23 @@ int64_t part_bytes(const FfProb &g, int parts) {
   return parts > 1 ? 4 * (int64_t)parts * g.N * round_up(g.M, 8) : 0;
 }
 
+// Adds up the parts of the products that were split.
+template <typename T, int G, class Group>
+hipError_t joins(const Group &grp, hipStream_t st) {
+  FfJoins<T, G> js{};
+  int used = 0;
+  int64_t most = 0;
+  for (int p = 0; p < G; ++p)
+    if (grp.prob[p].splits > 1) {
+      js.j[used++] = {grp.epi[p], grp.prob[p].splits, grp.prob[p].N};
+      most = std::max(most, grp.epi[p].part_stride / 8);
+    }
+  if (used == 0) return hipSuccess;
+  hipLaunchKernelGGL((k_ff_join<T, G>), dim3((unsigned)std::min<int64_t>(ceil_div(most, 256), 2048), used),
+                     dim3(256), 0, st, js);
+  return hipGetLastError();
+}
+
 // Up to G independent products written out, each split over K by its `splits`
 // (its partial sums then in epi.part), and the joins.
 template <typename T, int G>
@@ -790,19 +1051,8 @@ hipError_t products_out(FfGroup<EpiOut<T>, G> grp, hipStream_t st) {
     split = split || e.part;
   }
   if (!split && use_big(grp, false)) return launch_tiles<FfBig, NP, false>(grp, st);
-  hipError_t err = launch_tiles<FfMid, NP, false>(grp, st);
-  if (err != hipSuccess || !split) return err;
-  FfJoins<T, G> js{};
-  int used = 0;
-  int64_t most = 0;
-  for (int p = 0; p < G; ++p)
-    if (grp.prob[p].splits > 1) {
-      js.j[used++] = {grp.epi[p], grp.prob[p].splits, grp.prob[p].N};
-      most = std::max(most, grp.epi[p].part_stride / 8);
-    }
-  hipLaunchKernelGGL((k_ff_join<T, G>), dim3((unsigned)std::min<int64_t>(ceil_div(most, 256), 2048), used),
-                     dim3(256), 0, st, js);
-  return hipGetLastError();
+  const hipError_t err = launch_tiles<FfMid, NP, false>(grp, st);
+  return err != hipSuccess || !split ? err : joins<T, G>(grp, st);
 }
 
 // One product with an epilogue of its own.
@@ -919,6 +1169,143 @@ struct BwdPlan {
   }
 };
 
+// Whether a forward streams its weights (k_ff_small). Measured against the operands as
+// they lie below (us, streaming / that), fp32: 512 x 2048 at 8 tokens 13 / 26, at 32 20 / 27;
+// 1024 x 4096 at 16 26 / 45, at 24 50 / 45; 2048 x 8192 at 8 53 / 79, at 16 82 / 78. bf16:
+// 1024 x 4096 at 32 17 / 20; 2048 x 8192 at 16 27 / 29, at 24 42 / 29; 1999 x 3001 at 8
+// 17 / 27, at 16 33 / 27, at 32 32 / 28.
+bool single_tokens(int elem, int d, int F, int64_t n) {
+  return n <= 16 || (n <= 32 && n * d * F * elem <= 1 << 28);
+}
+// Whether it takes its operands as they lie (k_ff_direct), or has those that need it laid
+// out for the large tiles' kernel: whose time that pass is with few tokens. Both sides
+// measured (us, direct / laid out), fp32: 250 x 671 at 333 tokens 20 / 39, at 2048 39 / 43; 512
+// x 2048 at 512 46 / 64, at 2048 130 / 112; 1024 x 4096 at 64 44 / 102, at 512 123 / 128, at
+// 1024 228 / 194; 2048 x 8192 at 64 78 / 294, at 512 439 / 430. bf16: 1999 x 3001 at 64 28 /
+// 55, at 512 60 / 66, at 1024 102 / 83; whole steps of K: 256 x 1024 at 1024 15 / 18, at 2048
+// 20 / 20; 512 x 2048 at 333 19 / 21, at 1024 27 / 24; 1024 x 4096 at 128 23 / 27, at 333 31 /
+// 29; 2048 x 8192 at 64 29 / 39, at 128 37 / 44, at 200 57 / 50.
+bool few_forward(int elem, int d, int F, int64_t n) {
+  if (d < 8 || F < 8) return false;  // pieces of 8 values along a row
+  return n <= (elem == 4 || d % kStep || F % kStep ? 512 : 128) || n * d * F <= 1 << 29;
+}
+// The same for a backward, whose operands all need laying out. Measured (us, direct / laid out), fp32: 250 x 671 at
+// 333 tokens 33 / 59, at 2048 71 / 108; 512 x 2048 at 1024 138 / 175; 1024 x 4096 at 64
+// 76 / 140, at 512 241 / 283, at 1024 449 / 428; 2048 x 8192 at 64 186 / 421, at 512 924 /
+// 842. bf16: 250 x 671 at 2048 38 / 41; 512 x 2048 at 1024 51 / 57; 1024 x 4096 at 64 41 /
+// 53, at 512 70 / 75, at 1024 121 / 112; 2048 x 8192 at 64 76 / 135, at 200 133 / 155, at
+// 512 232 / 203; 1999 x 3001, where 16 bytes start at any element, at 64 61 / 80, at 333
+// 107 / 107, at 512 127 / 117.
+bool few_backward(int elem, int d, int F, int64_t n) {
+  if (d < 8 || F < 8) return false;  // pieces of 8 values along a row
+  const int64_t unit = (int64_t)1 << 30;
+  const int64_t most = elem == 4 ? 4 * unit - 1 : d % 8 || F % 8 ? 2 * unit : 3 * unit;
+  return n <= most / ((int64_t)d * F);
+}
+int direct_parts(int64_t tiles, int64_t steps) {
+  const int64_t s = std::min<int64_t>({2 * kCUs / std::max<int64_t>(tiles, 1), steps / 4, 64});
+  if (s < 2) return 1;
+  return (int)ceil_div(steps, ceil_div(steps, s));  // no empty part
+}
+// A product out of the direct kernel: its sizes and parts, and where those go.
+template <typename T>
+FfDirect<T> direct_product(Area &w, int M, int N, int K, int runs, float *&part) {
+  FfDirect<T> g{};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.runs = runs;
+  g.splits = direct_parts(ceil_div(M, kDTile) * ceil_div(N, kDTile), runs * ceil_div(K, kDStep<T>));
+  part = g.splits > 1 ? (float *)w.take(4 * (int64_t)g.splits * N * round_up(M, 8)) : nullptr;
+  return g;
+}
+template <typename T>
+EpiOut<T> direct_out(const FfDirect<T> &g, float *part, void *to, int64_t ld) {
+  const int64_t pl = round_up(g.M, 8);
+  return {(T *)to, nullptr, ld, g.M, g.N, 1 << 30, part, g.N * pl, pl};
+}
+template <typename T>
+struct DirectFwd {
+  T *z;
+  FfDirect<T> out;
+  float *part;
+  size_t bytes;
+  DirectFwd(void *base, int d, int F, int n) {
+    Area w{(char *)base};
+    z = (T *)w.take((int64_t)n * F * (int64_t)sizeof(T));
+    out = direct_product<T>(w, d, n, F, 1, part);
+    bytes = w.off;
+  }
+};
+template <typename T>
+struct DirectBwd {
+  T *da, *du, *z;
+  FfDirect<T> out[4];  // dx, dW_g, dW_u, dW_d
+  float *part[4];
+  size_t bytes;
+  DirectBwd(void *base, int d, int F, int n) {
+    Area w{(char *)base};
+    for (T **p : {&da, &du, &z}) *p = (T *)w.take((int64_t)n * F * (int64_t)sizeof(T));
+    out[0] = direct_product<T>(w, d, n, F, 2, part[0]);
+    out[1] = direct_product<T>(w, d, F, n, 1, part[1]);
+    out[2] = direct_product<T>(w, d, F, n, 1, part[2]);
+    out[3] = direct_product<T>(w, F, d, n, 1, part[3]);
+    bytes = w.off;
+  }
+};
+
+template <typename T, bool TURNED, bool DUAL, class Epi, int G>
+hipError_t launch_direct(FfDirects<T, Epi, G> grp, hipStream_t st) {
+  int at = 0;
+  for (int p = 0; p < G; ++p) {
+    const FfDirect<T> &g = grp.prob[p];
+    grp.start[p] = at;
+    at += (int)round_up(ceil_div(g.M, DUAL ? kDTile / 2 : kDTile) * ceil_div(g.N, kDTile) * g.splits, 8);
+  }
+  grp.start[G] = at;
+  hipLaunchKernelGGL((k_ff_direct<T, TURNED, DUAL, Epi, G>), dim3((unsigned)at), dim3(256), 0, st, grp);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t forward_direct(const FfArgs &p, hipStream_t st) {
+  const int d = p.d, F = p.F, n = (int)p.n;
+  const DirectFwd<T> w(p.ws, d, F, n);
+  const FfDirect<T> q{{(const T *)p.w_gate, (const T *)p.w_up, d}, {(const T *)p.x, nullptr, p.x_stride},
+                      false, F, n, d, 1, 1};
+  TRYH((launch_direct<T, false, true, EpiZDirect<T>, 1>({{q}, {EpiZDirect<T>{w.z, p.a, p.u, F}}, {}}, st)));
+  FfDirects<T, EpiOut<T>, 1> g{{w.out}, {direct_out(w.out, w.part, p.y, p.y_stride)}, {}};
+  g.prob[0].a = {(const T *)p.w_down, nullptr, F};
+  g.prob[0].b = {w.z, nullptr, F};
+  TRYH((launch_direct<T, false, false, EpiOut<T>, 1>(g, st)));
+  return joins<T, 1>(g, st);
+}
+
+template <typename T>
+hipError_t backward_direct(const FfArgs &p, hipStream_t st) {
+  const int d = p.d, F = p.F, n = (int)p.n;
+  const DirectBwd<T> w(p.ws, d, F, n);
+  const T *x = (const T *)p.x, *dy = (const T *)p.dy, *wd = (const T *)p.w_down;
+  // dz(f, t) = sum_c W_d(c, f) dy(t, c), and from it dA, dU and z
+  const FfDirect<T> dz{{wd, nullptr, F}, {dy, nullptr, p.dy_stride}, false, F, n, d, 1, 1};
+  TRYH((launch_direct<T, true, false, EpiDzDirect<T>, 1>(
+      {{dz}, {EpiDzDirect<T>{p.a, p.u, w.da, w.du, w.z, F}}, {}}, st)));
+  FfDirects<T, EpiOut<T>, 4> g{};
+  const auto out = [&](int k, FfSide<T> a, FfSide<T> b, void *to, int64_t ld) {
+    g.prob[k] = w.out[k];
+    g.prob[k].a = a;
+    g.prob[k].b = b;
+    g.prob[k].b_turned = k > 0;
+    g.epi[k] = direct_out(w.out[k], w.part[k], to, ld);
+  };
+  out(0, {(const T *)p.w_gate, (const T *)p.w_up, d}, {w.da, w.du, F}, p.dx, p.dx_stride);
+  out(1, {x, nullptr, p.x_stride}, {w.da, nullptr, F}, p.dw_gate, d);
+  out(2, {x, nullptr, p.x_stride}, {w.du, nullptr, F}, p.dw_up, d);
+  out(3, {w.z, nullptr, F}, {dy, nullptr, p.dy_stride}, p.dw_down, F);
+  TRYH((launch_direct<T, true, false, EpiOut<T>, 4>(g, st)));
+  return joins<T, 4>(g, st);
+}
+
 FfProb with_operands(FfProb g, const Opnd &a, const Opnd &b) {
   g.a = a.p;
   g.lda = a.ld;
@@ -935,10 +1322,15 @@ FfProb with_operands(FfProb g, const Opnd &a, const Opnd &b) {
 using namespace mfma;
 
 size_t ff_forward_workspace(int elem, int d, int F, int64_t n) {
-  if (few_tokens(elem, d, F, n)) return (size_t)round_up(std::max<int64_t>(n, 1) * F * elem, 256);
+  if (single_tokens(elem, d, F, n)) return (size_t)round_up(std::max<int64_t>(n, 1) * F * elem, 256);
+  if (few_forward(elem, d, F, n))
+    return elem == 2 ? DirectFwd<__bf16>(nullptr, d, F, (int)n).bytes : DirectFwd<float>(nullptr, d, F, (int)n).bytes;
   return FwdPlan(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes;
 }
 size_t ff_backward_workspace(int elem, int d, int F, int64_t n) {
+  if (few_backward(elem, d, F, n))
+    return std::max<size_t>(256, elem == 2 ? DirectBwd<__bf16>(nullptr, d, F, (int)n).bytes
+                                           : DirectBwd<float>(nullptr, d, F, (int)n).bytes);
   return std::max<size_t>(256, BwdPlan(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes);
 }
 
@@ -946,12 +1338,13 @@ template <typename T>
 hipError_t ff_forward(const FfArgs &p, hipStream_t st) {
   const int d = p.d, F = p.F, n = (int)p.n;
   const T *wg = (const T *)p.w_gate, *wu = (const T *)p.w_up, *wd = (const T *)p.w_down;
-  if (few_tokens((int)sizeof(T), d, F, n)) {
+  if (single_tokens((int)sizeof(T), d, F, n)) {
     T *z = (T *)p.ws;
     TRYH((launch_small<T, true>(wg, wu, (const T *)p.x, p.x_stride, n, F, d, z, F, p.a, p.u, st)));
     return launch_small<T, false>(wd, nullptr, z, F, n, d, F, (T *)p.y, p.y_stride, nullptr, nullptr,
                                   st);
   }
+  if (few_forward((int)sizeof(T), d, F, n)) return forward_direct<T>(p, st);
   constexpr int NP = planes_of<T>();
   const FwdPlan w(p.ws, NP, d, F, n);
   const int64_t Fp = kpad(F);
@@ -979,6 +1372,7 @@ hipError_t ff_backward(const FfArgs &p, hipStream_t st) {
                          dim3(256), 0, st, (uint16_t *)w, halves);
     return hipGetLastError();
   }
+  if (few_backward((int)sizeof(T), d, F, n)) return backward_direct<T>(p, st);
   constexpr int NP = planes_of<T>();
   const BwdPlan w(p.ws, NP, d, F, n);
   const int64_t dp = kpad(d), Fp = kpad(F), Tp = kpad(n);

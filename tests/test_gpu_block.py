@@ -330,8 +330,17 @@ FF_SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n,d,f,pad", FF_SHAPES)
+# Pieces of 8 and 4 values, steps of 64 and 32 and tiles of 64 and 32 that end early in
+# every operand; fewer values than a piece holds; both sides of the kernels' ranges.
+FF_SHAPES += [
+    (1, 8, 8, 0), (2, 9, 15, 3), (5, 31, 33, 1), (7, 63, 65, 0), (17, 8, 9, 0), (33, 71, 8, 0),
+    (40, 65, 127, 3), (66, 129, 71, 0), (100, 1000, 24, 8), (64, 1023, 1025, 1), (321, 40, 4096, 0),
+    (20, 5, 300, 0), (100, 300, 6, 0), (600, 901, 1100, 1), (1100, 1001, 2003, 3),
+]
+
+
+@pytest.mark.parametrize("dtype,n,d,f,pad", [(t, *s) for s in FF_SHAPES for t in ("bf16", "f32")]
+                         + [("f32", 1100, 2000, 2001, 0)])
 def test_ff(dtype, n, d, f, pad):
     t = TYPES[dtype]
     ws = ff_weights(d, f, t)

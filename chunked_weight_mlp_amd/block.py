@@ -310,14 +310,16 @@ class Norm:
         for name, t in (("mean", mean), ("rstd", rstd)):
             if t.numel() != n:
                 raise _invalid(f"{name} has {t.numel()} values, expected {n}")
-            _dense(name, t, t.shape, torch.float32, dev)
+            if t.dtype is not torch.float32 or t.device != dev or not t.is_contiguous():
+                _dense(name, t, t.shape, torch.float32, dev)
         dx = torch.empty_like(h, memory_format=_DENSE)
         dgamma = torch.empty(d, dtype=torch.float32, device=dev)
         dbeta = torch.empty(d, dtype=torch.float32, device=dev)
-        need = ipttt_norm_backward_workspace_bytes(self.desc, n)
+        need = load().ipttt_norm_backward_workspace_bytes(self._ref, n)
         ws = _temp(need, dev, stream)
-        ipttt_norm_backward(self.desc, h, hs, mean, rstd, dy, ds, dh, hh, n, dx, dgamma, dbeta, ws,
-                            need, st)
+        _check(load().ipttt_norm_backward(self._ref, h.data_ptr(), hs, mean.data_ptr(), rstd.data_ptr(),
+                                          dy.data_ptr(), ds, _p(dh), hh, n, dx.data_ptr(),
+                                          dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), need, st))
         if stream is not None:
             _used_on(stream, h, mean, rstd, dy, dh, dx, dgamma, dbeta, self.gamma)
         return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
@@ -366,9 +368,10 @@ def recurrence_forward(g, v, h0=None, starts=None, lens=None, stream=None):
     h = torch.empty_like(g, memory_format=_DENSE)
     r = _recurrence(g, v, h, h0, starts, lens)
     last = torch.empty((r.batch, r.d), dtype=torch.float32, device=dev)
-    need = ipttt_recurrence_workspace_bytes(r)
+    ref = ctypes.byref(r)
+    need = load().ipttt_recurrence_workspace_bytes(ref)
     ws = _temp(need, dev, stream)
-    ipttt_recurrence_forward(r, last, ws, need, st)
+    _check(load().ipttt_recurrence_forward(ref, last.data_ptr(), ws.data_ptr(), need, st))
     if stream is not None:
         _used_on(stream, g, v, h0, starts, lens, h, last)
     return h, last
@@ -409,11 +412,13 @@ def recurrence_backward(g, v, h, dh, h0=None, dh_last=None, starts=None, lens=No
     dh0 = torch.empty((r.batch, r.d), dtype=torch.float32, device=dev)
     if dh_last is not None:
         _dense("dh_last", dh_last, (r.batch, r.d), torch.float32, dev)
-    need = ipttt_recurrence_workspace_bytes(r)
+    views = [ctypes.byref(View(*_strides(name, t, shape, dtype, dev)))
+             for name, t in (("dh", dh), ("dg", dg), ("dv", dv))]
+    ref = ctypes.byref(r)
+    need = load().ipttt_recurrence_workspace_bytes(ref)
     ws = _temp(need, dev, stream)
-    ipttt_recurrence_backward(r, View(*_strides("dh", dh, shape, dtype, dev)), dh_last,
-                              View(*_strides("dg", dg, shape, dtype, dev)),
-                              View(*_strides("dv", dv, shape, dtype, dev)), dh0, ws, need, st)
+    _check(load().ipttt_recurrence_backward(ref, views[0], _p(dh_last), views[1], views[2],
+                                            dh0.data_ptr(), ws.data_ptr(), need, st))
     if stream is not None:
         _used_on(stream, g, v, h, dh, h0, dh_last, starts, lens, dg, dv, dh0)
     return {"dg": dg, "dv": dv, "dh0": dh0}
@@ -465,13 +470,13 @@ class FeedForward:
         ds = _rows("dy", dy, d, dtype, dev, n)
         for name, t in (("a", a), ("u", u)):
             _dense(name, t, x.shape[:-1] + (f,), torch.float32, dev)
-        new = lambda *s: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
-        g = {"dx": new(*x.shape), "dw_gate": new(f, d), "dw_up": new(f, d), "dw_down": new(d, f)}
-        need = ipttt_ff_backward_workspace_bytes(self.desc, n)
+        dx = torch.empty_like(x, memory_format=_DENSE)
+        dwg, dwu, dwd = (torch.empty_like(w) for w in (self.w_gate, self.w_up, self.w_down))
+        need = load().ipttt_ff_backward_workspace_bytes(self._ref, n)
         ws = _temp(need, dev, stream)
-        ipttt_ff_backward(self.desc, x, xs, a, u, dy, ds, n,
-                          FFGrads(_p(g["dx"]), d, _p(g["dw_gate"]), _p(g["dw_up"]), _p(g["dw_down"])),
-                          ws, need, st)
+        grads = FFGrads(dx.data_ptr(), d, dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr())
+        _check(load().ipttt_ff_backward(self._ref, x.data_ptr(), xs, a.data_ptr(), u.data_ptr(),
+                                        dy.data_ptr(), ds, n, ctypes.byref(grads), ws.data_ptr(), need, st))
         if stream is not None:
-            _used_on(stream, x, a, u, dy, self.w_gate, self.w_up, self.w_down, *g.values())
-        return g
+            _used_on(stream, x, a, u, dy, self.w_gate, self.w_up, self.w_down, dx, dwg, dwu, dwd)
+        return {"dx": dx, "dw_gate": dwg, "dw_up": dwu, "dw_down": dwd}

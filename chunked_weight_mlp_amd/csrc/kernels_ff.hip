@@ -1,9 +1,11 @@
 // The gated feed-forward block y = (SiLU(x W_g) * (x W_u)) W_d, forward and
 // backward.
 //
-// Every product of the block runs on one bf16 MFMA kernel (k_ff_gemm) over
-// operands whose K values are contiguous and padded with zeros to whole steps of
-// 64, with the output written contiguously along the first operand's rows:
+// Three kernels, by the number of tokens: k_ff_small streams the weights past single
+// tokens, k_ff_direct takes few tokens' operands as they lie, and with many tokens
+// every product runs on one bf16 MFMA kernel (k_ff_gemm) over operands whose K values
+// are contiguous and padded with zeros to whole steps of 64, with the output written
+// contiguously along the first operand's rows:
 //   a, u [n][F]  = W_g, W_u rows x x rows          K = d   (one launch, z fused)
 //   y    [n][d]  = W_d rows x z rows               K = F
 //   dz   [n][F]  = W_d^T rows x dy rows            K = d   (dA, dU, z fused)
@@ -17,6 +19,11 @@
 // p0 q2, p2 q0, p1 q1, p0 q1, p1 q0, p0 q0, which leaves out only terms below
 // 2^-24 of a product: fp32 accuracy at six times the bf16 work, against
 // 1/16 of the bf16 rate for the fp32 MFMA.
+//
+// k_ff_gemm is bound by LDS bandwidth (each MFMA's operands pass through it): 16384
+// tokens of 2560 x 9728 in bf16 take 1.93 ms, 1270 TFLOP/s, where a large library
+// product reaches 1581; its epilogues' traffic comes on top (the dz product of 8192
+// tokens of 2048 x 8192 has 1.2 GB of it, 300 of its 530 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -714,8 +721,11 @@ hipError_t launch_small(const T *w, const T *w2, const T *x, int64_t x_ld, int n
 // than the products. Here a product takes its operands as they lie, of either
 // orientation and any type, stride and width, turns them on their way into LDS and
 // uses the MFMA of their own type (fp32: no planes), in 64 x 64 tiles of which many
-// fit a small matrix. 128 bytes of K a step, two steps' loads in flight in registers
-// while a third is in LDS. Bound by the steps' latency, or by the weights' traffic.
+// fit a small matrix (or 64 x 32, direct_with). 128 bytes of K a step, two steps' loads in
+// flight in registers while a third is in LDS (four steps': 2048 x 8192 bf16, 64 tokens 90
+// us against 76). Bound by the weights' traffic with the fewest tokens (one token of 2048
+// x 8192, backward: fp32 149 us, 2.7 TB/s, bf16 72), else by the fp32 MFMA (512 tokens
+// forward 441 us, 117 of 154 TFLOP/s) or, in bf16, by its small tiles' LDS reads.
 
 // One operand: element (row, k) is p[row ld + k], or, turned, p[k ld + row]; the second
 // of two runs of K continues in p2.
@@ -751,23 +761,27 @@ __device__ __forceinline__ int dslot(int r, int q) { return r * 8 + (q ^ ((r ^ (
 // piece at the end moves back. Rows are then stored where they belong (a neighbour's,
 // with the same values, once more); of K, the values the piece before holds are zeroed,
 // on both sides of the product. A pair: 32 rows of p, then the same 32 of p2.
-template <typename T, bool turned, bool pair = false>
+template <typename T, bool turned, bool pair, int ROWS>
 struct DirectLoader {
   static constexpr int E = Quad<T>::E, S = kDStep<T>;
+  static_assert(ROWS == 64 || (ROWS == 32 && !turned), "two pieces a thread, or one straight one");
+  // pieces of a thread, and turned ones' distance in the step (bf16 takes pairs of values)
+  static constexpr int NQ = ROWS / 32, KI = E == 8 ? 1 : 16;
   const T *p, *p2;
-  int64_t at[2];  // of its rows
-  int64_t ks;     // distance between values of K
-  int row[2];     // in the tile
-  int pos;        // its place in the step (the first of turned values)
+  int64_t at[NQ];  // of its rows
+  int64_t ks;      // distance between values of K
+  int row[NQ];     // in the tile
+  int pos;         // its place in the step (the first of turned values)
   // the place in the step of piece i
-  __device__ __forceinline__ int place(int i) const { return turned ? pos + (E == 8 ? i : 16 * i) : pos; }
+  __device__ __forceinline__ int place(int i) const { return turned ? pos + KI * i : pos; }
   __device__ __forceinline__ DirectLoader(const FfSide<T> &s, int r0, int R) : p(s.p), p2(s.p2) {
+    constexpr int GR = ROWS / E;  // groups of E rows
     const int tid = threadIdx.x;
     ks = turned ? s.ld : 1;
-    pos = turned ? (E == 8 ? 2 * (tid >> 3) : tid >> 4) : E * (tid & 7);
+    pos = turned ? (E == 8 ? 2 : 1) * (tid / GR) : E * (tid & 7);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = turned ? min(r0 + E * (tid & (64 / E - 1)), R - E)
+    for (int i = 0; i < NQ; ++i) {
+      const int r = turned ? min(r0 + E * (tid & (GR - 1)), R - E)
                            : min(r0 + (tid >> 3) + (pair ? 0 : 32 * i), R - 1);
       at[i] = turned ? r : r * s.ld;
       // (rows before the tile go to its end, past the matrix's last)
@@ -781,13 +795,13 @@ struct DirectLoader {
   }
   __device__ __forceinline__ void load(Quad<T> (&q)[2], bool second, int k0, int K) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NQ; ++i)
       q[i] = quad_at<T>(((pair ? i == 1 : second) ? p2 : p) + at[i] + first_k(i, k0, K) * ks);
   }
   __device__ __forceinline__ void store(Quad<T> (&q)[2], Quad<T> *lds, int k0, int K) const {
     if (k0 + S > K) {  // the last step
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < NQ; ++i) {
         const int p = place(i), in = p & (E - 1), from = k0 + p - in, at0 = min(from, max(K - E, 0));
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -798,52 +812,52 @@ struct DirectLoader {
     }
     if constexpr (!turned) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) lds[dslot(row[i], pos / E)] = q[i];
+      for (int i = 0; i < NQ; ++i) lds[dslot(row[i], pos / E)] = q[i];
     } else if constexpr (E == 8) {
       const U32x4 lo = __builtin_bit_cast(U32x4, q[0]), hi = __builtin_bit_cast(U32x4, q[1]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {  // the e-th halves of both
         const unsigned h = hi[e >> 1], l = lo[e >> 1];
-        ((unsigned *)(lds + dslot((row[0] + e) & (kDTile - 1), pos >> 3)))[(pos & 7) >> 1] =
+        ((unsigned *)(lds + dslot((row[0] + e) & (ROWS - 1), pos >> 3)))[(pos & 7) >> 1] =
             __builtin_amdgcn_perm(h, l, e & 1 ? 0x07060302 : 0x05040100);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < NQ; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          ((float *)(lds + dslot((row[i] + e) & (kDTile - 1), place(i) >> 2)))[pos & 3] = q[i].v[e];
+          ((float *)(lds + dslot((row[i] + e) & (ROWS - 1), place(i) >> 2)))[pos & 3] = q[i].v[e];
     }
   }
 };
 
 // TURNED: a is (b where its problem says so). DUAL: two products of 32 rows each, of a.p
-// and a.p2, for one epilogue.
-template <typename T, bool TURNED, bool DUAL, class Epi, int G>
-__global__ __launch_bounds__(256) void k_ff_direct(FfDirects<T, Epi, G> grp) {
-  constexpr int S = kDStep<T>, AHEAD = 2, MT = DUAL ? kDTile / 2 : kDTile;
+// and a.p2, for one epilogue. TN: columns of a tile.
+template <typename T, bool TURNED, bool DUAL, int TN, class Epi, int G>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k_ff_direct(FfDirects<T, Epi, G> grp) {
+  constexpr int S = kDStep<T>, AHEAD = 2, MT = DUAL ? kDTile / 2 : kDTile, NJ = TN / 32;
   __shared__ Quad<T> lds[2][2][kDTile * 8];
   int which = 0;
 #pragma unroll
   for (int p = 1; p < G; ++p) which += (int)blockIdx.x >= grp.start[p];
   const FfDirect<T> g = grp.prob[which];
   const Epi epi = grp.epi[which];
-  const int nm = (g.M + MT - 1) / MT, nn = (g.N + kDTile - 1) / kDTile;
+  const int nm = (g.M + MT - 1) / MT, nn = (g.N + TN - 1) / TN;
   const int blocks = nm * nn * g.splits, bid = blockIdx.x - grp.start[which];
   if (bid >= blocks) return;
   const int id = xcd_remap(bid, blocks), sp = id / (nm * nn);
   int tm, tn;
   tile_of<8>(id % (nm * nn), nm, nn, tm, tn);
-  const int m0 = tm * MT, n0 = tn * kDTile;
+  const int m0 = tm * MT, n0 = tn * TN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = 32 * (wave & 1), gq = lane >> 4, lr = lane & 15;
+  const int wn = TN / 2 * (wave & 1), gq = lane >> 4, lr = lane & 15;
   const int wm = (DUAL ? 16 : 32) * (wave >> 1), wi = DUAL ? 32 : 16;  // its rows: 16 each from wm, wm + wi
   const int per_run = (g.K + S - 1) / S, steps = g.runs * per_run;
   const int per = (steps + g.splits - 1) / g.splits, first = sp * per, count = min(per, steps - first);
-  f32x4 acc[2][2] = {};
+  f32x4 acc[2][NJ] = {};
   const auto run = [&](auto tag) __attribute__((always_inline)) {
-    const DirectLoader<T, TURNED, DUAL> la(g.a, m0, g.M);
-    const DirectLoader<T, decltype(tag)::value> lb(g.b, n0, g.N);
+    const DirectLoader<T, TURNED, DUAL, kDTile> la(g.a, m0, g.M);
+    const DirectLoader<T, decltype(tag)::value, false, TN> lb(g.b, n0, g.N);
     Quad<T> qa[AHEAD][2], qb[AHEAD][2];
     const auto fetch = [&](int s, int j) __attribute__((always_inline)) {
       const bool second = first + s >= per_run;
@@ -862,16 +876,15 @@ __global__ __launch_bounds__(256) void k_ff_direct(FfDirects<T, Epi, G> grp) {
       lds_barrier();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        Quad<T> a[2], b[2];
+        Quad<T> a[2], b[NJ];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          a[i] = as[dslot(wm + wi * i + lr, 4 * u + gq)];
-          b[i] = bs[dslot(wn + 16 * i + lr, 4 * u + gq)];
-        }
+        for (int i = 0; i < 2; ++i) a[i] = as[dslot(wm + wi * i + lr, 4 * u + gq)];
+#pragma unroll
+        for (int k = 0; k < NJ; ++k) b[k] = bs[dslot(wn + 16 * k + lr, 4 * u + gq)];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) acc[i][k] = Quad<T>::mma(a[i], b[k], acc[i][k]);
+          for (int k = 0; k < NJ; ++k) acc[i][k] = Quad<T>::mma(a[i], b[k], acc[i][k]);
       }
     };
     fetch(0, 0);
@@ -885,24 +898,28 @@ __global__ __launch_bounds__(256) void k_ff_direct(FfDirects<T, Epi, G> grp) {
     if (s + 1 < count) step(s + 1, 1, false);
     if (s + 2 < count) step(s + 2, 0, false);
   };
-  if (G > 1 && g.b_turned)
-    run(std::true_type());
-  else
+  if constexpr (G > 1) {
+    if (g.b_turned)
+      run(std::true_type());
+    else
+      run(std::false_type());
+  } else {
     run(std::false_type());
+  }
   if constexpr (DUAL) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       const int n = n0 + wn + 16 * j + lr;
       if (n < g.N) epi.store(m0 + wm + 4 * gq, n, acc[0][j], acc[1][j]);
     }
   } else {
     const int m = m0 + wm + 8 * (gq >> 1) + 16 * (gq & 1);
-    typename Epi::In in[2];
+    typename Epi::In in[NJ];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < NJ; ++j)
       in[j] = epi.template load<false>(m, min(n0 + wn + 16 * j + lr, g.N - 1));
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       const int n = n0 + wn + 16 * j + lr;
       float v[8];
       rows8(acc[0][j], acc[1][j], v);
@@ -1170,17 +1187,17 @@ struct BwdPlan {
 };
 
 // Whether a forward streams its weights (k_ff_small). Measured against the operands as
-// they lie below (us, streaming / that), fp32: 512 x 2048 at 8 tokens 13 / 26, at 32 20 / 27;
-// 1024 x 4096 at 16 26 / 45, at 24 50 / 45; 2048 x 8192 at 8 53 / 79, at 16 82 / 78. bf16:
-// 1024 x 4096 at 32 17 / 20; 2048 x 8192 at 16 27 / 29, at 24 42 / 29; 1999 x 3001 at 8
-// 17 / 27, at 16 33 / 27, at 32 32 / 28.
+// they lie below (us, streaming / that), fp32: 512 x 2048 at 8 tokens 13 / 22, at 32 20 / 22;
+// 1024 x 4096 at 16 26 / 36, at 24 50 / 36; 2048 x 8192 at 8 53 / 61, at 16 82 / 61. bf16:
+// 1024 x 4096 at 32 17 / 20; 2048 x 8192 at 8 21 / 27, at 16 27 / 27, at 24 42 / 27; 1999 x
+// 3001 at 8 17 / 27, at 16 33 / 27.
 bool single_tokens(int elem, int d, int F, int64_t n) {
-  return n <= 16 || (n <= 32 && n * d * F * elem <= 1 << 28);
+  return n <= 8 || (n <= 32 && n * d * F * elem <= 1 << 28);
 }
 // Whether it takes its operands as they lie (k_ff_direct), or has those that need it laid
 // out for the large tiles' kernel: whose time that pass is with few tokens. Both sides
 // measured (us, direct / laid out), fp32: 250 x 671 at 333 tokens 20 / 39, at 2048 39 / 43; 512
-// x 2048 at 512 46 / 64, at 2048 130 / 112; 1024 x 4096 at 64 44 / 102, at 512 123 / 128, at
+// x 2048 at 512 46 / 64, at 2048 130 / 112; 1024 x 4096 at 64 37 / 102, at 512 123 / 128, at
 // 1024 228 / 194; 2048 x 8192 at 64 78 / 294, at 512 439 / 430. bf16: 1999 x 3001 at 64 28 /
 // 55, at 512 60 / 66, at 1024 102 / 83; whole steps of K: 256 x 1024 at 1024 15 / 18, at 2048
 // 20 / 20; 512 x 2048 at 333 19 / 21, at 1024 27 / 24; 1024 x 4096 at 128 23 / 27, at 333 31 /
@@ -1189,13 +1206,13 @@ bool few_forward(int elem, int d, int F, int64_t n) {
   if (d < 8 || F < 8) return false;  // pieces of 8 values along a row
   return n <= (elem == 4 || d % kStep || F % kStep ? 512 : 128) || n * d * F <= 1 << 29;
 }
-// The same for a backward, whose operands all need laying out. Measured (us, direct / laid out), fp32: 250 x 671 at
-// 333 tokens 33 / 59, at 2048 71 / 108; 512 x 2048 at 1024 138 / 175; 1024 x 4096 at 64
-// 76 / 140, at 512 241 / 283, at 1024 449 / 428; 2048 x 8192 at 64 186 / 421, at 512 924 /
-// 842. bf16: 250 x 671 at 2048 38 / 41; 512 x 2048 at 1024 51 / 57; 1024 x 4096 at 64 41 /
-// 53, at 512 70 / 75, at 1024 121 / 112; 2048 x 8192 at 64 76 / 135, at 200 133 / 155, at
-// 512 232 / 203; 1999 x 3001, where 16 bytes start at any element, at 64 61 / 80, at 333
-// 107 / 107, at 512 127 / 117.
+// The same for a backward, whose operands all need laying out. Measured (us, direct /
+// laid out), fp32: 250 x 671 at 333 tokens 30 / 59, at 2048 71 / 108; 512 x 2048 at 1024
+// 138 / 175; 1024 x 4096 at 64 68 / 140, at 512 241 / 283, at 1024 449 / 428; 2048 x 8192 at
+// 64 174 / 421, at 512 924 / 842. bf16: 250 x 671 at 2048 38 / 41; 512 x 2048 at 1024 51 / 57;
+// 1024 x 4096 at 64 39 / 53, at 512 70 / 75, at 1024 121 / 112; 2048 x 8192 at 64 74 / 135, at
+// 200 133 / 155, at 512 232 / 203; 1999 x 3001, where 16 bytes start at any element, at
+// 64 56 / 80, at 333 107 / 107, at 512 127 / 117.
 bool few_backward(int elem, int d, int F, int64_t n) {
   if (d < 8 || F < 8) return false;  // pieces of 8 values along a row
   const int64_t unit = (int64_t)1 << 30;
@@ -1254,17 +1271,29 @@ struct DirectBwd {
   }
 };
 
-template <typename T, bool TURNED, bool DUAL, class Epi, int G>
+template <typename T, bool TURNED, bool DUAL, int TN, class Epi, int G>
 hipError_t launch_direct(FfDirects<T, Epi, G> grp, hipStream_t st) {
   int at = 0;
   for (int p = 0; p < G; ++p) {
     const FfDirect<T> &g = grp.prob[p];
     grp.start[p] = at;
-    at += (int)round_up(ceil_div(g.M, DUAL ? kDTile / 2 : kDTile) * ceil_div(g.N, kDTile) * g.splits, 8);
+    at += (int)round_up(ceil_div(g.M, DUAL ? kDTile / 2 : kDTile) * ceil_div(g.N, TN) * g.splits, 8);
   }
   grp.start[G] = at;
-  hipLaunchKernelGGL((k_ff_direct<T, TURNED, DUAL, Epi, G>), dim3((unsigned)at), dim3(256), 0, st, grp);
+  hipLaunchKernelGGL((k_ff_direct<T, TURNED, DUAL, TN, Epi, G>), dim3((unsigned)at), dim3(256), 0, st, grp);
   return hipGetLastError();
+}
+// A product with an epilogue of its own, which cannot be split: in narrow tiles where wide
+// ones leave CUs without any or are half empty (us, narrow / wide, fp32: 512 x 2048, 64 tokens
+// forward 23 / 27, backward 36 / 41; 1216 x 1864, 64 tokens 33 / 42, 58 / 69; 2048 x 8192, 17
+// tokens forward 60 / 77; with narrow tiles up to two a CU 1024 x 4096, 175 tokens 61 / 68, but
+// 1216 x 1864, 333 tokens backward 130 / 127).
+template <typename T, bool TURNED, bool DUAL, class Epi>
+hipError_t direct_with(const FfDirect<T> &g, const Epi &epi, hipStream_t st) {
+  const FfDirects<T, Epi, 1> grp{{g}, {epi}, {}};
+  if (g.N <= 32 || ceil_div(g.M, DUAL ? kDTile / 2 : kDTile) * ceil_div(g.N, kDTile) < kCUs)
+    return launch_direct<T, TURNED, DUAL, 32>(grp, st);
+  return launch_direct<T, TURNED, DUAL, kDTile>(grp, st);
 }
 
 template <typename T>
@@ -1273,11 +1302,11 @@ hipError_t forward_direct(const FfArgs &p, hipStream_t st) {
   const DirectFwd<T> w(p.ws, d, F, n);
   const FfDirect<T> q{{(const T *)p.w_gate, (const T *)p.w_up, d}, {(const T *)p.x, nullptr, p.x_stride},
                       false, F, n, d, 1, 1};
-  TRYH((launch_direct<T, false, true, EpiZDirect<T>, 1>({{q}, {EpiZDirect<T>{w.z, p.a, p.u, F}}, {}}, st)));
+  TRYH((direct_with<T, false, true>(q, EpiZDirect<T>{w.z, p.a, p.u, F}, st)));
   FfDirects<T, EpiOut<T>, 1> g{{w.out}, {direct_out(w.out, w.part, p.y, p.y_stride)}, {}};
   g.prob[0].a = {(const T *)p.w_down, nullptr, F};
   g.prob[0].b = {w.z, nullptr, F};
-  TRYH((launch_direct<T, false, false, EpiOut<T>, 1>(g, st)));
+  TRYH((launch_direct<T, false, false, kDTile>(g, st)));
   return joins<T, 1>(g, st);
 }
 
@@ -1288,8 +1317,7 @@ hipError_t backward_direct(const FfArgs &p, hipStream_t st) {
   const T *x = (const T *)p.x, *dy = (const T *)p.dy, *wd = (const T *)p.w_down;
   // dz(f, t) = sum_c W_d(c, f) dy(t, c), and from it dA, dU and z
   const FfDirect<T> dz{{wd, nullptr, F}, {dy, nullptr, p.dy_stride}, false, F, n, d, 1, 1};
-  TRYH((launch_direct<T, true, false, EpiDzDirect<T>, 1>(
-      {{dz}, {EpiDzDirect<T>{p.a, p.u, w.da, w.du, w.z, F}}, {}}, st)));
+  TRYH((direct_with<T, true, false>(dz, EpiDzDirect<T>{p.a, p.u, w.da, w.du, w.z, F}, st)));
   FfDirects<T, EpiOut<T>, 4> g{};
   const auto out = [&](int k, FfSide<T> a, FfSide<T> b, void *to, int64_t ld) {
     g.prob[k] = w.out[k];
@@ -1302,7 +1330,7 @@ hipError_t backward_direct(const FfArgs &p, hipStream_t st) {
   out(1, {x, nullptr, p.x_stride}, {w.da, nullptr, F}, p.dw_gate, d);
   out(2, {x, nullptr, p.x_stride}, {w.du, nullptr, F}, p.dw_up, d);
   out(3, {w.z, nullptr, F}, {dy, nullptr, p.dy_stride}, p.dw_down, F);
-  TRYH((launch_direct<T, true, false, EpiOut<T>, 4>(g, st)));
+  TRYH((launch_direct<T, true, false, kDTile>(g, st)));
   return joins<T, 4>(g, st);
 }
 

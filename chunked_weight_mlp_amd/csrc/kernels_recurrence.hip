@@ -676,11 +676,15 @@ __global__ __launch_bounds__(256) void k_rec_clear(uint64_t *ws, int64_t slots) 
   }
 }
 
+// Tokens to which a thread walks its sequence itself (us, walked / in tiles, forward and
+// backward: 32 sequences of 16 x 2560 8.7 / 13.3 and 13.8 / 26.7, of 32 15.6 / 13.6 and 26.3 /
+// 27.5; one of 16 7.9 / 6.9 and 12.8 / 12.9, of 32 14.1 / 6.8 and 23.4 / 12.9).
 constexpr int64_t SEQ_MAX = 16;
 
 // Channels per lane, tokens per wave in the forward and the backward, waves, all
 // measured on 128k x 2560 forward / 8 x 16k x 2048 backward, bf16, where a copy of
-// the same bytes takes 421 / 674 us. As here 483 / 601 us. 8 tokens a wave 688 / 686,
+// the same bytes takes 421 / 674 us. As here 483 / 601 us (with the
+// measured cases' gates 443 / 635). 8 tokens a wave 688 / 686,
 // 32 (forward) 476 but 28 us against 17 for 5 x 1237 x 331; 4 waves of 16 tokens 572 /
 // 640, 16 waves of 8 (backward) 760; 4 channels a lane 725 / 899 and up (registers).
 // Slots a wave reads (LB) 1, 2, 3: 483, 513, 530 (forward). Bound by HBM.

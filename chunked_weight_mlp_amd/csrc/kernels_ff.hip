@@ -504,8 +504,8 @@ __global__ __launch_bounds__(256) void k_ff_zero(uint16_t *__restrict__ p, int64
 // share it). The MFMA's 16 operand rows would be 16 weight rows, whose 16-byte
 // pieces lie a row apart: 64 cache lines a load, and the loads' address work, not
 // memory, sets the time (n = 16: 46 us so, 27 as here, 2048 x 8192 in bf16). So an
-// operand row is a weight row
-// i and one of KF neighbouring pieces of K, s: rows i KF + s, and columns j KF + s
+// operand row is a weight row i and one of KF neighbouring pieces of K, s: rows i KF + s,
+// and columns j KF + s
 // of the other operand for token j. Lanes next to each other then read pieces
 // next to each other; of the products, those whose two s agree are summed.
 // A block owns RG groups of 16 / KF weight rows (of both W_g and W_u in the first
@@ -834,7 +834,8 @@ struct DirectLoader {
 // TURNED: a is (b where its problem says so). DUAL: two products of 32 rows each, of a.p
 // and a.p2, for one epilogue. TN: columns of a tile.
 template <typename T, bool TURNED, bool DUAL, int TN, class Epi, int G>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k_ff_direct(FfDirects<T, Epi, G> grp) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k_ff_direct(
+    FfDirects<T, Epi, G> grp) {
   constexpr int S = kDStep<T>, AHEAD = 2, MT = DUAL ? kDTile / 2 : kDTile, NJ = TN / 32;
   __shared__ Quad<T> lds[2][2][kDTile * 8];
   int which = 0;
@@ -1352,7 +1353,8 @@ using namespace mfma;
 size_t ff_forward_workspace(int elem, int d, int F, int64_t n) {
   if (single_tokens(elem, d, F, n)) return (size_t)round_up(std::max<int64_t>(n, 1) * F * elem, 256);
   if (few_forward(elem, d, F, n))
-    return elem == 2 ? DirectFwd<__bf16>(nullptr, d, F, (int)n).bytes : DirectFwd<float>(nullptr, d, F, (int)n).bytes;
+    return elem == 2 ? DirectFwd<__bf16>(nullptr, d, F, (int)n).bytes
+                     : DirectFwd<float>(nullptr, d, F, (int)n).bytes;
   return FwdPlan(nullptr, elem == 2 ? 1 : 3, d, F, n).bytes;
 }
 size_t ff_backward_workspace(int elem, int d, int F, int64_t n) {

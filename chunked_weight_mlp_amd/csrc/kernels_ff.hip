@@ -21,7 +21,7 @@
 // 1/16 of the bf16 rate for the fp32 MFMA.
 //
 // k_ff_gemm is bound by LDS bandwidth (each MFMA's operands pass through it): 16384
-// tokens of 2560 x 9728 in bf16 take 1.93 ms, 1270 TFLOP/s, where a large library
+// tokens of 2560 x 9728 in bf16 take 1.90 ms, 1290 TFLOP/s, where a large library
 // product reaches 1581; its epilogues' traffic comes on top (the dz product of 8192
 // tokens of 2048 x 8192 has 1.2 GB of it, 300 of its 530 us).
 #include <algorithm>

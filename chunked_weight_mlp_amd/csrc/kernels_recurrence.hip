@@ -681,20 +681,27 @@ __global__ __launch_bounds__(256) void k_rec_clear(uint64_t *ws, int64_t slots) 
 // 27.5; one of 16 7.9 / 6.9 and 12.8 / 12.9, of 32 14.1 / 6.8 and 23.4 / 12.9).
 constexpr int64_t SEQ_MAX = 16;
 
-// Channels per lane, tokens per wave in the forward and the backward, waves, all
+// Tokens per wave in the forward and the backward, waves, and channels per lane, all
 // measured on 128k x 2560 forward / 8 x 16k x 2048 backward, bf16, where a copy of
 // the same bytes takes 421 / 674 us. As here 483 / 601 us (with the
 // measured cases' gates 443 / 635). 8 tokens a wave 688 / 686,
 // 32 (forward) 476 but 28 us against 17 for 5 x 1237 x 331; 4 waves of 16 tokens 572 /
 // 640, 16 waves of 8 (backward) 760; 4 channels a lane 725 / 899 and up (registers).
 // Slots a wave reads (LB) 1, 2, 3: 483, 513, 530 (forward). Bound by HBM.
-constexpr int kV = 2, kFwdTokens = 16, kBwdTokens = 16, kWaves = 8;
+constexpr int kFwdTokens = 16, kBwdTokens = 16, kWaves = 8;
+// Two channels a lane, one where 64 lanes hold them all: 15 x 8670 x 64 fp32 forward 32 us
+// (two: 47), backward 45 (87); 5 x 33168 x 64 bf16 39 (46), 44 (77).
+int lane_channels(int d) { return d <= 64 ? 1 : 2; }
 constexpr int kFwdTile = kFwdTokens * kWaves, kBwdTile = kBwdTokens * kWaves;
 constexpr int kMinTile = kFwdTile < kBwdTile ? kFwdTile : kBwdTile;  // what the workspace holds
 
-int64_t channel_blocks(int d) { return (d + 64 * kV - 1) / (64 * kV); }
-int64_t tile_slots(int n, int d, int64_t nt) {  // and the groups'
-  return (nt + nt / (kWaves * LB) + 1) * n * channel_blocks(d) * 64 * kV;
+int64_t channel_blocks(int d) {
+  const int ch = 64 * lane_channels(d);
+  return (d + ch - 1) / ch;
+}
+// the tiles' and the groups', for either width of a tile
+int64_t tile_slots(int n, int d, int64_t nt) {
+  return (nt + nt / (kWaves * LB) + 1) * n * round_up(d, 128);
 }
 
 hipError_t clear_slots(const RecArgs &a, int64_t nt, hipStream_t st) {
@@ -730,9 +737,11 @@ hipError_t rec_forward(const RecArgs &a, hipStream_t st) {
   const int64_t nt = (a.L + kFwdTile - 1) / kFwdTile;
   const hipError_t e = clear_slots(a, nt, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_rec_fwd<T, kV, kFwdTokens, kWaves>),
-                     blk::grid_of(nt * a.n * channel_blocks(a.d)), dim3(64 * kWaves), 0, st, a,
-                     (int)nt);
+  const dim3 grid = blk::grid_of(nt * a.n * channel_blocks(a.d)), block(64 * kWaves);
+  if (lane_channels(a.d) == 1)
+    hipLaunchKernelGGL((k_rec_fwd<T, 1, kFwdTokens, kWaves>), grid, block, 0, st, a, (int)nt);
+  else
+    hipLaunchKernelGGL((k_rec_fwd<T, 2, kFwdTokens, kWaves>), grid, block, 0, st, a, (int)nt);
   return hipGetLastError();
 }
 
@@ -746,9 +755,11 @@ hipError_t rec_backward(const RecArgs &a, hipStream_t st) {
   const int64_t nt = (a.L + kBwdTile - 1) / kBwdTile;
   const hipError_t e = clear_slots(a, nt, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_rec_bwd<T, kV, kBwdTokens, kWaves>),
-                     blk::grid_of(nt * a.n * channel_blocks(a.d)), dim3(64 * kWaves), 0, st, a,
-                     (int)nt);
+  const dim3 grid = blk::grid_of(nt * a.n * channel_blocks(a.d)), block(64 * kWaves);
+  if (lane_channels(a.d) == 1)
+    hipLaunchKernelGGL((k_rec_bwd<T, 1, kBwdTokens, kWaves>), grid, block, 0, st, a, (int)nt);
+  else
+    hipLaunchKernelGGL((k_rec_bwd<T, 2, kBwdTokens, kWaves>), grid, block, 0, st, a, (int)nt);
   return hipGetLastError();
 }
 

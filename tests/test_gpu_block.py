@@ -169,6 +169,7 @@ def mix_inputs(n, length, d, t, fused, starts, ragged, seed=1):
 
 
 MIX = [
+    (3, 1500, 63, True, True, True), (2, 1500, 64, False, True, False), (4, 700, 1, False, False, True),
     (1, 1, 1, False, False, False), (2, 1, 130, True, False, False), (1, 2, 3, False, True, False),
     (3, 7, 64, True, True, False), (1, 17, 33, False, False, False), (6, 40, 65, True, True, True),
     (2, 128, 128, True, False, False), (1, 129, 130, False, True, False),
@@ -298,6 +299,7 @@ def test_recurrence_gradient_into_a_fused_projection():
 
 
 @pytest.mark.parametrize("n,length,d,starts", [(2, 3000, 300, True), (1, 60001, 43, False),
+                                               (3, 5000, 64, True), (3, 5000, 65, False),
                                                (9, 5000, 517, False)])
 def test_recurrence_repeats_bit_for_bit(n, length, d, starts):
     """fp32, whose last bits would show an order that depends on timing."""

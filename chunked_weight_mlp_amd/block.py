@@ -5,9 +5,13 @@ backward, over libipttt's HIP kernels.
 The `ipttt_*` functions are the C entry points with tensors for pointers; Norm
 and FeedForward hold an operator's weights, and recurrence_forward / _step /
 _backward allocate their outputs and workspace. Errors are ipttt.IptttError.
-Tensors must be on the device of the stream the call runs on (`stream`, or the
-current one); a stream other than the current one must already be ordered after
-whatever produced the inputs, as with any torch tensor.
+Tensors must be on the device of the stream the call runs on: the current one, or
+`stream` (a torch stream or its handle), with which a call does what it would do
+under `torch.cuda.stream(stream)`: its outputs and workspace come from that stream's
+memory. Such a stream must already be ordered after whatever produced the inputs, and
+whoever uses the outputs on another stream after this one, as with any torch tensor;
+that neither's memory is handed out again too early, on `stream` or on the stream
+that was current, is taken care of.
 """
 from __future__ import annotations
 
@@ -230,35 +234,44 @@ def _rows(name, t, d, dtype, device, n=None):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(stream, device):
-    """The HIP stream of a call whose tensors are on `device`."""
+def _on(device):
+    """The current HIP stream, for a call whose tensors are on `device`."""
     index = device.index
     if device.type != "cuda":
         raise _invalid(f"tensors are on {device}, not on a GPU")
     if index != torch.cuda.current_device():
         raise _invalid(f"tensors are on {device}, the current device is cuda:"
                        f"{torch.cuda.current_device()}")
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(index)
-    return _stream(stream)
+    return _stream(None) if _raw_stream is None else _raw_stream(index)
 
 
-def _temp(nbytes, device, stream):
-    """Workspace from torch's allocator. On a stream other than the current one the
-    allocator is told, so the memory is not handed out again while the call runs."""
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        _used_on(stream, t)
-    return t
-
-
-def _used_on(stream, *tensors):
+def _call_on(stream, op, args, weights=()):
+    """op(*args) on another stream than the current one. Outputs and workspace are
+    allocated as that stream's: a block of the current stream's memory may still have
+    work queued on it by a tensor that is gone, which `stream` is not ordered after.
+    The allocator is told that `stream` uses the inputs, and the current stream the
+    outputs, so that neither is handed out again while the other still works on it."""
+    if args[0].device.type != "cuda":
+        return op(*args)   # which refuses them
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
-    if stream != torch.cuda.current_stream(stream.device):
-        for t in tensors:
-            if t is not None and t.is_cuda:
-                t.record_stream(stream)
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return op(*args)
+    with torch.cuda.stream(stream):
+        out = op(*args)
+    for t in (*args, *weights):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    for t in (out,) if isinstance(out, torch.Tensor) else out.values() if isinstance(out, dict) else out:
+        if t is not None:
+            t.record_stream(current)
+    return out
+
+
+def _temp(nbytes, device):
+    """Workspace from torch's allocator."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 class Norm:
@@ -278,9 +291,11 @@ class Norm:
     def forward(self, x, res=None, stream=None):
         """Returns (y, h, mean, rstd): h = x + res (x itself without res), y its norm,
         and the rows' statistics for the backward. x, res: [..., d]."""
+        if stream is not None:
+            return _call_on(stream, self.forward, (x, res), (self.gamma, self.beta))
         d, dtype, dev = self.d, self.dtype, self.device
         xs = _rows("x", x, d, dtype, dev)
-        st = _on(stream, dev)
+        st = _on(dev)
         shape = x.shape
         n = x.numel() // d
         y = torch.empty_like(x, memory_format=_DENSE)
@@ -294,16 +309,16 @@ class Norm:
             hp = h.data_ptr()
         _check(load().ipttt_norm_forward(self._ref, x.data_ptr(), xs, r, rs, n, hp, y.data_ptr(),
                                          mean.data_ptr(), rstd.data_ptr(), st))
-        if stream is not None:
-            _used_on(stream, x, res, h, y, mean, rstd, self.gamma, self.beta)
         return y, (x if h is None else h), mean, rstd
 
     def backward(self, h, mean, rstd, dy, dh=None, stream=None):
         """Returns {"dx", "dgamma", "dbeta"}: the gradient of x and res ([..., d], the
         activations' dtype) and the fp32 weight gradients, from dL/dy and dL/dh."""
+        if stream is not None:
+            return _call_on(stream, self.backward, (h, mean, rstd, dy, dh), (self.gamma,))
         d, dtype, dev = self.d, self.dtype, self.device
         hs = _rows("h", h, d, dtype, dev)
-        st = _on(stream, dev)
+        st = _on(dev)
         n = h.numel() // d
         ds = _rows("dy", dy, d, dtype, dev, n)
         hh = 0 if dh is None else _rows("dh", dh, d, dtype, dev, n)
@@ -316,12 +331,10 @@ class Norm:
         dgamma = torch.empty(d, dtype=torch.float32, device=dev)
         dbeta = torch.empty(d, dtype=torch.float32, device=dev)
         need = load().ipttt_norm_backward_workspace_bytes(self._ref, n)
-        ws = _temp(need, dev, stream)
+        ws = _temp(need, dev)
         _check(load().ipttt_norm_backward(self._ref, h.data_ptr(), hs, mean.data_ptr(), rstd.data_ptr(),
                                           dy.data_ptr(), ds, _p(dh), hh, n, dx.data_ptr(),
                                           dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), need, st))
-        if stream is not None:
-            _used_on(stream, h, mean, rstd, dy, dh, dx, dgamma, dbeta, self.gamma)
         return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
 
 
@@ -361,29 +374,31 @@ def recurrence_forward(g, v, h0=None, starts=None, lens=None, stream=None):
     (slices of a wider tensor will do). h0: fp32 [batch, d]; starts: bool or uint8
     [batch, seq_len], nonzero where a packed document begins; lens: int32 [batch].
     Returns (h, h_last): h like g, h_last fp32 [batch, d], the state for the next call."""
+    if stream is not None:
+        return _call_on(stream, recurrence_forward, (g, v, h0, starts, lens))
     if g.dim() != 3:
         raise _invalid("g must be [batch, seq_len, d]")
     dev = g.device
-    st = _on(stream, dev)
+    st = _on(dev)
     h = torch.empty_like(g, memory_format=_DENSE)
     r = _recurrence(g, v, h, h0, starts, lens)
     last = torch.empty((r.batch, r.d), dtype=torch.float32, device=dev)
     ref = ctypes.byref(r)
     need = load().ipttt_recurrence_workspace_bytes(ref)
-    ws = _temp(need, dev, stream)
+    ws = _temp(need, dev)
     _check(load().ipttt_recurrence_forward(ref, last.data_ptr(), ws.data_ptr(), need, st))
-    if stream is not None:
-        _used_on(stream, g, v, h0, starts, lens, h, last)
     return h, last
 
 
 def recurrence_step(g, v, state, out=None, stream=None):
     """One token per sequence: g, v [batch, d], state fp32 [batch, d] or None (zero).
     Returns (h [batch, d], the new state); pass out=state to update it in place."""
+    if stream is not None:
+        return _call_on(stream, recurrence_step, (g, v, state, out))
     if g.dim() != 2:
         raise _invalid("g must be [batch, d]")
     dev = g.device
-    st = _on(stream, dev)
+    st = _on(dev)
     h = torch.empty_like(g, memory_format=_DENSE)
     r = _recurrence(g, v, h, state)
     if out is None:
@@ -392,8 +407,6 @@ def recurrence_step(g, v, state, out=None, stream=None):
     else:
         _dense("out", out, g.shape, torch.float32, dev)
     _check(load().ipttt_recurrence_step(ctypes.byref(r), out.data_ptr(), st))
-    if stream is not None:
-        _used_on(stream, g, v, state, h, out)
     return h, out
 
 
@@ -402,10 +415,12 @@ def recurrence_backward(g, v, h, dh, h0=None, dh_last=None, starts=None, lens=No
     """Gradients of recurrence_forward from its output h, dL/dh and dL/dh_last (fp32
     [batch, d] or None): {"dg", "dv", "dh0"}. dg and dv may be passed in (for
     example the two halves of one projection's gradient)."""
+    if stream is not None:
+        return _call_on(stream, recurrence_backward, (g, v, h, dh, h0, dh_last, starts, lens, dg, dv))
     if g.dim() != 3:
         raise _invalid("g must be [batch, seq_len, d]")
     shape, dtype, dev = g.shape, g.dtype, g.device
-    st = _on(stream, dev)
+    st = _on(dev)
     r = _recurrence(g, v, h, h0, starts, lens)
     dg = torch.empty_like(g, memory_format=_DENSE) if dg is None else dg
     dv = torch.empty_like(g, memory_format=_DENSE) if dv is None else dv
@@ -416,11 +431,9 @@ def recurrence_backward(g, v, h, dh, h0=None, dh_last=None, starts=None, lens=No
              for name, t in (("dh", dh), ("dg", dg), ("dv", dv))]
     ref = ctypes.byref(r)
     need = load().ipttt_recurrence_workspace_bytes(ref)
-    ws = _temp(need, dev, stream)
+    ws = _temp(need, dev)
     _check(load().ipttt_recurrence_backward(ref, views[0], _p(dh_last), views[1], views[2],
                                             dh0.data_ptr(), ws.data_ptr(), need, st))
-    if stream is not None:
-        _used_on(stream, g, v, h, dh, h0, dh_last, starts, lens, dg, dv, dh0)
     return {"dg": dg, "dv": dv, "dh0": dh0}
 
 
@@ -443,9 +456,11 @@ class FeedForward:
     def forward(self, x, save: bool = False, stream=None):
         """x: [..., d]. Returns y, or (y, a, u) with the pre-activations (fp32) for the
         backward."""
+        if stream is not None:
+            return _call_on(stream, self.forward, (x, save), (self.w_gate, self.w_up, self.w_down))
         d, dtype, dev = self.d, self.dtype, self.device
         xs = _rows("x", x, d, dtype, dev)
-        st = _on(stream, dev)
+        st = _on(dev)
         n = x.numel() // d
         y = torch.empty_like(x, memory_format=_DENSE)
         a = u = None
@@ -453,19 +468,19 @@ class FeedForward:
             a = torch.empty(x.shape[:-1] + (self.d_ff,), dtype=torch.float32, device=dev)
             u = torch.empty_like(a)
         need = load().ipttt_ff_workspace_bytes(self._ref, n)
-        ws = _temp(need, dev, stream)
+        ws = _temp(need, dev)
         _check(load().ipttt_ff_forward(self._ref, x.data_ptr(), xs, n, y.data_ptr(), d, _p(a), _p(u),
                                        ws.data_ptr(), need, st))
-        if stream is not None:
-            _used_on(stream, x, y, a, u, self.w_gate, self.w_up, self.w_down)
         return (y, a, u) if save else y
 
     def backward(self, x, a, u, dy, stream=None):
         """Gradients from dL/dy and the saved pre-activations: {"dx", "dw_gate", "dw_up",
         "dw_down"}, all in the weights' dtype."""
+        if stream is not None:
+            return _call_on(stream, self.backward, (x, a, u, dy), (self.w_gate, self.w_up, self.w_down))
         d, f, dtype, dev = self.d, self.d_ff, self.dtype, self.device
         xs = _rows("x", x, d, dtype, dev)
-        st = _on(stream, dev)
+        st = _on(dev)
         n = x.numel() // d
         ds = _rows("dy", dy, d, dtype, dev, n)
         for name, t in (("a", a), ("u", u)):
@@ -473,10 +488,8 @@ class FeedForward:
         dx = torch.empty_like(x, memory_format=_DENSE)
         dwg, dwu, dwd = (torch.empty_like(w) for w in (self.w_gate, self.w_up, self.w_down))
         need = load().ipttt_ff_backward_workspace_bytes(self._ref, n)
-        ws = _temp(need, dev, stream)
+        ws = _temp(need, dev)
         grads = FFGrads(dx.data_ptr(), d, dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr())
         _check(load().ipttt_ff_backward(self._ref, x.data_ptr(), xs, a.data_ptr(), u.data_ptr(),
                                         dy.data_ptr(), ds, n, ctypes.byref(grads), ws.data_ptr(), need, st))
-        if stream is not None:
-            _used_on(stream, x, a, u, dy, self.w_gate, self.w_up, self.w_down, dx, dwg, dwu, dwd)
         return {"dx": dx, "dw_gate": dwg, "dw_up": dwu, "dw_down": dwd}

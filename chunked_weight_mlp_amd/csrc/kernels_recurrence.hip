@@ -10,6 +10,15 @@
 // state that is not finite does not leak through 0 x inf). The backward runs the
 // same way from the last token to the first on the gradient of the state.
 // Few tokens (SEQ_MAX) are walked by one thread per channel pair instead.
+//
+// A gate that remembers has f within a few 2^-24 of 1, and a rounded f is wrong in what it
+// forgets, 1 - f, the same way at every token: at g = 12, 131072 tokens would leave a
+// state off by 7e-3. So what is handed on, from tile to tile and from call to call,
+// goes by 1 - f: a product of gates is kept as 1 minus itself while it is above a half
+// (Factor). Rounded factors serve over 16 tokens, a wave's or a walk's, where they are off
+// by 5e-7 at most.
+#include <float.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -20,13 +29,52 @@ namespace {
 
 using blk::Pack;
 
-// f = 1 / (1 + e^-x) and i = 1 - f = 1 / (1 + e^x), each to a few ulp: for x > 0
-// i is e^-x f (1 - f would cancel), else it is 1 - f (e^-x may overflow).
+// f = 1 / (1 + e^-x) and i = 1 - f = 1 / (1 + e^x): for x > 0 i is e^-x f (1 - f would
+// cancel), else it is 1 - f (e^-x may overflow). e^-x is off by about |x| 2^-24 of
+// itself, a rounding of x log2(e): so are i for x > 0 and f for x < 0 (8 ulp at |x| = 20,
+// 31 at 80).
 __device__ __forceinline__ void gate(float x, float &f, float &i) {
   const float e = __expf(-x);
   f = __builtin_amdgcn_rcpf(1.f + e);
   i = x > 0.f ? e * f : 1.f - f;
 }
+
+// s, or the largest value of its sign where it is infinite: what is then taken from an
+// infinite state leaves it what it is.
+__device__ __forceinline__ float finite(float s) {
+  return __builtin_amdgcn_fmed3f(s, -FLT_MAX, FLT_MAX);
+}
+
+// A Factor is a product A of gates: A itself up to 1/2, and above that -(1 - A), told
+// apart by the sign (-0 is 1). -1 stands for a document start between (kCut), past which
+// the state before counts for nothing.
+constexpr float kCut = -1.f;
+__device__ __forceinline__ bool sign_set(float a) { return (int)__builtin_bit_cast(uint32_t, a) < 0; }
+// A s + b (the factor no document start)
+__device__ __forceinline__ float affine(float a, float s, float b) {
+  const float x = fmaf(a, sign_set(a) ? finite(s) : s, b);
+  return sign_set(a) ? s + x : x;
+}
+// The state s through the map (a, b).
+__device__ __forceinline__ float through(float a, float b, float s) {
+  const float x = affine(a, s, b);
+  return a == kCut ? b : x;
+}
+// A product as it grows: itself, and the sum of what each gate took of it, which is 1
+// minus it.
+struct Product {
+  float p = 1.f, n = 0.f;
+  __device__ __forceinline__ void take(float f, float i) {
+    n = fmaf(i, p, n);
+    p *= f;
+  }
+  // the same for a Factor
+  __device__ __forceinline__ void times(float a) {
+    n = fmaf(sign_set(a) ? -a : 1.f - a, p, n);
+    p *= sign_set(a) ? 1.f + a : a;
+  }
+  __device__ __forceinline__ float factor() const { return p > 0.5f ? -n : p; }
+};
 
 // V channels from channel c of a row; channels at or past d read as zero.
 template <typename T, int V>
@@ -58,8 +106,8 @@ __device__ __forceinline__ int64_t seq_length(const RecArgs &a, int n) {
   return a.lens ? min(max((int64_t)a.lens[n], (int64_t)0), a.L) : a.L;
 }
 
-// One thread walks V channels of one sequence from its first token to its last,
-// U tokens' loads in flight.
+// One thread walks V channels of one sequence from its first token to its last, U tokens'
+// loads in flight, and makes the map of them all for the state it hands on.
 constexpr int SEQ_V = 2, SEQ_U = 8;
 
 template <typename T>
@@ -71,6 +119,11 @@ __global__ __launch_bounds__(64) void k_rec_seq_fwd(RecArgs a) {
   T *h = seq_of<T>(a.h, n);
   float s[SEQ_V] = {};
   if (a.h0) load_ch<float, SEQ_V>(a.h0 + (int64_t)n * a.d, c, a.d, s);
+  float s0[SEQ_V], q[SEQ_V] = {};
+  Product W[SEQ_V];
+  bool any = false;  // a document start
+#pragma unroll
+  for (int e = 0; e < SEQ_V; ++e) s0[e] = s[e];
   for (int64_t t0 = 0; t0 < len; t0 += SEQ_U) {
     float gv[SEQ_U][SEQ_V], vv[SEQ_U][SEQ_V];
     bool cut[SEQ_U];
@@ -90,11 +143,18 @@ __global__ __launch_bounds__(64) void k_rec_seq_fwd(RecArgs a) {
         gate(gv[u][e], f, i);
         const float b = i * vv[u][e];
         s[e] = cut[u] ? b : fmaf(f, s[e], b);
+        q[e] = cut[u] ? b : fmaf(f, q[e], b);
+        W[e].take(f, i);
       }
+      any = any || cut[u];
       store_ch<T, SEQ_V>(h + (t0 + u) * a.h.tok_stride, c, a.d, s);
     }
   }
-  if (a.h_last) store_ch<float, SEQ_V>(a.h_last + (int64_t)n * a.d, c, a.d, s);
+  if (a.h_last) {
+#pragma unroll
+    for (int e = 0; e < SEQ_V; ++e) s[e] = through(any ? kCut : W[e].factor(), q[e], s0[e]);
+    store_ch<float, SEQ_V>(a.h_last + (int64_t)n * a.d, c, a.d, s);
+  }
   const float zero[SEQ_V] = {};
   for (int64_t t = len; t < a.L; ++t) store_ch<T, SEQ_V>(h + t * a.h.tok_stride, c, a.d, zero);
 }
@@ -110,6 +170,11 @@ __global__ __launch_bounds__(64) void k_rec_seq_bwd(RecArgs a) {
   float h0[SEQ_V] = {}, s[SEQ_V] = {};  // s: gradient of the state after token t
   if (a.h0) load_ch<float, SEQ_V>(a.h0 + (int64_t)n * a.d, c, a.d, h0);
   if (a.dh_last) load_ch<float, SEQ_V>(a.dh_last + (int64_t)n * a.d, c, a.d, s);
+  float s0[SEQ_V], q[SEQ_V] = {};
+  Product W[SEQ_V];
+  bool any = false;  // a document start
+#pragma unroll
+  for (int e = 0; e < SEQ_V; ++e) s0[e] = s[e];
   const float zero[SEQ_V] = {};
   for (int64_t t = a.L - 1; t >= len; --t) {
     store_ch<T, SEQ_V>(dg + t * a.dg.tok_stride, c, a.d, zero);
@@ -141,12 +206,19 @@ __global__ __launch_bounds__(64) void k_rec_seq_bwd(RecArgs a) {
         ov[e] = i * delta;
         og[e] = delta * (prev - vv[u][e]) * (f * i);
         s[e] = cut[u] ? 0.f : f * delta;
+        q[e] = cut[u] ? 0.f : f * (dd[u][e] + q[e]);
+        W[e].take(f, i);
       }
+      any = any || cut[u];
       store_ch<T, SEQ_V>(dg + t * a.dg.tok_stride, c, a.d, og);
       store_ch<T, SEQ_V>(dv + t * a.dv.tok_stride, c, a.d, ov);
     }
   }
-  if (a.dh0) store_ch<float, SEQ_V>(a.dh0 + (int64_t)n * a.d, c, a.d, s);
+  if (a.dh0) {
+#pragma unroll
+    for (int e = 0; e < SEQ_V; ++e) s[e] = through(any ? kCut : W[e].factor(), q[e], s0[e]);
+    store_ch<float, SEQ_V>(a.dh0 + (int64_t)n * a.d, c, a.d, s);
+  }
 }
 
 // ---- tiles ---------------------------------------------------------------------------
@@ -155,10 +227,10 @@ __global__ __launch_bounds__(64) void k_rec_seq_bwd(RecArgs a) {
 //
 // Tiles of one (sequence, channel block) form a chain in groups of G. They meet in
 // slots of 8 bytes per channel: all ones (empty, written by k_rec_clear), then a map
-// (A, B), or (-1, s) for one that ignores the state: a value that validates itself,
-// so a slot needs no flag and no fence. A tile publishes its map. The last tile of a
-// group composes the group's maps in order, publishes that map, and then, once it
-// knows the state before the group, the state after it in the same slot. A tile's
+// (A, B), A as a Factor, or (kCut, s) for one that ignores the state: a value that
+// validates itself, so a slot needs no flag and no fence. A tile publishes its map. The
+// last tile of a group composes the group's maps in order, publishes that map, and then,
+// once it knows the state before the group, the state after it in the same slot. A tile's
 // state is that of its group's start, the nearest published state behind it with the
 // groups' maps in between applied in order, and the maps of the tiles before it in
 // its group, in order: the same operations whichever slots already held states, so
@@ -182,13 +254,6 @@ __device__ __forceinline__ void slot_put(uint64_t *p, float a, float b) {
 }
 __device__ __forceinline__ uint64_t slot_get(const uint64_t *p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// One map after another: the state s through map (a, b), and map (a, b) after (p, q).
-__device__ __forceinline__ float through(float a, float b, float s) { return a == -1.f ? b : fmaf(a, s, b); }
-__device__ __forceinline__ void after(float a, float b, float &p, float &q) {
-  q = a == -1.f ? b : fmaf(a, q, b);
-  p = a == -1.f || p == -1.f ? -1.f : a * p;
 }
 
 // A chain's place in the workspace. Tile `ord` of the launch's order and group g of
@@ -216,7 +281,7 @@ __device__ __forceinline__ void take_slots(uint64_t (&w)[LB][V], const uint64_t 
       for (int e = 0; e < V; ++e) {
         const auto ready = [&]() {
           return w[k][e] != kEmpty && (!state_last || t < count - 1 ||
-                                       __builtin_bit_cast(float, (uint32_t)w[k][e]) == -1.f);
+                                       __builtin_bit_cast(float, (uint32_t)w[k][e]) == kCut);
         };
         while (!ready() && polls < kMaxPolls) {
           __builtin_amdgcn_s_sleep(1);
@@ -234,7 +299,8 @@ __device__ __forceinline__ void take_slots(uint64_t (&w)[LB][V], const uint64_t 
 
 // The state before tile `ord`, the ci-th of its chain, whose own map is (A, B); state
 // holds the chain's initial state (used in its first group). `more`: tiles follow.
-// Called by the whole block with A, B valid in wave `pub`; every wave gets the state.
+// Called by the whole block with A, B valid in wave `pub`, which alone gets the state
+// (the other waves' instructions are the other block's time).
 template <int V, int NW>
 __device__ __forceinline__ void chain_state(const Chain &c, int64_t ord, int ci, bool more, int pub,
                                             const float (&A)[V], const float (&B)[V],
@@ -264,39 +330,96 @@ __device__ __forceinline__ void chain_state(const Chain &c, int64_t ord, int ci,
   take_slots<V, NW>(wt, tiles, c.step, idx, false, polls, mapA[0], mapB[0]);
   __syncthreads();
   float p[V], q[V];
-  if (wave == pub && last) {
+  if (wave == pub && last) {  // the group's map
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      p[e] = mapA[0][0][V * lane + e];
-      q[e] = mapB[0][0][V * lane + e];
-      for (int t = 1; t < G - 1; ++t) after(mapA[0][t][V * lane + e], mapB[0][t][V * lane + e], p[e], q[e]);
-      after(A[e], B[e], p[e], q[e]);
+      Product P;
+      bool cut = false;
+      q[e] = 0.f;
+      for (int t = 0; t < G; ++t) {
+        const float x = t < G - 1 ? mapA[0][t][V * lane + e] : A[e];
+        const float y = t < G - 1 ? mapB[0][t][V * lane + e] : B[e];
+        q[e] = through(x, y, q[e]);
+        P.times(x);
+        cut = cut || x == kCut;
+      }
+      p[e] = cut ? kCut : P.factor();
       if (g > 0) slot_put(c.group(g) + V * lane + e, p[e], q[e]);
     }
   }
   if (g > 0) {
     take_slots<V, NW>(wg, groups, -c.step, window, true, polls, mapA[1], mapB[1]);
     __syncthreads();
+  }
+  if (wave != pub) return;
+  if (g > 0) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const int ch = V * lane + e;
       int t = 0;
-      while (t < window - 1 && mapA[1][t][ch] != -1.f) ++t;
+      while (t < window - 1 && mapA[1][t][ch] != kCut) ++t;
       float s = mapB[1][t][ch];
-      for (--t; t >= 0; --t) s = fmaf(mapA[1][t][ch], s, mapB[1][t][ch]);
+      for (--t; t >= 0; --t) s = affine(mapA[1][t][ch], s, mapB[1][t][ch]);
       state[e] = s;
     }
   }
-  if (wave == pub && last) {
+  if (last) {
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      if (g == 0 || p[e] != -1.f)
-        slot_put(c.group(g) + V * lane + e, -1.f, through(p[e], q[e], state[e]));
+      if (g == 0 || p[e] != kCut)
+        slot_put(c.group(g) + V * lane + e, kCut, through(p[e], q[e], state[e]));
   }
 #pragma unroll
   for (int e = 0; e < V; ++e)
     for (int t = 0; t < idx; ++t)
       state[e] = through(mapA[0][t][V * lane + e], mapB[0][t][V * lane + e], state[e]);
+}
+
+// Composes the maps (sA, sB; sCut: with a document start) of a tile's waves, first to last
+// or, with `back`, last to first: (A, B) is all of them as one, and each wave's own is
+// replaced by the one of the waves before it.
+template <int V, int NW>
+__device__ __forceinline__ void compose_waves(float (&sA)[NW][64 * V], float (&sB)[NW][64 * V],
+                                              const int (&sCut)[NW], bool back, float (&A)[V],
+                                              float (&B)[V]) {
+  const int lane = threadIdx.x & 63;
+  Product P[V];
+  bool cut = false;
+#pragma unroll
+  for (int e = 0; e < V; ++e) B[e] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < NW; ++k) {
+    const int w = back ? NW - 1 - k : k;
+    const bool here = sCut[w] != 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      float &a = sA[w][V * lane + e], &b = sB[w][V * lane + e];
+      const float x = a, y = b;
+      a = cut ? kCut : P[e].factor();
+      b = B[e];
+      const float z = affine(x, B[e], y);
+      B[e] = here ? y : z;
+      P[e].times(x);
+    }
+    cut = cut || here;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) A[e] = cut ? kCut : P[e].factor();
+}
+
+// The state before each wave, from the tile's in wave `pub`, through the waves before it.
+template <int V, int NW>
+__device__ __forceinline__ void wave_state(const float (&sA)[NW][64 * V], const float (&sB)[NW][64 * V],
+                                           float (&sS)[64 * V], int pub, float (&s)[V]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave == pub) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) sS[V * lane + e] = s[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    s[e] = through(sA[wave][V * lane + e], sB[wave][V * lane + e], sS[V * lane + e]);
 }
 
 // The first of the V channels of a lane whose own ones start at channel c: c, or,
@@ -374,6 +497,7 @@ template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
   __shared__ float sA[NW][CH], sB[NW][CH], lA[2][NW * LB][CH], lB[2][NW * LB][CH];
+  __shared__ float sS[CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   if (tl.ord >= nt) return;
@@ -398,6 +522,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
   // FAST: all R tokens, whole packs and no document start, as most waves have it:
   // straight code.
   float P[R][V], hl[R][V];
+  Product W[V];
   const uint64_t cuts = start_bits<R>(a, n, tb, tb + cnt);
   const bool fast = cnt == R && d >= V && cuts == 0;
   const uint32_t at = (c < d ? c : 0) * (uint32_t)sizeof(T);
@@ -416,12 +541,9 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
         vr[r] = load_raw<T, V>(v + t * a.v.tok_stride, c, d);
       }
     }
-    float p[V], q[V];
+    float q[V] = {};
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      p[e] = 1.f;
-      q[e] = 0.f;
-    }
+    for (int e = 0; e < V; ++e) W[e] = Product();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (FAST || r < cnt) {
@@ -432,12 +554,12 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
           gate((float)gr[r].v[e], f, i);
           const float b = i * (float)vr[r].v[e];
           q[e] = cut ? b : fmaf(f, q[e], b);
-          p[e] *= f;
+          W[e].take(f, i);
         }
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        P[r][e] = p[e];
+        P[r][e] = W[e].p;
         hl[r][e] = q[e];
       }
     }
@@ -448,40 +570,16 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
     local(std::false_type());
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    sA[wave][V * lane + e] = P[R - 1][e];
+    sA[wave][V * lane + e] = W[e].factor();
     sB[wave][V * lane + e] = hl[R - 1][e];
   }
   if (lane == 0) sCut[wave] = cuts != 0;
   __syncthreads();
-  // the map of the waves in front of this one, and wave 0's of the whole tile
-  const int upto = wave == 0 ? NW : wave;
   float A[V], B[V];
-  bool cut = false;
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    A[e] = 1.f;
-    B[e] = 0.f;
-  }
-  for (int w = 0; w < upto; ++w) {
-    const bool k = sCut[w] != 0;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = sA[w][V * lane + e], y = sB[w][V * lane + e];
-      B[e] = k ? y : fmaf(x, B[e], y);
-      A[e] *= x;
-    }
-    cut = cut || k;
-  }
-  if (cut) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) A[e] = -1.f;
-  }
+  if (wave == 0) compose_waves<V, NW>(sA, sB, sCut, false, A, B);
   if (nt > 1)
     chain_state<V, NW>(chain_of<V>(a, tl, nt), tl.ord, (int)tl.ord, t0 + TT < len, 0, A, B, lA, lB, s);
-  if (wave > 0) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = through(A[e], B[e], s[e]);
-  }
+  wave_state<V, NW>(sA, sB, sS, 0, s);
   if (c >= d) return;
   float o[V] = {};
   if (fast) {
@@ -501,7 +599,11 @@ __global__ __launch_bounds__(64 * NW) void k_rec_fwd(RecArgs a, int nt) {
         store_ch<T, V>(h + (tb + r) * a.h.tok_stride, c, d, o);
       }
   }
-  if (a.h_last && cnt > 0 && tb + cnt == len) store_ch<float, V>(a.h_last + (int64_t)n * d, c, d, o);
+  if (a.h_last && cnt > 0 && tb + cnt == len) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = through(cuts ? kCut : W[e].factor(), hl[R - 1][e], s[e]);
+    store_ch<float, V>(a.h_last + (int64_t)n * d, c, d, s);
+  }
 }
 
 // The gradient G of the state before token t: G_t = f_t (dh_t + G_{t+1}), 0 at a
@@ -510,6 +612,7 @@ template <typename T, int V, int R, int NW>
 __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
   constexpr int TT = NW * R, CH = 64 * V;
   __shared__ float sA[NW][CH], sB[NW][CH], lA[2][NW * LB][CH], lB[2][NW * LB][CH];
+  __shared__ float sS[CH];
   __shared__ int sCut[NW];
   const Tile tl = next_tile<V>(a, nt);
   if (tl.ord >= nt) return;
@@ -537,12 +640,8 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
   const bool fast = cnt == R && d >= V && cuts == 0 && tb > 0;
   const uint32_t at = (c < d ? c : 0) * (uint32_t)sizeof(T);
   Pack<T, V> gr[R], dr[R], vr[R], pr[R];
-  float A[V], B[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    A[e] = 1.f;
-    B[e] = 0.f;
-  }
+  float A[V], B[V] = {}, own[V];
+  Product W[V];
   // FAST: all R tokens with a token before them, whole packs, no document start
   const auto local = [&](auto tag) __attribute__((always_inline)) {
     constexpr bool FAST = decltype(tag)::value;
@@ -579,7 +678,7 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
           float f, i;
           gate((float)gr[r].v[e], f, i);
           B[e] = k ? 0.f : f * ((float)dr[r].v[e] + B[e]);
-          A[e] *= f;
+          W[e].take(f, i);
         }
       }
   };
@@ -589,41 +688,22 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
     local(std::false_type());
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    sA[wave][V * lane + e] = A[e];
-    sB[wave][V * lane + e] = B[e];
+    sA[wave][V * lane + e] = W[e].factor();
+    sB[wave][V * lane + e] = own[e] = B[e];
   }
   if (lane == 0) sCut[wave] = cuts != 0;
   __syncthreads();
-  // the map of the waves behind this one, and the last wave's of the whole tile
-  const int down = wave == NW - 1 ? 0 : wave + 1;
-  bool cut = false;
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    A[e] = 1.f;
-    B[e] = 0.f;
-  }
-  for (int w = NW - 1; w >= down; --w) {
-    const bool k = sCut[w] != 0;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = sA[w][V * lane + e], y = sB[w][V * lane + e];
-      B[e] = k ? y : fmaf(x, B[e], y);
-      A[e] *= x;
-    }
-    cut = cut || k;
-  }
-  if (cut) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) A[e] = -1.f;
-  }
+  if (wave == NW - 1) compose_waves<V, NW>(sA, sB, sCut, true, A, B);
   if (nt > 1)
     chain_state<V, NW>(chain_of<V>(a, tl, nt), tl.ord, (int)((len - 1) / TT - tile), tile > 0, NW - 1, A,
                        B, lA, lB, s);
-  if (wave < NW - 1) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = through(A[e], B[e], s[e]);
-  }
+  wave_state<V, NW>(sA, sB, sS, NW - 1, s);
   if (c >= d) return;
+  if (a.dh0 && tb == 0) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) own[e] = through(cuts ? kCut : W[e].factor(), own[e], s[e]);
+    store_ch<float, V>(a.dh0 + (int64_t)n * d, c, d, own);
+  }
   const auto finish = [&](auto tag) __attribute__((always_inline)) {
     constexpr bool FAST = decltype(tag)::value;
 #pragma unroll
@@ -662,7 +742,6 @@ __global__ __launch_bounds__(64 * NW) void k_rec_bwd(RecArgs a, int nt) {
     finish(std::true_type());
   else
     finish(std::false_type());
-  if (a.dh0 && tb == 0) store_ch<float, V>(a.dh0 + (int64_t)n * d, c, d, s);
 }
 
 // Empties the slots and the tile counter.
@@ -677,14 +756,17 @@ __global__ __launch_bounds__(256) void k_rec_clear(uint64_t *ws, int64_t slots) 
 }
 
 // Tokens to which a thread walks its sequence itself (us, walked / in tiles, forward and
-// backward: 32 sequences of 16 x 2560 8.7 / 13.3 and 13.8 / 26.7, of 32 15.6 / 13.6 and 26.3 /
-// 27.5; one of 16 7.9 / 6.9 and 12.8 / 12.9, of 32 14.1 / 6.8 and 23.4 / 12.9).
+// backward: 32 sequences of 16 x 2560 9.5 / 14.0 and 15.8 / 29.5, of 32 17.2 / 14.5 and 31.7 /
+// 30.5; one of 16 8.8 / 7.8 and 14.4 / 14.4, of 32 14.8 / 7.8 and 25.9 / 14.4). The number of
+// sequences is left out: where it would decide, at 16 tokens of one, it is 1 us. Not
+// more than 16, by the rounded factors above.
 constexpr int64_t SEQ_MAX = 16;
 
 // Tokens per wave in the forward and the backward, waves, and channels per lane, all
 // measured on 128k x 2560 forward / 8 x 16k x 2048 backward, bf16, where a copy of
-// the same bytes takes 421 / 674 us. As here 483 / 601 us (with the
-// measured cases' gates 443 / 635). 8 tokens a wave 688 / 686,
+// the same bytes takes 421 / 674 us. As here 497 / 602 us (with the measured cases'
+// gates 460 / 633); before what is handed on went by 1 - f 483 / 601, and so the
+// variants: 8 tokens a wave 688 / 686,
 // 32 (forward) 476 but 28 us against 17 for 5 x 1237 x 331; 4 waves of 16 tokens 572 /
 // 640, 16 waves of 8 (backward) 760; 4 channels a lane 725 / 899 and up (registers).
 // Slots a wave reads (LB) 1, 2, 3: 483, 513, 530 (forward). Bound by HBM.

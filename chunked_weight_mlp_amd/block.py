@@ -279,8 +279,8 @@ class Norm:
     [d] in the activations' dtype (float32 or bfloat16), beta may be None."""
 
     def __init__(self, gamma, beta=None, eps: float = 1e-5):
-        if gamma.dim() != 1:
-            raise _invalid("gamma must be [d]")
+        if gamma.dim() != 1 or gamma.numel() == 0:
+            raise _invalid("gamma must be [d], d > 0")
         self.d, self.dtype, self.device = gamma.shape[0], gamma.dtype, gamma.device
         dt = _dtype_of(gamma)
         self.gamma = _dense("gamma", gamma, (self.d,), self.dtype, self.device)
@@ -442,8 +442,8 @@ class FeedForward:
     weights: w_gate, w_up [d_ff, d], w_down [d, d_ff], float32 or bfloat16."""
 
     def __init__(self, w_gate, w_up, w_down):
-        if w_gate.dim() != 2:
-            raise _invalid("w_gate must be [d_ff, d]")
+        if w_gate.dim() != 2 or w_gate.numel() == 0:
+            raise _invalid("w_gate must be [d_ff, d], both > 0")
         f, d = w_gate.shape
         self.d, self.d_ff, self.dtype, self.device = d, f, w_gate.dtype, w_gate.device
         dt = _dtype_of(w_gate)

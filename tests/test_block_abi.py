@@ -297,3 +297,10 @@ def test_refusals_under_asan(tmp_path):
     r = run([exe], env=dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0",
                             UBSAN_OPTIONS="print_stacktrace=1"), timeout=120)
     assert "all checks passed" in r.stdout
+
+
+def test_widths_of_zero_are_refused():
+    """An operator over no columns: an error of the library's kind, not of arithmetic."""
+    refused(INV, K.Norm, torch.ones(0), text="d > 0")
+    for f, d in ((0, 4), (6, 0), (0, 0)):
+        refused(INV, K.FeedForward, torch.ones(f, d), torch.ones(f, d), torch.ones(d, f), text="> 0")

@@ -304,3 +304,14 @@ def test_widths_of_zero_are_refused():
     refused(INV, K.Norm, torch.ones(0), text="d > 0")
     for f, d in ((0, 4), (6, 0), (0, 0)):
         refused(INV, K.FeedForward, torch.ones(f, d), torch.ones(f, d), torch.ones(d, f), text="> 0")
+
+
+@pytest.mark.parametrize("n,length,d", [(1, 1025, 128), (1, 9000, 130), (3, 1000, 130), (2, 131072, 2560),
+                                        (5, 4097, 33), (2, 20000, 64)])
+def test_recurrence_workspace_holds_the_groups_of_tiles(lib, n, length, d):
+    """Behind the tiles' slots lie those of their groups, of 8 tiles each and one begun."""
+    for dtype in (B.IPTTT_F32, B.IPTTT_BF16):
+        got = K.ipttt_recurrence_workspace_bytes(K.RecurrenceDesc(batch=n, d=d, seq_len=length, dtype=dtype))
+        tiles = -(-length // 128)
+        width = -(-d // 128) * 128 if d > 64 else 64
+        assert got >= 256 + 8 * (tiles + tiles // 8 + 1) * n * width

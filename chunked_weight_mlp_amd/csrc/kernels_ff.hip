@@ -1207,18 +1207,22 @@ bool few_forward(int elem, int d, int F, int64_t n) {
   if (d < 8 || F < 8) return false;  // pieces of 8 values along a row
   return n <= (elem == 4 || d % kStep || F % kStep ? 512 : 128) || n * d * F <= 1 << 29;
 }
-// The same for a backward, whose operands all need laying out. Measured (us, direct /
-// laid out), fp32: 250 x 671 at 333 tokens 30 / 59, at 2048 71 / 108; 512 x 2048 at 1024
-// 138 / 175; 1024 x 4096 at 64 68 / 140, at 512 241 / 283, at 1024 449 / 428; 2048 x 8192 at
-// 64 174 / 421, at 512 924 / 842. bf16: 250 x 671 at 2048 38 / 41; 512 x 2048 at 1024 51 / 57;
-// 1024 x 4096 at 64 39 / 53, at 512 70 / 75, at 1024 121 / 112; 2048 x 8192 at 64 74 / 135, at
-// 200 133 / 155, at 512 232 / 203; 1999 x 3001, where 16 bytes start at any element, at
-// 64 56 / 80, at 333 107 / 107, at 512 127 / 117.
+// The same for a backward, whose operands all need laying out. Laying out the weights
+// takes their bytes' time whatever the tokens, so with large ones the two cross at one
+// number of tokens; with small ones, where launches count, at one n d d_ff. Measured (us,
+// direct / laid out), bf16: 2048 x 8192 at 64 tokens 72 / 131, at 200 128 / 151, at 320 156 /
+// 165, at 512 226 / 194; 2560 x 9728 at 200 206 / 237, at 320 238 / 256, at 512 348 / 311; 1024
+// x 4096 at 64 39 / 51, at 512 67 / 74, at 768 91 / 85; 512 x 2048 at 1024 51 / 56, at 3200 115 /
+// 112; 256 x 1024 at 6000 69 / 77; 1999 x 3001, where 16 bytes start at any element, at 320
+// 89 / 102, at 512 124 / 111; 1000 x 1500 at 2000 101 / 101. fp32: 2048 x 8192 at 64 167 / 421,
+// at 320 610 / 642, at 512 904 / 822; 2560 x 9728 at 320 875 / 916; 1024 x 4096 at 640 310 / 307,
+// at 1024 457 / 413; 512 x 2048 at 4100 512 / 527; 1000 x 1500 at 1400 279 / 275, at 2600 476 /
+// 414.
 bool few_backward(int elem, int d, int F, int64_t n) {
   if (d < 8 || F < 8) return false;  // pieces of 8 values along a row
   const int64_t unit = (int64_t)1 << 30;
   const int64_t most = elem == 4 ? 4 * unit - 1 : d % 8 || F % 8 ? 2 * unit : 3 * unit;
-  return n <= most / ((int64_t)d * F);
+  return n <= 320 || n <= most / ((int64_t)d * F);
 }
 int direct_parts(int64_t tiles, int64_t steps) {
   const int64_t s = std::min<int64_t>({2 * kCUs / std::max<int64_t>(tiles, 1), steps / 4, 64});

@@ -315,3 +315,16 @@ def test_recurrence_workspace_holds_the_groups_of_tiles(lib, n, length, d):
         tiles = -(-length // 128)
         width = -(-d // 128) * 128 if d > 64 else 64
         assert got >= 256 + 8 * (tiles + tiles // 8 + 1) * n * width
+
+
+@pytest.mark.parametrize("dtype", [B.IPTTT_F32, B.IPTTT_BF16])
+@pytest.mark.parametrize("d,f", [(1024, 4096), (2048, 8192), (2560, 9728), (4096, 16384)])
+def test_few_tokens_backward_lays_out_no_weights(lib, d, f, dtype):
+    """To 320 tokens of any size the products take the weights as they lie, which is the
+    faster of the two ways there: the workspace holds no copies of them."""
+    desc, e = K.FFDesc(d=d, d_ff=f, dtype=dtype), 2 if dtype == B.IPTTT_BF16 else 4
+    for n in (1, 64, 129, 193, 256, 320):
+        z, sums = 3 * n * f * e, 64 * 4 * n * (d + 8)   # dA, dU, z; dx's partial sums
+        assert K.ipttt_ff_backward_workspace_bytes(desc, n) <= z + sums + 4096
+    # and with very many they are copied (bf16) or split into planes (fp32)
+    assert K.ipttt_ff_backward_workspace_bytes(desc, 1 << 15) >= 3 * d * f * (2 if e == 2 else 6)

@@ -124,3 +124,10 @@ def test_large_tiles_in_the_down_product(dtype, n, d, f):
     (2048, 1024, 2048, 0)])
 def test_bounds_of_the_arithmetic(dtype, n, d, f, pad):
     check(n, d, f, dtype, pad=pad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [200, 320, 321])
+def test_both_sides_of_the_few_token_limit(n, dtype):
+    """A backward of up to 320 tokens takes the weights as they lie, beyond them a copy."""
+    check(n, 2048, 8192, dtype)

@@ -12,6 +12,9 @@ memory. Such a stream must already be ordered after whatever produced the inputs
 whoever uses the outputs on another stream after this one, as with any torch tensor;
 that neither's memory is handed out again too early, on `stream` or on the stream
 that was current, is taken care of.
+
+Outputs are detached: the operators record nothing for torch's autograd, and an input
+that requires a gradient is used by its value. Their `backward` calls give the gradients.
 """
 from __future__ import annotations
 
@@ -414,7 +417,8 @@ def recurrence_backward(g, v, h, dh, h0=None, dh_last=None, starts=None, lens=No
                         stream=None):
     """Gradients of recurrence_forward from its output h, dL/dh and dL/dh_last (fp32
     [batch, d] or None): {"dg", "dv", "dh0"}. dg and dv may be passed in (for
-    example the two halves of one projection's gradient)."""
+    example the two halves of one projection's gradient); they must overlap neither
+    each other nor an input."""
     if stream is not None:
         return _call_on(stream, recurrence_backward, (g, v, h, dh, h0, dh_last, starts, lens, dg, dv))
     if g.dim() != 3:

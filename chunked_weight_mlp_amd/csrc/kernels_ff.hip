@@ -20,10 +20,19 @@
 // 2^-24 of a product: fp32 accuracy at six times the bf16 work, against
 // 1/16 of the bf16 rate for the fp32 MFMA.
 //
-// k_ff_gemm is bound by LDS bandwidth (each MFMA's operands pass through it): 16384
-// tokens of 2560 x 9728 in bf16 take 1.90 ms, 1290 TFLOP/s, where a large library
-// product reaches 1581; its epilogues' traffic comes on top (the dz product of 8192
-// tokens of 2048 x 8192 has 1.2 GB of it, 300 of its 530 us).
+// k_ff_gemm's large tiles keep the matrix cores busy for 58 to 68 % of the cycles, and LDS,
+// which each MFMA's operands pass through, for as many: its reads take half of them and
+// the copies into it a sixth, with no bank conflicts. Neither is full: one block fills a
+// CU, so that one's barriers and epilogue pause both; and under this load the clock is
+// 1.5 to 1.9 GHz of 2.4. 16384 tokens of 2560 x 9728 in bf16 take 1.90 ms, 1290 TFLOP/s,
+// where a large library product reaches 1581. The epilogues' traffic comes on top: the dz
+// product of 8192 tokens of 2048 x 8192 has 1.2 GB of it and takes 515 us, a quarter of
+// them busy with MFMAs.
+//
+// In bf16 what goes from one product into the next (z, and dA and dU) is rounded to bf16,
+// in every kernel alike, as the operand of an MFMA has to be: results are off by 2.35e-3
+// where rounding the exact ones is 1.7e-3. Two bf16 planes of it would save that at
+// twice the time of the products it enters; fp32 keeps it all, at six times the time.
 #include <algorithm>
 #include <type_traits>
 
@@ -959,7 +968,7 @@ struct EpiZDirect {
   }
 };
 
-// dz -> dA, dU and z by token, as they are.
+// dz -> dA, dU and z by token, in T, as the products after it take them.
 template <typename T>
 struct EpiDzDirect {
   struct In {

@@ -305,13 +305,14 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const float *__restrict__ pa
 
 // Waves a row is spread over. Forward: one wave to 4096 columns, four beyond;
 // with too few rows to fill the GPU a row takes four waves from 1024 columns on (us, one
-// wave a row / four, with the residual add: 8 x 2560 4.5 / 3.6, 256 x 2560 5.0 / 4.0, 1024 x
-// 1024 4.0 / 4.1, 2048 x 2560 7.9 / 8.7, 32768 x 2560 96 / 112, 32768 x 512 19 / 43).
+// wave a row / four, with the residual add, inputs and outputs not in cache: 8 x 2560 4.8 /
+// 4.4, 256 x 2560 5.9 / 4.9, 1024 x 1024 5.0 / 5.2, 2048 x 2560 13.0 / 13.0, 32768 x 2560 122 /
+// 125, 32768 x 512 27 / 64).
 int fwd_waves(int d, int64_t n) { return d > 4096 || (d >= 1024 && n <= 1024) ? 4 : 1; }
 // Backward: a lane also holds its columns' sums, so a wave takes 2560 columns at
 // most, and each wave should walk several rows per sum it writes (one wave a row
-// against four: 131072 x 2048 412 and 419 us, 65536 x 2560 276 and 318, 262144 x 639
-// 495 and 737, but 4096 x 2560 44 and 27).
+// against four: 131072 x 2048 390 and 416 us, 65536 x 2560 267 and 249, 262144 x 639 484
+// and 1262, but 4096 x 2560 39 and 22).
 int bwd_waves(int d, int64_t n) {
   if (d > 8192) return 8;
   return d > 2560 || (d > 512 && n < 16384) ? 4 : 1;

@@ -22,7 +22,8 @@
  * nearest even. Row and token strides are in elements, at least the width d
  * (so a tensor may be a slice of a wider one), and may be odd; pointers need
  * the alignment of their element type, except where a call says 16 bytes.
- * Outputs must not overlap inputs unless said otherwise.
+ * Outputs must not overlap inputs unless said otherwise. In bf16 the feed-forward
+ * block also rounds what passes from one of its products to the next.
  */
 #ifndef IPTTT_BLOCK_H
 #define IPTTT_BLOCK_H
@@ -91,6 +92,11 @@ typedef struct {
   const float *h0;       /* [batch][d] or NULL (zero)                           */
 } ipttt_recurrence;
 
+/* Inside a long sequence blocks of tokens wait for the state of the blocks before
+ * them, which run already. The wait is bounded: one that were to last a second
+ * (another stream writing to the call's workspace, say) ends in NaN results, which
+ * the status, long returned by then, does not show. */
+
 /* Workspace of the forward and of the backward (the same), 0 if a size is
  * invalid; short sequences need none and get a minimum. Pointers in `r` are
  * not read. The workspace must be 256-byte aligned. */
@@ -109,7 +115,8 @@ ipttt_status ipttt_recurrence_step(const ipttt_recurrence *r, float *state, void
  * the last token):
  *   dv_t = (1 - f_t) D_t,  dg_t = D_t (h_{t-1} - v_t) f_t (1 - f_t)
  *   dh0 = f_0 D_0 (0 at a document start), [batch][d] or NULL
- * h is the forward's output. dg and dv are zero past a sequence's length. */
+ * h is the forward's output. dg and dv are zero past a sequence's length; they
+ * overlap neither each other nor an input. */
 ipttt_status ipttt_recurrence_backward(const ipttt_recurrence *r, const ipttt_view *dh,
                                        const float *dh_last, const ipttt_view *dg,
                                        const ipttt_view *dv, float *dh0, void *workspace,

@@ -24,7 +24,7 @@
 // which each MFMA's operands pass through, for as many: its reads take half of them and
 // the copies into it a sixth, with no bank conflicts. Neither is full: one block fills a
 // CU, so that one's barriers and epilogue pause both; and under this load the clock is
-// 1.5 to 1.9 GHz of 2.4. 16384 tokens of 2560 x 9728 in bf16 take 1.90 ms, 1290 TFLOP/s,
+// 1.5 to 1.9 GHz of 2.4. 16384 tokens of 2560 x 9728 in bf16 take 1.9 ms, 1260 TFLOP/s,
 // where a large library product reaches 1581. The epilogues' traffic comes on top: the dz
 // product of 8192 tokens of 2048 x 8192 has 1.2 GB of it and takes 515 us, a quarter of
 // them busy with MFMAs.

@@ -70,7 +70,9 @@ ipttt_status ipttt_norm_backward(const ipttt_norm_desc *desc, const void *h, int
  *   f_t = 1 / (1 + e^-g_t)
  *   h_t = f_t h_{t-1} + (1 - f_t) v_t,   h_{-1} = h0
  * starts[t] != 0 marks the first token of a packed document: h_{t-1} counts as
- * zero there, whatever it holds (the layer's reset of W at document starts).
+ * zero there, whatever it holds (the layer's reset of W at document starts). A
+ * state that is not finite stays so until then, but an infinite one may become NaN
+ * where gates forget it (their product over 16 tokens can be zero in fp32).
  * lens[n] (clamped to 0 .. seq_len) ends sequence n: past it nothing is read
  * for the result, outputs are zero, and the last state is the one after token
  * lens[n] - 1 (h0 for length zero). */

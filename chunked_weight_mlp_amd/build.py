@@ -1,6 +1,6 @@
 """Builds the libraries in-tree with hipcc for gfx950 (no JIT, no site-packages install):
-  libipttt.so        the layer (include/ipttt.h) and the operators around it
-                     (include/ipttt_block.h)
+  libipttt.so        the layer (include/ipttt.h), the operators around it
+                     (include/ipttt_block.h) and attention (include/ipttt_attention.h)
   libipttt_probe.so  measurement-only micro-benchmarks (include/ipttt_probe.h)
 Host and device code compile with -Wall -Wextra -Werror."""
 from __future__ import annotations
@@ -18,7 +18,8 @@ PROBE_LIB = os.path.join(HERE, "libipttt_probe.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["ipttt.cpp", "kernels_generic.hip", "kernels_mfma.hip", "kernels_decode.hip",
            "kernels_backward.hip", "scratch.hip", "block.cpp", "kernels_norm.hip",
-           "kernels_recurrence.hip", "kernels_ff.hip"]
+           "kernels_recurrence.hip", "kernels_ff.hip", "attention.cpp", "kernels_heads.hip",
+           "kernels_attention.hip", "kernels_step.hip"]
 PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"
 FLAGS = [

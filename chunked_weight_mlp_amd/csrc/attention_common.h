@@ -1,0 +1,207 @@
+// Building blocks of the attention kernels (gfx950): LDS tiles of heads' rows, the MFMA
+// operands read from them, and the sequences of a packed batch. Device code only.
+//
+// All products are 32x32 MFMA tiles with 16 values of the summed index a step. Lane l
+// has half h = l / 32 and column l % 32:
+//   operand        8 values of row (column) l % 32: 8 h .. 8 h + 7 of the step's 16
+//   result         16 values of column l % 32: rows 8 (i / 4) + 4 h + i % 4, i < 16
+// Scores are computed so that a result's column is the row of the next product's other
+// operand: the 8 results i = 8 s .. 8 s + 7 of a lane are then its operand values of
+// step s, for the summed index in the order 16 s + 8 (j / 4) + 4 h + j % 4, j < 8, and
+// the partner operand is read from LDS in the same order (col_frag). Nothing moves
+// between lanes. In fp32 a step is 8 products of 2 values each, of the same shape.
+#pragma once
+
+#include <type_traits>
+
+#include "attention_internal.h"
+#include "block_internal.h"
+#include "mfma_common.h"
+
+namespace ipttt {
+namespace attn {
+
+using mfma::bf16x8;
+using mfma::f32x16;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct f32x8 {
+  float v[8];
+};
+template <typename T>
+struct FragOf;
+template <>
+struct FragOf<__bf16> {
+  typedef bf16x8 type;
+};
+template <>
+struct FragOf<float> {
+  typedef f32x8 type;
+};
+template <typename T>
+using Frag = typename FragOf<T>::type;
+
+__device__ __forceinline__ f32x16 mma(const bf16x8 &a, const bf16x8 &b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(const f32x8 &a, const f32x8 &b, f32x16 c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], c, 0, 0, 0);
+  return c;
+}
+// Results 8 s .. 8 s + 7 as an operand (bf16: rounded to nearest even).
+template <typename T>
+__device__ __forceinline__ Frag<T> as_operand(const f32x16 &x, int s) {
+  Frag<T> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (std::is_same<T, float>::value) f.v[j] = x[8 * s + j];
+    else f[j] = (__bf16)x[8 * s + j];
+  }
+  return f;
+}
+template <typename T>
+__device__ __forceinline__ Frag<T> zero_frag() {
+  Frag<T> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (std::is_same<T, float>::value) f.v[j] = 0.f;
+    else f[j] = (__bf16)0.f;
+  }
+  return f;
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+// The other half's value of the same column.
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+
+// A tile of rows of DP channels (64 or 128, at least head_dim; the rest zero) in LDS, in
+// pieces of 16 bytes. Piece p of row r is at place p ^ swizzle(r): the 16 rows that one
+// step of a row_frag reads at one piece, and the 4 rows x 4 pieces that one of a col_frag
+// reads, then fall on distinct banks.
+template <typename T, int DP>
+struct Tile {
+  static constexpr int PE = 16 / sizeof(T);  // elements a piece
+  static constexpr int NP = DP / PE;         // pieces a row: 8, 16 or 32
+  static constexpr int STEPS = DP / 16;
+  static_assert(NP >= 8, "rows of at least 128 bytes");
+  __device__ static __forceinline__ int swizzle(int r) {
+    if constexpr (NP >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+    else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  }
+  __device__ static __forceinline__ int at(int r, int p) { return r * DP + ((p ^ swizzle(r)) * PE); }
+
+  // Operand values: channels 16 s + 8 h .. + 7 of row r.
+  __device__ static __forceinline__ Frag<T> row_frag(const T *tile, int r, int s, int h) {
+    if constexpr (std::is_same<T, float>::value) {
+      f32x8 f;
+      *(float4 *)&f.v[0] = *(const float4 *)(tile + at(r, 4 * s + 2 * h));
+      *(float4 *)&f.v[4] = *(const float4 *)(tile + at(r, 4 * s + 2 * h + 1));
+      return f;
+    } else {
+      return *(const bf16x8 *)(tile + at(r, 2 * s + h));
+    }
+  }
+  // Operand values: channel c0 + l % 32 of rows r0 + 8 (j / 4) + 4 h + j % 4, j < 8
+  // (r0 a multiple of 16). In bf16 by two transposing reads: 16 lanes read 4 rows x 16
+  // channels and each gets one channel of the 4 rows.
+  __device__ static __forceinline__ Frag<T> col_frag(const T *tile, int r0, int c0, int l) {
+    if constexpr (std::is_same<T, float>::value) {
+      f32x8 f;
+      const int c = c0 + (l & 31);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f.v[j] = tile[at(r0 + 8 * (j / 4) + 4 * (l >> 5) + j % 4, c / PE) + c % PE];
+      return f;
+    } else {
+      const int r = r0 + 4 * (l >> 5) + ((l & 15) >> 2);
+      const int c = c0 + 16 * ((l >> 4) & 1) + 4 * (l & 3);
+      const mfma::v4i16 lo = mfma::ds_read_tr16(tile + at(r, c / 8) + c % 8);
+      const mfma::v4i16 hi = mfma::ds_read_tr16(tile + at(r + 8, c / 8) + c % 8);
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// Elements c .. c + N - 1 of a row of dh, zero behind it. Rows start anywhere.
+template <typename T, int N>
+__device__ __forceinline__ void load_some(const T *row, int c, int dh, T (&v)[N]) {
+  if (c + N <= dh) {
+    const blk::Pack<T, N> k = *(const blk::Pack<T, N> *)(row + c);
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = k.v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = c + e < dh ? row[c + e] : (T)0.f;
+  }
+}
+// The operand of a row in global memory: channels 16 s + 8 h .. + 7.
+template <typename T>
+__device__ __forceinline__ Frag<T> load_frag(const T *row, int s, int h, int dh) {
+  T v[8];
+  load_some<T, 8>(row, 16 * s + 8 * h, dh, v);
+  Frag<T> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (std::is_same<T, float>::value) f.v[j] = v[j];
+    else f[j] = v[j];
+  }
+  return f;
+}
+
+// Scores are kept without the scale, whose size enters with the exponent (log2_scale); its
+// sign is that of the operand held in registers. A scale of 0 is that of zeros.
+__device__ __forceinline__ float log2_scale(float scale) {
+  return scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
+}
+template <typename T>
+__device__ __forceinline__ Frag<T> with_sign(Frag<T> f, float scale) {
+  if (scale > 0.f) return f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (std::is_same<T, float>::value) f.v[j] = scale == 0.f ? 0.f : -f.v[j];
+    else f[j] = scale == 0.f ? (__bf16)0.f : -f[j];
+  }
+  return f;
+}
+
+// ---- the sequences of a packed batch -------------------------------------------------
+// Offset i of a batch as the operators read it: the first is 0, all are within n (none
+// given: one sequence).
+__device__ __forceinline__ int64_t offset_of(const int32_t *off, int i, int64_t n) {
+  if (i <= 0) return 0;
+  if (!off) return n;
+  const int64_t v = off[i];
+  return v < 0 ? 0 : v > n ? n : v;
+}
+// One sequence's rows, of which sequence `batch` is what lies behind the last one.
+struct Rows {
+  int64_t start;
+  int len;
+};
+__device__ __forceinline__ Rows rows_of(const int32_t *off, int s, int batch, int64_t n) {
+  const int64_t b = batch ? offset_of(off, s, n) : 0;
+  const int64_t e = s < batch ? offset_of(off, s + 1, n) : n;
+  return Rows{b, (int)(e > b ? e - b : 0)};
+}
+// Tiles of at most M rows that lie in one sequence, without a table of them: sequence s
+// has the numbers from start / M + s on, which is enough for any start and length, and
+// n / M + batch + 1 in all. Some are empty. All 64 lanes take part.
+inline int64_t tiles_of(int64_t n, int M, int batch) { return n / M + batch + 1; }
+__device__ __forceinline__ int sequence_of(const int32_t *off, int batch, int64_t n, int M,
+                                           int64_t tile, int lane) {
+  int s = 0;
+  for (int base = 1; base <= batch; base += 64) {
+    const int i = base + lane;
+    const bool before = i <= batch && offset_of(off, i, n) / M + i <= tile;
+    const int k = __popcll(__ballot(before));
+    s += k;
+    if (k < 64) break;
+  }
+  return s;
+}
+
+}  // namespace attn
+}  // namespace ipttt

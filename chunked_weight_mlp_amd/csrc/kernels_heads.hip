@@ -1,0 +1,410 @@
+// Norms of queries and keys for each head with the rotation by position (gfx950).
+//
+// A head's channels are held as pairs (a, b): the rotated pairs first, then the
+// others two by two with the angle 0, so that one formula serves all of them:
+//   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin),  n = x r gamma.
+// A wave takes one token: its 64 lanes compute the token's (at most 64) sines and
+// cosines once, pass them on through LDS, and then go over the token's heads, some
+// lanes a head and several heads at a time; each lane holds W consecutive pairs, two
+// loads of W elements (one of 2 W where the pairs are neighbours). Every element is
+// read once and written once: HBM bounds the large sizes, one kernel's latency the
+// small ones, where a token's heads are spread over several waves.
+#include <type_traits>
+
+#include "attention_internal.h"
+#include "block_internal.h"
+
+namespace ipttt {
+namespace {
+
+using blk::Pack;
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+
+// How a head's channels fall to lanes.
+struct Split {
+  int r2;     // rotated pairs
+  int pairs;  // all pairs
+  int half;   // distance of a and b in the channels that are not rotated
+  int lanes;  // lanes a head: a power of 2, of which pairs / W hold something
+};
+
+// The largest run of pairs that neither crosses the end of the rotated ones nor that
+// of the head, up to 16 bytes a load.
+int run_of(int dh, int rotary, int most) {
+  if (dh % 2) return 1;
+  for (int w = most; w > 1; w /= 2)
+    if ((rotary / 2) % w == 0 && ((dh - rotary) / 2) % w == 0) return w;
+  return 1;
+}
+Split split_of(const HeadArgs &a, int w) {
+  Split s;
+  s.r2 = a.rotary / 2;
+  s.half = (a.dh - a.rotary + 1) / 2;
+  s.pairs = s.r2 + s.half;
+  s.lanes = 1;
+  while (s.lanes * w < s.pairs) s.lanes *= 2;
+  return s;
+}
+
+// A lane's place in a head: the first of its W pairs, and where their channels are.
+template <int W, bool IL>
+struct Place {
+  int pair, ca, cb;
+  bool on, has_b;  // anything here; the b of a lone last channel is missing (W = 1)
+  __device__ __forceinline__ Place(const Split &s, int dh, int lane) {
+    pair = (lane & (s.lanes - 1)) * W;
+    on = pair < s.pairs;
+    const int r = 2 * s.r2;
+    if (IL) {
+      ca = 2 * pair;
+      cb = ca + 1;
+    } else if (pair < s.r2) {
+      ca = pair;
+      cb = pair + s.r2;
+    } else {
+      ca = r + pair - s.r2;
+      cb = ca + s.half;
+    }
+    has_b = cb < dh;
+  }
+};
+
+template <typename T, int W, bool IL>
+__device__ __forceinline__ void load_pairs(const T *row, const Place<W, IL> &p, float (&a)[W],
+                                           float (&b)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; ++e) a[e] = b[e] = 0.f;
+  if (!p.on) return;
+  if constexpr (W == 1) {
+    a[0] = (float)row[p.ca];
+    if (p.has_b) b[0] = (float)row[p.cb];
+  } else if constexpr (IL) {
+    float v[2 * W];
+    blk::load_pack<T, 2 * W>(row + p.ca, v);
+#pragma unroll
+    for (int e = 0; e < W; ++e) a[e] = v[2 * e], b[e] = v[2 * e + 1];
+  } else {
+    blk::load_pack<T, W>(row + p.ca, a);
+    blk::load_pack<T, W>(row + p.cb, b);
+  }
+}
+template <typename T, int W, bool IL>
+__device__ __forceinline__ void store_pairs(T *row, const Place<W, IL> &p, const float (&a)[W],
+                                            const float (&b)[W]) {
+  if (!p.on) return;
+  if constexpr (W == 1) {
+    row[p.ca] = (T)a[0];
+    if (p.has_b) row[p.cb] = (T)b[0];
+  } else if constexpr (IL) {
+    float v[2 * W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[2 * e] = a[e], v[2 * e + 1] = b[e];
+    blk::store_pack<T, 2 * W>(row + p.ca, v);
+  } else {
+    blk::store_pack<T, W>(row + p.ca, a);
+    blk::store_pack<T, W>(row + p.cb, b);
+  }
+}
+
+// Sum over the lanes of one head.
+__device__ __forceinline__ float head_sum(float v, int lanes) {
+  for (int m = lanes >> 1; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// cos and sin of a token's pairs for this lane. The angle pos inv_freq is reduced to a
+// fraction of a turn in 64 bits: at position 2^20 it has 20 bits before the point,
+// which 32 bits would take from the angle. cs: this wave's 64 places in LDS.
+template <int W>
+__device__ __forceinline__ void angles(const double *inv_freq, int r2, int pos, int lane, int pair,
+                                       float2 *cs, float (&c)[W], float (&s)[W]) {
+  float2 v = make_float2(1.f, 0.f);
+  if (lane < r2) {
+    const double turns = (double)pos * inv_freq[lane] * 0.15915494309189533577;
+    sincospif(2.f * (float)(turns - rint(turns)), &v.y, &v.x);
+  }
+  // one wave's own places: its LDS operations keep their order
+  __builtin_amdgcn_wave_barrier();
+  cs[lane] = v;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    const float2 u = cs[(pair + e) & 63];
+    c[e] = u.x;
+    s[e] = u.y;
+  }
+}
+
+template <typename T, int W, bool IL>
+__device__ __forceinline__ void load_gamma(const T *g, const Place<W, IL> &p, float (&a)[W],
+                                           float (&b)[W]) {
+  if (g) {
+    load_pairs<T, W, IL>(g, p, a, b);
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e) a[e] = b[e] = 1.f;
+  }
+}
+
+// The page's row of a new token, or null.
+template <typename T>
+__device__ __forceinline__ T *cache_row(const HeadArgs &a, void *base, int64_t t, int pos) {
+  const int64_t seq = a.seqs ? a.seqs[t] : t;
+  if (seq < 0 || seq >= a.table.batch || pos < 0) return nullptr;
+  const int ps = a.cache.page_size, at = pos / ps;
+  if (at >= a.table.width) return nullptr;
+  const int page = a.table.p[seq * a.table.stride + at];
+  if (page < 0 || page >= a.cache.pages) return nullptr;
+  return (T *)base + ((int64_t)page * a.hk * ps + (pos - at * ps)) * a.dh;
+}
+
+// slices: waves a token, each taking every slices-th batch of heads.
+template <typename T, int W, bool IL, bool APPEND>
+__global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a, Split s, int slices) {
+  __shared__ float2 cs[kThreads];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t unit = blk::block_id() * kWaves + wave;
+  const int64_t t = unit / slices;
+  const int slice = (int)(unit - t * slices);
+  if (t >= a.n) return;
+  const Place<W, IL> p(s, a.dh, lane);
+  const int pos = a.pos[t];
+  T *kc = nullptr, *vc = nullptr;
+  const int64_t cache_head = APPEND ? (int64_t)a.cache.page_size * a.dh : 0;
+  if constexpr (APPEND) {
+    kc = cache_row<T>(a, a.cache.k, t, pos);
+    vc = cache_row<T>(a, a.cache.v, t, pos);
+  }
+  float gq[2][W], gk[2][W];
+  load_gamma<T, W, IL>((const T *)a.q_gamma, p, gq[0], gq[1]);
+  load_gamma<T, W, IL>((const T *)a.k_gamma, p, gk[0], gk[1]);
+  const int at_once = 64 / s.lanes, sub = lane / s.lanes;
+  const int rows = a.hq + a.hk + (APPEND ? a.hk : 0);
+  const float inv_d = 1.f / (float)a.dh;
+  float c[W], sn[W];
+  angles<W>(a.inv_freq, s.r2, pos, lane, p.pair, cs + 64 * wave, c, sn);
+  for (int base = slice * at_once; base < rows; base += slices * at_once) {
+    const int h = base + sub;
+    const bool live = h < rows, is_q = h < a.hq, is_v = h >= a.hq + a.hk;
+    const T *src = nullptr;
+    T *dst = nullptr;
+    if (is_q) {
+      src = (const T *)a.q.p + t * a.q.tok_stride + h * a.q.head_stride;
+      dst = (T *)a.q_out.p + t * a.q_out.tok_stride + h * a.q_out.head_stride;
+    } else if (!is_v) {
+      const int hh = h - a.hq;
+      src = (const T *)a.k.p + t * a.k.tok_stride + hh * a.k.head_stride;
+      if constexpr (APPEND)
+        dst = kc ? kc + hh * cache_head : nullptr;
+      else
+        dst = (T *)a.k_out.p + t * a.k_out.tok_stride + hh * a.k_out.head_stride;
+    } else if (APPEND && live) {
+      const int hh = h - a.hq - a.hk;
+      src = (const T *)a.v.p + t * a.v.tok_stride + hh * a.v.head_stride;
+      dst = vc ? vc + hh * cache_head : nullptr;
+    }
+    float xa[W], xb[W];
+    if (live) {
+      load_pairs<T, W, IL>(src, p, xa, xb);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) xa[e] = xb[e] = 0.f;
+    }
+    if (!is_v) {
+      const bool normed = is_q ? a.q_gamma != nullptr : a.k_gamma != nullptr;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < W; ++e) sum += xa[e] * xa[e] + xb[e] * xb[e];
+      sum = head_sum(sum, s.lanes);
+      const float r = normed ? 1.f / sqrtf(sum * inv_d + a.eps) : 1.f;
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float na = xa[e] * r * (is_q ? gq[0][e] : gk[0][e]);
+        const float nb = xb[e] * r * (is_q ? gq[1][e] : gk[1][e]);
+        xa[e] = na * c[e] - nb * sn[e];
+        xb[e] = nb * c[e] + na * sn[e];
+      }
+    }
+    if (live && dst) store_pairs<T, W, IL>(dst, p, xa, xb);
+  }
+}
+
+// Each wave goes over tokens and keeps its lanes' part of the weights' gradients; a
+// block adds up its waves' and leaves one row of partial sums for each weight.
+template <typename T, int W, bool IL>
+__global__ __launch_bounds__(kThreads) void k_heads_bwd(HeadArgs a, Split s) {
+  __shared__ float2 cs[kThreads];
+  __shared__ float sums[kWaves][2][kHeadMaxDim];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Place<W, IL> p(s, a.dh, lane);
+  float gq[2][W], gk[2][W], sq[2][W], sk[2][W];
+  load_gamma<T, W, IL>((const T *)a.q_gamma, p, gq[0], gq[1]);
+  load_gamma<T, W, IL>((const T *)a.k_gamma, p, gk[0], gk[1]);
+#pragma unroll
+  for (int e = 0; e < W; ++e) sq[0][e] = sq[1][e] = sk[0][e] = sk[1][e] = 0.f;
+  const int at_once = 64 / s.lanes, sub = lane / s.lanes, rows = a.hq + a.hk;
+  const float inv_d = 1.f / (float)a.dh;
+  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.n; t += (int64_t)gridDim.x * kWaves) {
+    float c[W], sn[W];
+    angles<W>(a.inv_freq, s.r2, a.pos[t], lane, p.pair, cs + 64 * wave, c, sn);
+    for (int base = 0; base < rows; base += at_once) {
+      const int h = base + sub;
+      const bool live = h < rows, is_q = h < a.hq;
+      const int hh = is_q ? h : h - a.hq;
+      float xa[W], xb[W], ya[W], yb[W];
+      T *dst = nullptr;
+      if (live) {
+        const ipttt_heads &x = is_q ? a.q : a.k, &dy = is_q ? a.dq : a.dk;
+        const ipttt_heads &dx = is_q ? a.q_out : a.k_out;
+        load_pairs<T, W, IL>((const T *)x.p + t * x.tok_stride + hh * x.head_stride, p, xa, xb);
+        load_pairs<T, W, IL>((const T *)dy.p + t * dy.tok_stride + hh * dy.head_stride, p, ya, yb);
+        dst = (T *)dx.p + t * dx.tok_stride + hh * dx.head_stride;
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) xa[e] = xb[e] = ya[e] = yb[e] = 0.f;
+      }
+      const bool normed = is_q ? a.q_gamma != nullptr : a.k_gamma != nullptr;
+      float sum = 0.f, dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        sum += xa[e] * xa[e] + xb[e] * xb[e];
+        const float ga = ya[e] * c[e] + yb[e] * sn[e], gb = yb[e] * c[e] - ya[e] * sn[e];
+        ya[e] = ga;
+        yb[e] = gb;
+        dot += ga * (is_q ? gq[0][e] : gk[0][e]) * xa[e] + gb * (is_q ? gq[1][e] : gk[1][e]) * xb[e];
+      }
+      sum = head_sum(sum, s.lanes);
+      dot = head_sum(dot, s.lanes);
+      if (!live) continue;  // whole heads drop out: no sum is split
+      const float r = 1.f / sqrtf(sum * inv_d + a.eps);
+      const float k = dot * r * r * r * inv_d;
+      if (normed) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float za = ya[e] * xa[e] * r, zb = yb[e] * xb[e] * r;
+          sq[0][e] += is_q ? za : 0.f;
+          sq[1][e] += is_q ? zb : 0.f;
+          sk[0][e] += is_q ? 0.f : za;
+          sk[1][e] += is_q ? 0.f : zb;
+          ya[e] = ya[e] * (is_q ? gq[0][e] : gk[0][e]) * r - xa[e] * k;
+          yb[e] = yb[e] * (is_q ? gq[1][e] : gk[1][e]) * r - xb[e] * k;
+        }
+      }
+      store_pairs<T, W, IL>(dst, p, ya, yb);
+    }
+  }
+  if (!a.part) return;
+  // over the lanes that hold the same pairs, then over the waves
+  for (int m = s.lanes; m < 64; m <<= 1)
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        sq[b][e] += __shfl_xor(sq[b][e], m, 64);
+        sk[b][e] += __shfl_xor(sk[b][e], m, 64);
+      }
+  if (sub == 0) {
+    store_pairs<float, W, IL>(sums[wave][0], p, sq[0], sq[1]);
+    store_pairs<float, W, IL>(sums[wave][1], p, sk[0], sk[1]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.dh; i += kThreads) {
+    const int which = i / a.dh, ch = i - which * a.dh;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += sums[w][which][ch];
+    a.part[(int64_t)blockIdx.x * 2 * a.dh + i] = v;
+  }
+}
+
+// Column sums of the blocks' partial rows, in a fixed order: 32 columns a block, 32
+// threads a column.
+__global__ __launch_bounds__(1024) void k_heads_gamma(const float *part, int blocks, int dh,
+                                                      float *dq_gamma, float *dk_gamma) {
+  __shared__ float sums[32][33];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
+  float v = 0.f;
+  if (col < 2 * dh) {
+#pragma unroll 8
+    for (int b = row; b < blocks; b += 32) v += part[(int64_t)b * 2 * dh + col];
+  }
+  sums[row][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (row == 0 && col < 2 * dh) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += sums[i][threadIdx.x];
+    float *out = col < dh ? dq_gamma : dk_gamma;
+    if (out) out[col < dh ? col : col - dh] = v;
+  }
+}
+
+// f(run of pairs, neighbouring pairs) as compile-time constants.
+template <typename T, class F>
+void by_layout(const HeadArgs &a, F f) {
+  constexpr int most = sizeof(T) == 2 ? 8 : 4;
+  const auto run = [&](auto il) {
+    switch (run_of(a.dh, a.rotary, most)) {
+      case 8:
+        if constexpr (most == 8) f(std::integral_constant<int, 8>(), il);
+        break;
+      case 4: f(std::integral_constant<int, 4>(), il); break;
+      case 2: f(std::integral_constant<int, 2>(), il); break;
+      default: f(std::integral_constant<int, 1>(), il);
+    }
+  };
+  if (a.interleaved) run(std::true_type()); else run(std::false_type());
+}
+
+template <typename T, bool APPEND>
+hipError_t launch_heads(const HeadArgs &a, hipStream_t st) {
+  by_layout<T>(a, [&](auto w, auto il) {
+    constexpr int W = decltype(w)::value;
+    const Split s = split_of(a, W);
+    const int at_once = 64 / s.lanes, rows = a.hq + a.hk * (APPEND ? 2 : 1);
+    const int batches = (rows + at_once - 1) / at_once;
+    // a wave a token once there are 8192 tokens, more while there are fewer
+    int64_t slices = (8192 + a.n - 1) / a.n;
+    if (slices > batches) slices = batches;
+    k_heads<T, W, decltype(il)::value, APPEND>
+        <<<blk::grid_of((a.n * slices + kWaves - 1) / kWaves), kThreads, 0, st>>>(a, s, (int)slices);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int heads_bwd_blocks(int64_t n) {
+  const int64_t b = (n + kWaves - 1) / kWaves;
+  return (int)(b < 1 ? 1 : b > 2048 ? 2048 : b);
+}
+
+template <typename T>
+hipError_t heads_forward(const HeadArgs &a, hipStream_t st) {
+  return launch_heads<T, false>(a, st);
+}
+template <typename T>
+hipError_t heads_append(const HeadArgs &a, hipStream_t st) {
+  return launch_heads<T, true>(a, st);
+}
+template <typename T>
+hipError_t heads_backward(const HeadArgs &a, hipStream_t st) {
+  const int blocks = heads_bwd_blocks(a.n);
+  by_layout<T>(a, [&](auto w, auto il) {
+    constexpr int W = decltype(w)::value;
+    k_heads_bwd<T, W, decltype(il)::value><<<blocks, kThreads, 0, st>>>(a, split_of(a, W));
+  });
+  if (a.part)
+    k_heads_gamma<<<(2 * a.dh + 31) / 32, 1024, 0, st>>>(a.part, blocks, a.dh, a.dq_gamma, a.dk_gamma);
+  return hipGetLastError();
+}
+
+template hipError_t heads_forward<float>(const HeadArgs &, hipStream_t);
+template hipError_t heads_forward<__bf16>(const HeadArgs &, hipStream_t);
+template hipError_t heads_append<float>(const HeadArgs &, hipStream_t);
+template hipError_t heads_append<__bf16>(const HeadArgs &, hipStream_t);
+template hipError_t heads_backward<float>(const HeadArgs &, hipStream_t);
+template hipError_t heads_backward<__bf16>(const HeadArgs &, hipStream_t);
+
+}  // namespace ipttt

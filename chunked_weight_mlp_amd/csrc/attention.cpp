@@ -363,7 +363,7 @@ size_t ipttt_attention_backward_workspace_bytes(const ipttt_attention *desc) {
   if (!desc || desc->q_heads < 1 || desc->q_heads > kMaxHeads || desc->n_q < 0 ||
       desc->n_q > ((int64_t)1 << 30))
     return 0;
-  return (size_t)round_up((int64_t)desc->q_heads * desc->n_q * 4 + 1, 256);
+  return (size_t)round_up((int64_t)desc->q_heads * desc->n_q * 8 + 1, 256);
 }
 
 ipttt_status ipttt_attention_backward(const ipttt_attention *desc, const ipttt_heads *q,
@@ -386,6 +386,7 @@ ipttt_status ipttt_attention_backward(const ipttt_attention *desc, const ipttt_h
   a.dk = view(dk, a.n_k, a.hk);
   a.dv = view(dv, a.n_k, a.hk);
   a.delta = (float *)workspace;
+  a.lse2 = a.delta + a.hq * a.n_q;
   const hipStream_t st = (hipStream_t)hip_stream;
   return launched(
       desc->dtype == IPTTT_BF16 ? attn_backward<__bf16>(a, st) : attn_backward<float>(a, st),

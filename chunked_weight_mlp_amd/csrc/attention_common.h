@@ -167,6 +167,73 @@ __device__ __forceinline__ Frag<T> with_sign(Frag<T> f, float scale) {
   return f;
 }
 
+// ---- rows of global memory into a tile ------------------------------------------------
+// What becomes of a value on its way into a tile. A product of a tile with weights that are
+// zero where a row is not seen still takes a value there that is not finite into the sum
+// (0 x infinity). A block whose results are not all finite is therefore computed again:
+// once for how many values that are not finite each result sees (kCount), and once with
+// those values left out (kFinite); where the count is not zero the result is NaN.
+enum Fix { kAsIs, kCount, kFinite };
+template <typename T>
+__device__ __forceinline__ T fixed(T v, int fix) {
+  if (fix == kAsIs) return v;
+  const bool ok = __builtin_isfinite((float)v);
+  return fix == kCount ? (T)(ok ? 0.f : 1.f) : ok ? v : (T)0.f;
+}
+
+// Copies ROWS rows of one head into tiles, WAVES waves together: directly (16 bytes a
+// lane, no registers; the copies are counted by vmcnt and land later) where every piece
+// is whole and on a 16-byte boundary, else through registers. Rows at or behind `end`
+// repeat the last one before it. Pieces behind dh are left as they are: clear() first.
+template <typename T, int DP, int ROWS, int WAVES>
+struct Copier {
+  using L = Tile<T, DP>;
+  static constexpr int RPI = 64 / L::NP;              // rows an instruction fills
+  static constexpr int NI = ROWS / (RPI * WAVES);     // instructions a wave
+  static_assert(ROWS % (RPI * WAVES) == 0, "rows must split evenly over the waves");
+  const T *base;
+  int64_t stride;
+  int dh;
+  bool direct;
+  __device__ __forceinline__ Copier(const T *p, int64_t tok_stride, int dh_)
+      : base(p), stride(tok_stride), dh(dh_) {
+    direct = dh % L::PE == 0 && (uintptr_t)p % 16 == 0 && tok_stride * sizeof(T) % 16 == 0;
+  }
+  // wave must be wave-uniform
+  __device__ __forceinline__ void issue(T *tile, int first, int end, int wave, int lane,
+                                        int fix) const {
+    if (direct && fix == kAsIs) {
+      const bool last = first + ROWS > end;
+      const T *const p0 = base + (int64_t)first * stride;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r0 = (i * WAVES + wave) * RPI, r = r0 + lane / L::NP;
+        const int piece = (lane % L::NP) ^ L::swizzle(r);
+        const int rr = last && first + r >= end ? end - 1 - first : r;
+        if (DP == dh || piece * L::PE < dh)
+          __builtin_amdgcn_global_load_lds((mfma::gbl_cvoid_t *)(p0 + rr * stride + piece * L::PE),
+                                           (mfma::lds_void_t *)(tile + r0 * DP), 16, 0, 0);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < NI; ++i) {
+        const int r = (i * WAVES + wave) * RPI + lane / L::NP, piece = lane % L::NP;
+        const int row = first + r < end ? first + r : end - 1;
+        T v[L::PE];
+        load_some<T, L::PE>(base + row * stride, piece * L::PE, dh, v);
+#pragma unroll
+        for (int e = 0; e < L::PE; ++e) tile[L::at(r, piece) + e] = fixed(v[e], fix);
+      }
+    }
+  }
+};
+// All tiles zero, for those whose rows are narrower than DP. A barrier must follow.
+template <typename T>
+__device__ __forceinline__ void clear(T *tiles, int elems, int tid, int threads) {
+  for (int i = tid; i < elems * (int)sizeof(T) / 16; i += threads)
+    ((uint4 *)tiles)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // ---- the sequences of a packed batch -------------------------------------------------
 // Offset i of a batch as the operators read it: the first is 0, all are within n (none
 // given: one sequence).

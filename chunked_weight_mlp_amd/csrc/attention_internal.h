@@ -48,7 +48,7 @@ struct AttnArgs {
   ipttt_heads q, k, v, o;
   float *lse;              // [hq][n_q]; or null in the forward
   ipttt_heads dy, dq, dk, dv;  // backward
-  float *delta;            // backward: [hq][n_q], sum(dy o)
+  float *delta, *lse2;     // backward: [hq][n_q], sum(dy o) and lse in units of log2
 };
 // Whether the tiles of such a call can be counted in 31 bits.
 bool attn_size_ok(int hq, int batch, int64_t n);

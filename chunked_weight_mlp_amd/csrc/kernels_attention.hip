@@ -7,37 +7,7 @@ namespace {
 using namespace attn;
 
 constexpr int kRows = 32;  // queries (keys) a wave holds
-constexpr int kWaves = 8, kThreads = 64 * kWaves, kBlock = kRows * kWaves;
-constexpr int kStage = 64;  // rows of the other side a step
-
-// What becomes of a value on its way into a tile. A product of a tile with weights that are
-// zero where a row is not seen still takes a value there that is not finite into the sum
-// (0 x infinity). A block whose results are not all finite is therefore computed again:
-// once for how many values that are not finite each result sees (kCount), and once with
-// those values left out (kFinite); where the count is not zero the result is NaN.
-enum Fix { kAsIs, kCount, kFinite };
-template <typename T>
-__device__ __forceinline__ T fixed(T v, int fix) {
-  if (fix == kAsIs) return v;
-  const bool ok = __builtin_isfinite((float)v);
-  return fix == kCount ? (T)(ok ? 0.f : 1.f) : ok ? v : (T)0.f;
-}
-
-// Copies kStage rows from `first` of a tensor's head into a tile; rows at or behind `end`
-// repeat the last one before it.
-template <typename T, int DP>
-__device__ __forceinline__ void stage(T *tile, const T *base, int64_t stride, int first, int end,
-                                      int dh, int tid, int fix) {
-  using L = Tile<T, DP>;
-  for (int i = tid; i < kStage * L::NP; i += kThreads) {
-    const int r = i / L::NP, p = i % L::NP;
-    const int row = first + r < end ? first + r : end - 1;
-    T v[L::PE];
-    load_some<T, L::PE>(base + row * stride, p * L::PE, dh, v);
-#pragma unroll
-    for (int e = 0; e < L::PE; ++e) tile[L::at(r, p) + e] = fixed(v[e], fix);
-  }
-}
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kBlock = kRows * kWaves;
 
 // What a query sees of its sequence's keys: [lo, hi).
 struct Seen {
@@ -51,37 +21,19 @@ __device__ __forceinline__ Seen seen_by(const AttnArgs &a, int i, int lq, int lk
 
 template <int N>
 __device__ __forceinline__ bool all_finite(const f32x16 (&x)[N]) {
-  bool ok = true;
+  float z = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) ok &= __builtin_isfinite(x[i][e]);
-  return ok;
+    for (int e = 0; e < 16; ++e) z = __builtin_fmaf(x[i][e], 0.f, z);
+  return z == 0.f;
 }
 
-// Results that are not zero, and NaN for them.
-template <int N>
-__device__ __forceinline__ uint64_t nonzero(const f32x16 (&x)[N]) {
-  uint64_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) bits |= (uint64_t)(x[i][e] != 0.f) << (16 * i + e);
-  return bits;
-}
-template <int N>
-__device__ __forceinline__ void spoil(f32x16 (&x)[N], uint64_t bits) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (bits >> (16 * i + e) & 1) x[i][e] = NAN;
-}
-
-// Rows of a lane's results x scale to a row of dh channels in memory.
+// A lane's results x scale to its row of dh channels in memory. kCount leaves NaN there where
+// something was counted and zero elsewhere, and kFinite adds to that.
 template <typename T, int DP>
 __device__ __forceinline__ void store_row(T *row, const f32x16 (&x)[DP / 32], float scale, int h,
-                                          int dh) {
+                                          int dh, int fix) {
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -90,6 +42,13 @@ __device__ __forceinline__ void store_row(T *row, const f32x16 (&x)[DP / 32], fl
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = x[d][4 * g + e] * scale;
+      if (fix != kAsIs) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (fix == kCount) v[e] = x[d][4 * g + e] != 0.f ? NAN : 0.f;
+          else if (c + e < dh) v[e] += (float)row[c + e];
+        }
+      }
       if (c + 4 <= dh) {
         blk::store_pack<T, 4>(row + c, v);
       } else {
@@ -117,15 +76,24 @@ __device__ __forceinline__ Work work_of(const AttnArgs &a, int64_t tiles) {
   return w;
 }
 
+// Rows of the other side a step: two steps' tiles of two blocks fit a CU's LDS.
+template <typename T>
+constexpr int step_rows() { return sizeof(T) == 2 ? 64 : 32; }
+// The running maximum may fall behind by this much (in log2): weights are then up to 2^8,
+// which costs neither bf16 nor fp32 precision, and the sums are seldom rescaled.
+constexpr float kSlack = 8.f;
+
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void k_fwd(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
+  constexpr int KS = step_rows<T>(), NT = KS / 32;
+  using C = Copier<T, DP, KS, kWaves>;
   extern __shared__ __align__(16) char smem[];
-  T *const kt = (T *)smem, *const vt = kt + kStage * DP;
-  const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, h = l >> 5;
+  T *const buf = (T *)smem;  // [2][K tile, V tile]
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const Work w = work_of(a, tiles);
   if (w.tile < 0) return;
-  const int s = sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l);
+  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l));
   const Rows rq = rows_of(a.q_off, s, a.batch, a.n_q);
   const Rows rk = s < a.batch ? rows_of(a.k_off, s, a.batch, a.n_k) : Rows{0, 0};
   const int first = (int)(w.tile - (rq.start / kBlock + s)) * kBlock;  // the block's first query
@@ -134,8 +102,8 @@ __global__ __launch_bounds__(kThreads) void k_fwd(AttnArgs a, int64_t tiles) {
   const int q0 = first + kRows * wave, qi = q0 + (l & 31);
   const int qr = min(qi, lq - 1);
   const T *qp = (const T *)a.q.p + (rq.start + qr) * a.q.tok_stride + w.head * a.q.head_stride;
-  const T *kp = (const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride;
-  const T *vp = (const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride;
+  const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh);
+  const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh);
   Frag<T> q[L::STEPS];
 #pragma unroll
   for (int i = 0; i < L::STEPS; ++i) q[i] = with_sign<T>(load_frag<T>(qp, i, h, a.dh), a.scale);
@@ -144,101 +112,114 @@ __global__ __launch_bounds__(kThreads) void k_fwd(AttnArgs a, int64_t tiles) {
   // of this wave's rows (those behind the last query are not stored)
   const Seen wf = seen_by(a, q0, lq, lk), wl = seen_by(a, q0 + kRows - 1, lq, lk);
   const float c = log2_scale(a.scale);
+  if (a.dh != DP) {
+    clear(buf, 4 * KS * DP, tid, kThreads);
+    __syncthreads();
+  }
   f32x16 acc[DP / 32];
   float m, sum;
-  uint64_t bad = 0;
+  const int begin = head.lo / KS * KS;
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
     m = -INFINITY;
     sum = 0.f;
-    for (int k0 = head.lo / kStage * kStage; k0 < tail.hi; k0 += kStage) {
-      __syncthreads();
-      stage<T, DP>(kt, kp, a.k.tok_stride, k0, lk, a.dh, tid, kAsIs);
-      stage<T, DP>(vt, vp, a.v.tok_stride, k0, lk, a.dh, tid, fix);
-      __syncthreads();
-      if (k0 >= wl.hi || k0 + kStage <= wf.lo) continue;  // nothing here for this wave
-      f32x16 x[kStage / 32];
-#pragma unroll
-      for (int t = 0; t < kStage / 32; ++t) {
-        x[t] = f32x16{};
-#pragma unroll
-        for (int i = 0; i < L::STEPS; ++i)
-          x[t] = mma(L::row_frag(kt, 32 * t + (l & 31), i, h), q[i], x[t]);
+    int cur = 0;
+    if (begin < tail.hi) {
+      kc.issue(buf, begin, lk, wave, l, kAsIs);
+      vc.issue(buf + KS * DP, begin, lk, wave, l, fix);
+    }
+    for (int k0 = begin; k0 < tail.hi; k0 += KS) {
+      // this tile has landed, and no wave reads the other one any more
+      mfma::wait_vm<0>();
+      mfma::lds_barrier();
+      const T *const kt = buf + cur * 2 * KS * DP, *const vt = kt + KS * DP;
+      cur ^= 1;
+      if (k0 + KS < tail.hi) {
+        T *const next = buf + cur * 2 * KS * DP;
+        kc.issue(next, k0 + KS, lk, wave, l, kAsIs);
+        vc.issue(next + KS * DP, k0 + KS, lk, wave, l, fix);
       }
-      const bool whole = k0 + kStage <= wf.hi && k0 >= wl.lo;
-      if (!whole) {
+      if (k0 >= wl.hi || k0 + KS <= wf.lo) continue;  // nothing here for this wave
+      // whether the lane's query sees its key j of the tile
+      const int from = k0 + 4 * h - mine.lo;
+      const unsigned keys = max(0, mine.hi - mine.lo);
+      const auto sees = [&](int j) { return (unsigned)(from + j) < keys; };
+      f32x16 x[NT];
 #pragma unroll
-        for (int t = 0; t < kStage / 32; ++t)
+      for (int t = 0; t < NT; ++t) x[t] = f32x16{};
+#pragma unroll
+      for (int i = 0; i < L::STEPS; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[t] = mma(L::row_frag(kt, 32 * t + (l & 31), i, h), q[i], x[t]);
+      if (k0 + KS > wf.hi || k0 < wl.lo) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int j = k0 + 32 * t + 8 * (i / 4) + 4 * h + i % 4;
-            if (j < mine.lo || j >= mine.hi) x[t][i] = -INFINITY;
+            if (!sees(32 * t + 8 * (i / 4) + i % 4)) x[t][i] = -INFINITY;
           }
       }
-      // running maximum
-      float top = -INFINITY;
+      float top = x[0][0];
 #pragma unroll
-      for (int t = 0; t < kStage / 32; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          top = fmaxf(top, x[t][i]);
-        }
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, x[t][i]);
       top = fmaxf(top, other_half(top));
-      const float next = fmaxf(m, top);
-      const float base = next == -INFINITY ? 0.f : next;
-      const float f = exp2_((m - base) * c);
-      m = next;
-      sum *= f;
+      if (__ballot((top - m) * c > kSlack)) {
+        const float next = fmaxf(m, top);
+        const float f = next == -INFINITY ? 1.f : exp2_((m - next) * c);
+        m = next;
+        sum *= f;
 #pragma unroll
-      for (int d = 0; d < DP / 32; ++d)
+        for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+          for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+      }
+      const float mc = m == -INFINITY ? 0.f : m * c;
 #pragma unroll
-      for (int t = 0; t < kStage / 32; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          x[t][i] = exp2_((x[t][i] - base) * c);
+          x[t][i] = exp2_(__builtin_fmaf(x[t][i], c, -mc));
           sum += x[t][i];
         }
       if (fix == kCount) {
 #pragma unroll
-        for (int t = 0; t < kStage / 32; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int j = k0 + 32 * t + 8 * (i / 4) + 4 * h + i % 4;
-            x[t][i] = j >= mine.lo && j < mine.hi ? 1.f : 0.f;
+            x[t][i] = sees(32 * t + 8 * (i / 4) + i % 4) ? 1.f : 0.f;
           }
       }
 #pragma unroll
-      for (int i = 0; i < kStage / 16; ++i) {
+      for (int i = 0; i < KS / 16; ++i) {
         const Frag<T> p = as_operand<T>(x[i / 2], i % 2);
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
           acc[d] = mma(L::col_frag(vt, 16 * i, 32 * d, l), p, acc[d]);
       }
     }
-    if (fix == kFinite) spoil(acc, bad);
-    if (fix == kCount) bad = nonzero(acc);
-    if (fix == kFinite || (fix == kAsIs && __syncthreads_and(all_finite(acc)))) break;
-  }
-  sum += other_half(sum);
-  if (qi >= lq) return;
-  const bool none = mine.lo >= mine.hi;
-  T *const op = (T *)a.o.p + (rq.start + qi) * a.o.tok_stride + w.head * a.o.head_stride;
-  if (none) {
+    if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
+    const float total = sum + other_half(sum);
+    if (qi < lq) {
+      const bool none = mine.lo >= mine.hi;
+      T *const op = (T *)a.o.p + (rq.start + qi) * a.o.tok_stride + w.head * a.o.head_stride;
+      if (none) {
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
+        for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
+      }
+      store_row<T, DP>(op, acc, none ? 0.f : 1.f / total, h, a.dh, fix);
+      if (a.lse && h == 0)
+        a.lse[w.head * a.n_q + rq.start + qi] = none ? -INFINITY : (m * c + log2f(total)) * kLn2;
+    }
+    if (fix != kCount) break;
+    __syncthreads();  // the buffers are filled anew
   }
-  store_row<T, DP>(op, acc, none ? 0.f : 1.f / sum, h, a.dh);
-  if (a.lse && h == 0)
-    a.lse[w.head * a.n_q + rq.start + qi] = none ? -INFINITY : (m * c + log2f(sum)) * kLn2;
 }
 
-// The forward's lse in units of log2. A row with an infinite score has no softmax.
-__device__ __forceinline__ float log2_sum(float lse) { return lse == INFINITY ? NAN : lse * kLog2e; }
-
-// delta = sum(dy o) of each query and head: 16 lanes a row.
+// delta = sum(dy o) of each query and head, and the forward's lse in units of log2: 16
+// lanes a row. A row with an infinite score has no softmax: its gradients are NaN.
 template <typename T>
 __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
   const int64_t row = (blk::block_id() * 256 + threadIdx.x) / 16;  // token-major
@@ -258,19 +239,25 @@ __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
   }
 #pragma unroll
   for (int k = 8; k >= 1; k >>= 1) v += __shfl_xor(v, k, 64);
-  if ((threadIdx.x & 15) == 0) a.delta[hd * a.n_q + t] = v;
+  if ((threadIdx.x & 15) == 0) {
+    const float lse = a.lse[hd * a.n_q + t];
+    a.delta[hd * a.n_q + t] = v;
+    a.lse2[hd * a.n_q + t] = lse == INFINITY ? NAN : lse * kLog2e;
+  }
 }
 
 // dq: a block's queries, over the keys that they see.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void k_dq(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
+  constexpr int KS = step_rows<T>(), NT = KS / 32;
+  using C = Copier<T, DP, KS, kWaves>;
   extern __shared__ __align__(16) char smem[];
-  T *const kt = (T *)smem, *const vt = kt + kStage * DP;
-  const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, h = l >> 5;
+  T *const buf = (T *)smem;  // [2][K tile, V tile]
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const Work w = work_of(a, tiles);
   if (w.tile < 0) return;
-  const int s = sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l);
+  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l));
   const Rows rq = rows_of(a.q_off, s, a.batch, a.n_q);
   const Rows rk = s < a.batch ? rows_of(a.k_off, s, a.batch, a.n_k) : Rows{0, 0};
   const int first = (int)(w.tile - (rq.start / kBlock + s)) * kBlock;
@@ -280,8 +267,8 @@ __global__ __launch_bounds__(kThreads) void k_dq(AttnArgs a, int64_t tiles) {
   const int64_t qr = rq.start + min(qi, lq - 1);
   const T *qp = (const T *)a.q.p + qr * a.q.tok_stride + w.head * a.q.head_stride;
   const T *yp = (const T *)a.dy.p + qr * a.dy.tok_stride + w.head * a.dy.head_stride;
-  const T *kp = (const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride;
-  const T *vp = (const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride;
+  const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh);
+  const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh);
   Frag<T> q[L::STEPS], dy[L::STEPS];
 #pragma unroll
   for (int i = 0; i < L::STEPS; ++i) {
@@ -292,76 +279,89 @@ __global__ __launch_bounds__(kThreads) void k_dq(AttnArgs a, int64_t tiles) {
   const Seen head = seen_by(a, first, lq, lk), tail = seen_by(a, min(first + kBlock, lq) - 1, lq, lk);
   const Seen wf = seen_by(a, q0, lq, lk), wl = seen_by(a, q0 + kRows - 1, lq, lk);
   const float c = log2_scale(a.scale);
-  const float lse = log2_sum(a.lse[w.head * a.n_q + qr]), delta = a.delta[w.head * a.n_q + qr];
+  const float lse = a.lse2[w.head * a.n_q + qr], delta = a.delta[w.head * a.n_q + qr];
+  if (a.dh != DP) {
+    clear(buf, 4 * KS * DP, tid, kThreads);
+    __syncthreads();
+  }
+  const int begin = head.lo / KS * KS;
   f32x16 acc[DP / 32];
-  uint64_t bad = 0;
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
-    for (int k0 = head.lo / kStage * kStage; k0 < tail.hi; k0 += kStage) {
-      __syncthreads();
-      stage<T, DP>(kt, kp, a.k.tok_stride, k0, lk, a.dh, tid, fix);
-      stage<T, DP>(vt, vp, a.v.tok_stride, k0, lk, a.dh, tid, kAsIs);
-      __syncthreads();
-      if (k0 >= wl.hi || k0 + kStage <= wf.lo) continue;
-      f32x16 x[kStage / 32];
-      const bool whole = k0 + kStage <= wf.hi && k0 >= wl.lo;
+    int cur = 0;
+    if (begin < tail.hi) {
+      kc.issue(buf, begin, lk, wave, l, fix);
+      vc.issue(buf + KS * DP, begin, lk, wave, l, kAsIs);
+    }
+    for (int k0 = begin; k0 < tail.hi; k0 += KS) {
+      mfma::wait_vm<0>();
+      mfma::lds_barrier();
+      const T *const kt = buf + cur * 2 * KS * DP, *const vt = kt + KS * DP;
+      cur ^= 1;
+      if (k0 + KS < tail.hi) {
+        T *const next = buf + cur * 2 * KS * DP;
+        kc.issue(next, k0 + KS, lk, wave, l, fix);
+        vc.issue(next + KS * DP, k0 + KS, lk, wave, l, kAsIs);
+      }
+      if (k0 >= wl.hi || k0 + KS <= wf.lo) continue;
+      const bool whole = k0 + KS <= wf.hi && k0 >= wl.lo;
+      const int from = k0 + 4 * h - mine.lo;
+      const unsigned keys = max(0, mine.hi - mine.lo);
+      const auto sees = [&](int j) { return (unsigned)(from + j) < keys; };
 #pragma unroll
-      for (int t = 0; t < kStage / 32; ++t) {
-        f32x16 dp{};
-        x[t] = f32x16{};
+      for (int t = 0; t < NT; ++t) {
+        f32x16 x{}, dp{};
 #pragma unroll
         for (int i = 0; i < L::STEPS; ++i) {
-          x[t] = mma(L::row_frag(kt, 32 * t + (l & 31), i, h), q[i], x[t]);
+          x = mma(L::row_frag(kt, 32 * t + (l & 31), i, h), q[i], x);
           dp = mma(L::row_frag(vt, 32 * t + (l & 31), i, h), dy[i], dp);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = exp2_(x[t][i] * c - lse);
-          x[t][i] = p * (dp[i] - delta);
-          const int j = k0 + 32 * t + 8 * (i / 4) + 4 * h + i % 4;
-          if (!whole && (j < mine.lo || j >= mine.hi)) x[t][i] = 0.f;
+        for (int i = 0; i < 16; ++i) x[i] = exp2_(__builtin_fmaf(x[i], c, -lse)) * (dp[i] - delta);
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!sees(32 * t + 8 * (i / 4) + i % 4)) x[i] = 0.f;
+        }
+        if (fix == kCount) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = sees(32 * t + 8 * (i / 4) + i % 4) ? 1.f : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Frag<T> ds = as_operand<T>(x, i);
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d)
+            acc[d] = mma(L::col_frag(kt, 32 * t + 16 * i, 32 * d, l), ds, acc[d]);
         }
       }
-      if (fix == kCount) {
-#pragma unroll
-        for (int t = 0; t < kStage / 32; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = k0 + 32 * t + 8 * (i / 4) + 4 * h + i % 4;
-            x[t][i] = j >= mine.lo && j < mine.hi ? 1.f : 0.f;
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < kStage / 16; ++i) {
-        const Frag<T> ds = as_operand<T>(x[i / 2], i % 2);
-#pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
-          acc[d] = mma(L::col_frag(kt, 16 * i, 32 * d, l), ds, acc[d]);
-      }
     }
-    if (fix == kFinite) spoil(acc, bad);
-    if (fix == kCount) bad = nonzero(acc);
-    if (fix == kFinite || (fix == kAsIs && __syncthreads_and(all_finite(acc)))) break;
+    if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
+    if (qi < lq)
+      store_row<T, DP>((T *)a.dq.p + (rq.start + qi) * a.dq.tok_stride + w.head * a.dq.head_stride, acc, a.scale,
+                       h, a.dh, fix);
+    if (fix != kCount) break;
+    __syncthreads();
   }
-  if (qi >= lq) return;
-  T *const out = (T *)a.dq.p + (rq.start + qi) * a.dq.tok_stride + w.head * a.dq.head_stride;
-  store_row<T, DP>(out, acc, a.scale, h, a.dh);
 }
 
-// dk and dv: a block's keys, over the queries of the group's heads that see them.
+// dk and dv: a block's keys, over the queries of the group's heads that see them. The steps
+// of all heads are one sequence of tiles: head g's steps are g n .. g n + n - 1.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void k_dkv(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
+  constexpr int QS = step_rows<T>(), NT = QS / 32;
+  using C = Copier<T, DP, QS, kWaves>;
   extern __shared__ __align__(16) char smem[];
-  T *const qt = (T *)smem, *const yt = qt + kStage * DP;
-  float *const row_lse = (float *)(yt + kStage * DP), *const row_delta = row_lse + kStage;
-  const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, h = l >> 5;
+  T *const buf = (T *)smem;                            // [2][q tile, dy tile]
+  float *const stats = (float *)(buf + 4 * QS * DP);   // [2][lse, delta][64]
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const int64_t id = blk::block_id();
   const int kv = (int)(id % a.hk);
   const int64_t tile = id / a.hk;
   if (tile >= tiles) return;
-  const int s = sequence_of(a.k_off, a.batch, a.n_k, kBlock, tile, l);
+  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.k_off, a.batch, a.n_k, kBlock, tile, l));
   const Rows rk = rows_of(a.k_off, s, a.batch, a.n_k);
   const Rows rq = s < a.batch ? rows_of(a.q_off, s, a.batch, a.n_q) : Rows{0, 0};
   const int first = (int)(tile - (rk.start / kBlock + s)) * kBlock;
@@ -380,82 +380,101 @@ __global__ __launch_bounds__(kThreads) void k_dkv(AttnArgs a, int64_t tiles) {
   // the queries that see key j: [from(j), to(j))
   const int off = lk - lq;
   const auto from = [&](int j) { return a.causal ? max(0, j - off) : 0; };
-  const auto to = [&](int j) {
-    return a.causal && a.window > 0 ? max(0, min((int64_t)lq, (int64_t)j + a.window - off)) : lq;
+  const auto to = [&](int j) -> int {
+    if (!a.causal || a.window <= 0) return lq;
+    return (int)max((int64_t)0, min((int64_t)lq, (int64_t)j + a.window - off));
   };
-  const int my_from = from(kj), my_to = kj < lk ? (int)to(kj) : 0;
-  const int q_from = from(first), q_to = (int)to(min(first + kBlock, lk) - 1);
-  const int w_from = from(k0), w_to = k0 < lk ? (int)to(min(k0 + kRows, lk) - 1) : 0;
-  const int w_all_from = from(k0 + kRows - 1), w_all_to = k0 + kRows <= lk ? (int)to(k0) : 0;
+  const int my_from = from(kj), my_to = kj < lk ? to(kj) : 0;
+  const int q_from = from(first), q_to = to(min(first + kBlock, lk) - 1);
+  const int w_from = from(k0), w_to = k0 < lk ? to(min(k0 + kRows, lk) - 1) : 0;
+  const int all_from = from(k0 + kRows - 1), all_to = k0 + kRows <= lk ? to(k0) : 0;
+  const int begin = q_from / QS * QS, steps = q_to > begin ? (q_to - begin + QS - 1) / QS : 0;
   const float c = log2_scale(a.scale);
+  if (a.dh != DP) {
+    clear(buf, 4 * QS * DP, tid, kThreads);
+    __syncthreads();
+  }
+  // step n: head n / steps, queries from begin + n % steps * QS
+  const auto issue = [&](int g, int i0, int b, int fix) __attribute__((always_inline)) {
+    const int hd = kv * group + g;
+    T *const t = buf + b * 2 * QS * DP;
+    const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + hd * a.q.head_stride, a.q.tok_stride, a.dh);
+    const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride, a.dh);
+    qc.issue(t, i0, lq, wave, l, fix);
+    yc.issue(t + QS * DP, i0, lq, wave, l, fix);
+    if (wave < 2) {
+      const float *src = (wave ? a.delta : a.lse2) + hd * a.n_q + rq.start + min(i0 + l, lq - 1);
+      __builtin_amdgcn_global_load_lds((mfma::gbl_cvoid_t *)src,
+                                       (mfma::lds_void_t *)(stats + (2 * b + wave) * 64), 4, 0, 0);
+    }
+  };
   f32x16 dk[DP / 32], dv[DP / 32];
-  uint64_t bad = 0;
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = f32x16{};
-    for (int g = 0; g < group; ++g) {
-      const int head = kv * group + g;
-      const T *qp = (const T *)a.q.p + rq.start * a.q.tok_stride + head * a.q.head_stride;
-      const T *yp = (const T *)a.dy.p + rq.start * a.dy.tok_stride + head * a.dy.head_stride;
-      const float *lse = a.lse + head * a.n_q + rq.start, *delta = a.delta + head * a.n_q + rq.start;
-      for (int i0 = q_from / kStage * kStage; i0 < q_to; i0 += kStage) {
-        __syncthreads();
-        stage<T, DP>(qt, qp, a.q.tok_stride, i0, lq, a.dh, tid, fix);
-        stage<T, DP>(yt, yp, a.dy.tok_stride, i0, lq, a.dh, tid, fix);
-        if (tid < kStage) {
-          const int i = min(i0 + tid, lq - 1);
-          row_lse[tid] = log2_sum(lse[i]);
-          row_delta[tid] = delta[i];
+    int cur = 0;
+    if (steps > 0) issue(0, begin, 0, fix);
+    for (int g = 0, n = 0; g < group && steps > 0;) {
+      mfma::wait_vm<0>();
+      mfma::lds_barrier();
+      const T *const qt = buf + cur * 2 * QS * DP, *const yt = qt + QS * DP;
+      const float *const lse = stats + 2 * cur * 64, *const delta = lse + 64;
+      cur ^= 1;
+      const int i0 = begin + n * QS;
+      if (++n == steps) n = 0, ++g;
+      if (g < group) issue(g, begin + n * QS, cur, fix);
+      if (i0 >= w_to || i0 + QS <= w_from) continue;
+      const bool whole = i0 >= all_from && i0 + QS <= all_to;
+      const int rel = i0 + 4 * h - my_from;
+      const unsigned rows = max(0, my_to - my_from);
+      const auto seen = [&](int r) { return (unsigned)(rel + r) < rows; };
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        f32x16 x{}, y{};
+#pragma unroll
+        for (int i = 0; i < L::STEPS; ++i) {
+          x = mma(L::row_frag(qt, 32 * t + (l & 31), i, h), k[i], x);
+          y = mma(L::row_frag(yt, 32 * t + (l & 31), i, h), v[i], y);
         }
-        __syncthreads();
-        if (i0 >= w_to || i0 + kStage <= w_from) continue;
-        const bool whole = i0 >= w_all_from && i0 + kStage <= w_all_to;
-        f32x16 x[kStage / 32], y[kStage / 32];
 #pragma unroll
-        for (int t = 0; t < kStage / 32; ++t) {
-          x[t] = y[t] = f32x16{};
+        for (int i = 0; i < 4; ++i) {
+          const float4 e = *(const float4 *)(lse + 32 * t + 8 * i + 4 * h);
+          const float4 d = *(const float4 *)(delta + 32 * t + 8 * i + 4 * h);
+          const float ee[4] = {e.x, e.y, e.z, e.w}, dd[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-          for (int i = 0; i < L::STEPS; ++i) {
-            x[t] = mma(L::row_frag(qt, 32 * t + (l & 31), i, h), k[i], x[t]);
-            y[t] = mma(L::row_frag(yt, 32 * t + (l & 31), i, h), v[i], y[t]);
+          for (int j = 0; j < 4; ++j) {
+            x[4 * i + j] = exp2_(__builtin_fmaf(x[4 * i + j], c, -ee[j]));
+            y[4 * i + j] = x[4 * i + j] * (y[4 * i + j] - dd[j]);
           }
+        }
+        if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = 32 * t + 8 * (i / 4) + 4 * h + i % 4;
-            float p = exp2_(x[t][i] * c - row_lse[r]);
-            float ds = p * (y[t][i] - row_delta[r]);
-            if (!whole && (i0 + r < my_from || i0 + r >= my_to)) p = ds = 0.f;
-            x[t][i] = p;
-            y[t][i] = ds;
-          }
+          for (int i = 0; i < 16; ++i)
+            if (!seen(32 * t + 8 * (i / 4) + i % 4)) x[i] = y[i] = 0.f;
         }
         if (fix == kCount) {
 #pragma unroll
-          for (int t = 0; t < kStage / 32; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = i0 + 32 * t + 8 * (i / 4) + 4 * h + i % 4;
-              x[t][i] = r >= my_from && r < my_to ? 1.f : 0.f;
-            }
+          for (int i = 0; i < 16; ++i) x[i] = seen(32 * t + 8 * (i / 4) + i % 4) ? 1.f : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < kStage / 16; ++i) {
-          const Frag<T> p = as_operand<T>(x[i / 2], i % 2), ds = as_operand<T>(y[i / 2], i % 2);
+        for (int i = 0; i < 2; ++i) {
+          const Frag<T> p = as_operand<T>(x, i), ds = as_operand<T>(y, i);
 #pragma unroll
           for (int d = 0; d < DP / 32; ++d) {
-            dv[d] = mma(L::col_frag(yt, 16 * i, 32 * d, l), p, dv[d]);
-            dk[d] = mma(L::col_frag(qt, 16 * i, 32 * d, l), ds, dk[d]);
+            dv[d] = mma(L::col_frag(yt, 32 * t + 16 * i, 32 * d, l), p, dv[d]);
+            dk[d] = mma(L::col_frag(qt, 32 * t + 16 * i, 32 * d, l), ds, dk[d]);
           }
         }
       }
     }
-    if (fix == kFinite) spoil(dv, bad);
-    if (fix == kCount) bad = nonzero(dv);
-    if (fix == kFinite || (fix == kAsIs && __syncthreads_and(all_finite(dk) && all_finite(dv)))) break;
+    if (fix == kAsIs && !__syncthreads_and(all_finite(dk) && all_finite(dv))) continue;
+    if (kj < lk) {
+      store_row<T, DP>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk, a.scale, h, a.dh, kAsIs);
+      store_row<T, DP>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv, 1.f, h, a.dh, fix);
+    }
+    if (fix != kCount) break;
+    __syncthreads();
   }
-  if (kj >= lk) return;
-  store_row<T, DP>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk, a.scale, h, a.dh);
-  store_row<T, DP>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv, 1.f, h, a.dh);
 }
 
 template <typename T, class F>
@@ -474,7 +493,8 @@ hipError_t attn_forward(const AttnArgs &a, hipStream_t st) {
   by_width<T>(a.dh, [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
     const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);
-    k_fwd<T, DP><<<blk::grid_of(tiles * a.hq), kThreads, 2 * kStage * DP * sizeof(T), st>>>(a, tiles);
+    k_fwd<T, DP><<<blk::grid_of(tiles * a.hq), kThreads, 4 * step_rows<T>() * DP * sizeof(T), st>>>(
+        a, tiles);
   });
   return hipGetLastError();
 }
@@ -484,10 +504,10 @@ hipError_t attn_backward(const AttnArgs &a, hipStream_t st) {
   if (a.n_q > 0) k_delta<T><<<blk::grid_of((a.n_q * a.hq + 15) / 16), 256, 0, st>>>(a);
   by_width<T>(a.dh, [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
-    const size_t lds = 2 * kStage * DP * sizeof(T);
+    const size_t lds = 4 * step_rows<T>() * DP * sizeof(T);
     if (a.n_k > 0) {
       const int64_t tiles = tiles_of(a.n_k, kBlock, a.batch);
-      k_dkv<T, DP><<<blk::grid_of(tiles * a.hk), kThreads, lds + 8 * kStage, st>>>(a, tiles);
+      k_dkv<T, DP><<<blk::grid_of(tiles * a.hk), kThreads, lds + 4 * 64 * sizeof(float), st>>>(a, tiles);
     }
     if (a.n_q > 0) {
       const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);

@@ -74,8 +74,19 @@ __device__ __forceinline__ Frag<T> zero_frag() {
 }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
-// The other half's value of the same column.
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+// The lower and the upper half's value of this lane's column.
+__device__ __forceinline__ float2 halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_max(float v) {
+  const float2 r = halves(v);
+  return fmaxf(r.x, r.y);
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const float2 r = halves(v);
+  return r.x + r.y;
+}
 
 // A tile of rows of DP channels (64 or 128, at least head_dim; the rest zero) in LDS, in
 // pieces of 16 bytes. Piece p of row r is at place p ^ swizzle(r): the 16 rows that one
@@ -167,6 +178,13 @@ __device__ __forceinline__ Frag<T> with_sign(Frag<T> f, float scale) {
   return f;
 }
 
+// A value that the compiler takes to be another one each time: what is computed from it in a
+// rare path inside a loop is not computed, and held in registers, ahead of the loop.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // ---- rows of global memory into a tile ------------------------------------------------
 // What becomes of a value on its way into a tile. A product of a tile with weights that are
 // zero where a row is not seen still takes a value there that is not finite into the sum
@@ -181,10 +199,37 @@ __device__ __forceinline__ T fixed(T v, int fix) {
   return fix == kCount ? (T)(ok ? 0.f : 1.f) : ok ? v : (T)0.f;
 }
 
+// 16 (or 4) bytes a lane from base + offset in global memory to LDS at dst + 16 (4) x lane,
+// counted by vmcnt. base and dst are wave-uniform. In assembly because behind the builtin
+// the compiler waits for all copies in flight before every transposing LDS read; the loops
+// below wait for a tile where they begin it. No register is loaded, and M0 is set and
+// restored in the same block.
+template <int BYTES>
+__device__ __forceinline__ void copy_to_lds(const void *base, uint32_t offset, const void *dst) {
+  static_assert(BYTES == 16 || BYTES == 4, "");
+  const uint32_t at = (uint32_t)(uintptr_t)(mfma::lds_void_t *)dst;
+  uint32_t m0;
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(at), "v"(offset), "s"(base) : "memory");
+  else
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "global_load_lds_dword %2, %3\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(at), "v"(offset), "s"(base) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ const T *uniform(const T *p) {
+  const uint64_t v = (uint64_t)p;
+  return (const T *)((uint64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
 // Copies ROWS rows of one head into tiles, WAVES waves together: directly (16 bytes a
 // lane, no registers; the copies are counted by vmcnt and land later) where every piece
-// is whole and on a 16-byte boundary, else through registers. Rows at or behind `end`
-// repeat the last one before it. Pieces behind dh are left as they are: clear() first.
+// is whole and on a 16-byte boundary and a tile spans less than 2^31 bytes, else through
+// registers. Rows at or behind `end` repeat the last one before it. Pieces behind dh are
+// left as they are: clear() first.
 template <typename T, int DP, int ROWS, int WAVES>
 struct Copier {
   using L = Tile<T, DP>;
@@ -193,36 +238,48 @@ struct Copier {
   static_assert(ROWS % (RPI * WAVES) == 0, "rows must split evenly over the waves");
   const T *base;
   int64_t stride;
-  int dh;
+  uint32_t offset[NI];  // of this lane's piece from the tile's first row
   bool direct;
-  __device__ __forceinline__ Copier(const T *p, int64_t tok_stride, int dh_)
-      : base(p), stride(tok_stride), dh(dh_) {
-    direct = dh % L::PE == 0 && (uintptr_t)p % 16 == 0 && tok_stride * sizeof(T) % 16 == 0;
+  __device__ __forceinline__ Copier(const T *p, int64_t tok_stride, int dh, int wave, int lane)
+      : base(uniform(p)), stride(tok_stride) {
+    direct = dh % L::PE == 0 && (uintptr_t)p % 16 == 0 && tok_stride * sizeof(T) % 16 == 0 &&
+             tok_stride < (1 << 30) / ROWS / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = row(i, wave, lane);
+      offset[i] = (r * (uint32_t)stride + piece(r, lane) * L::PE) * sizeof(T);
+    }
   }
+  __device__ static __forceinline__ int row(int i, int wave, int lane) {
+    return (i * WAVES + wave) * RPI + lane / L::NP;
+  }
+  __device__ static __forceinline__ int piece(int r, int lane) { return (lane % L::NP) ^ L::swizzle(r); }
   // wave must be wave-uniform
-  __device__ __forceinline__ void issue(T *tile, int first, int end, int wave, int lane,
+  __device__ __forceinline__ void issue(T *tile, int first, int end, int dh, int wave, int lane,
                                         int fix) const {
     if (direct && fix == kAsIs) {
-      const bool last = first + ROWS > end;
       const T *const p0 = base + (int64_t)first * stride;
+      const bool over = first + ROWS > end;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int r0 = (i * WAVES + wave) * RPI, r = r0 + lane / L::NP;
-        const int piece = (lane % L::NP) ^ L::swizzle(r);
-        const int rr = last && first + r >= end ? end - 1 - first : r;
-        if (DP == dh || piece * L::PE < dh)
-          __builtin_amdgcn_global_load_lds((mfma::gbl_cvoid_t *)(p0 + rr * stride + piece * L::PE),
-                                           (mfma::lds_void_t *)(tile + r0 * DP), 16, 0, 0);
+        uint32_t at = offset[i];
+        if (over) {
+          const int r = row(i, wave, here(lane));
+          at -= max(0, first + r - (end - 1)) * (uint32_t)stride * (uint32_t)sizeof(T);
+        }
+        if (DP == dh || piece(row(i, wave, lane), lane) * L::PE < dh)
+          copy_to_lds<16>(p0, at, tile + (i * WAVES + wave) * RPI * DP);
       }
     } else {
+      const int ln = here(lane), width = here(dh);
 #pragma unroll 1
       for (int i = 0; i < NI; ++i) {
-        const int r = (i * WAVES + wave) * RPI + lane / L::NP, piece = lane % L::NP;
-        const int row = first + r < end ? first + r : end - 1;
+        const int r = row(i, wave, ln), p = ln % L::NP;
+        const int from = first + r < end ? first + r : end - 1;
         T v[L::PE];
-        load_some<T, L::PE>(base + row * stride, piece * L::PE, dh, v);
+        load_some<T, L::PE>(base + from * stride, p * L::PE, width, v);
 #pragma unroll
-        for (int e = 0; e < L::PE; ++e) tile[L::at(r, piece) + e] = fixed(v[e], fix);
+        for (int e = 0; e < L::PE; ++e) tile[L::at(r, p) + e] = fixed(v[e], fix);
       }
     }
   }

@@ -32,8 +32,9 @@ __device__ __forceinline__ bool all_finite(const f32x16 (&x)[N]) {
 // A lane's results x scale to its row of dh channels in memory. kCount leaves NaN there where
 // something was counted and zero elsewhere, and kFinite adds to that.
 template <typename T, int DP>
-__device__ __forceinline__ void store_row(T *row, const f32x16 (&x)[DP / 32], float scale, int h,
-                                          int dh, int fix) {
+__device__ __forceinline__ void store_row(T *row, const f32x16 (&x)[DP / 32], float scale, int half,
+                                          int width, int fix) {
+  const int h = here(half), dh = here(width);
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -82,6 +83,7 @@ constexpr int step_rows() { return sizeof(T) == 2 ? 64 : 32; }
 // The running maximum may fall behind by this much (in log2): weights are then up to 2^8,
 // which costs neither bf16 nor fp32 precision, and the sums are seldom rescaled.
 constexpr float kSlack = 8.f;
+constexpr int kAhead = 4;  // operands read from LDS ahead of their products
 
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) {
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
   constexpr int KS = step_rows<T>(), NT = KS / 32;
   using C = Copier<T, DP, KS, kWaves>;
   extern __shared__ __align__(16) char smem[];
-  T *const buf = (T *)smem;  // [2][K tile, V tile]
+  T *const buf = (T *)smem;  // two tiles of keys, two of values
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const Work w = work_of(a, tiles);
   if (w.tile < 0) return;
@@ -102,56 +104,71 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
   const int q0 = first + kRows * wave, qi = q0 + (l & 31);
   const int qr = min(qi, lq - 1);
   const T *qp = (const T *)a.q.p + (rq.start + qr) * a.q.tok_stride + w.head * a.q.head_stride;
-  const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh);
-  const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh);
+  const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh, wave, l);
+  const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh, wave, l);
   Frag<T> q[L::STEPS];
 #pragma unroll
   for (int i = 0; i < L::STEPS; ++i) q[i] = with_sign<T>(load_frag<T>(qp, i, h, a.dh), a.scale);
   const Seen mine = seen_by(a, qi, lq, lk);
   const Seen head = seen_by(a, first, lq, lk), tail = seen_by(a, min(first + kBlock, lq) - 1, lq, lk);
-  // of this wave's rows (those behind the last query are not stored)
+  // what all, and what some, of this wave's rows see (those behind the last are not stored)
   const Seen wf = seen_by(a, q0, lq, lk), wl = seen_by(a, q0 + kRows - 1, lq, lk);
   const float c = log2_scale(a.scale);
   if (a.dh != DP) {
     clear(buf, 4 * KS * DP, tid, kThreads);
     __syncthreads();
   }
-  f32x16 acc[DP / 32];
-  float m, sum;
+  f32x16 acc[DP / 32], x[NT];
+  Frag<T> p[KS / 16], v[kAhead];
+  float m, sum, mc = 0.f;
   const int begin = head.lo / KS * KS;
+  constexpr int N = KS / 16 * (DP / 32), PER = 16 * NT / N;
+  const auto key = [&](const T *kt, int n) __attribute__((always_inline)) {
+    return L::row_frag(kt, 32 * (n % NT) + (l & 31), n / NT, h);
+  };
+  const auto value = [&](const T *vt, int n) __attribute__((always_inline)) {
+    return L::col_frag(vt, 16 * (n / (DP / 32)), 32 * (n % (DP / 32)), l);
+  };
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
+#pragma unroll
+    for (int i = 0; i < KS / 16; ++i) p[i] = zero_frag<T>();
     m = -INFINITY;
     sum = 0.f;
-    int cur = 0;
-    if (begin < tail.hi) {
-      kc.issue(buf, begin, lk, wave, l, kAsIs);
-      vc.issue(buf + KS * DP, begin, lk, wave, l, fix);
-    }
+    int cur = 0;  // this tile's buffers; the other value buffer holds the tile before
+    if (begin < tail.hi) kc.issue(buf, begin, lk, a.dh, wave, l, kAsIs);
+    clear(buf + 3 * KS * DP, KS * DP, tid, kThreads);  // no tile before the first
     for (int k0 = begin; k0 < tail.hi; k0 += KS) {
-      // this tile has landed, and no wave reads the other one any more
+      // this tile's keys and the values of the one before have landed, and no wave reads
+      // what is overwritten now: the keys and values of the tiles before those
       mfma::wait_vm<0>();
       mfma::lds_barrier();
-      const T *const kt = buf + cur * 2 * KS * DP, *const vt = kt + KS * DP;
+      const T *const kt = buf + cur * KS * DP, *const before = buf + (2 + (cur ^ 1)) * KS * DP;
+      vc.issue(buf + (2 + cur) * KS * DP, k0, lk, a.dh, wave, l, fix);
       cur ^= 1;
-      if (k0 + KS < tail.hi) {
-        T *const next = buf + cur * 2 * KS * DP;
-        kc.issue(next, k0 + KS, lk, wave, l, kAsIs);
-        vc.issue(next + KS * DP, k0 + KS, lk, wave, l, fix);
-      }
-      if (k0 >= wl.hi || k0 + KS <= wf.lo) continue;  // nothing here for this wave
+      if (k0 + KS < tail.hi) kc.issue(buf + cur * KS * DP, k0 + KS, lk, a.dh, wave, l, kAsIs);
       // whether the lane's query sees its key j of the tile
       const int from = k0 + 4 * h - mine.lo;
       const unsigned keys = max(0, mine.hi - mine.lo);
       const auto sees = [&](int j) { return (unsigned)(from + j) < keys; };
-      f32x16 x[NT];
+      {
+        constexpr int M = NT * L::STEPS;
+        Frag<T> k[kAhead];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) x[t] = f32x16{};
+        for (int n = 0; n < kAhead; ++n) k[n] = key(kt, n);
 #pragma unroll
-      for (int i = 0; i < L::STEPS; ++i)
+        for (int t = 0; t < NT; ++t) x[t] = f32x16{};
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] = mma(L::row_frag(kt, 32 * t + (l & 31), i, h), q[i], x[t]);
+        for (int n = 0; n < M; ++n) {
+          x[n % NT] = mma(k[n % kAhead], q[n / NT], x[n % NT]);
+          if (n + kAhead < M) k[n % kAhead] = key(kt, n + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) v[n] = value(before, n);
       if (k0 + KS > wf.hi || k0 < wl.lo) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -165,25 +182,40 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, x[t][i]);
-      top = fmaxf(top, other_half(top));
-      if (__ballot((top - m) * c > kSlack)) {
+      top = half_max(top);
+      const bool rescale = __ballot((top - m) * c > kSlack) != 0;
+      float f = 1.f;
+      if (rescale) {
         const float next = fmaxf(m, top);
-        const float f = next == -INFINITY ? 1.f : exp2_((m - next) * c);
+        f = next == -INFINITY ? 1.f : exp2_((m - next) * c);
         m = next;
+        mc = m == -INFINITY ? 0.f : m * c;
         sum *= f;
+      }
+      // The tile before is added to the values while this one's scores become weights: the
+      // matrix cores work on the one, the vector units on the other.
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        f32x16 &o = acc[n % (DP / 32)];
+        o = mma(v[n % kAhead], p[n / (DP / 32)], o);
+        if (n + kAhead < N) v[n % kAhead] = value(before, n + kAhead);
+#pragma unroll
+        for (int e = PER * n; e < PER * (n + 1); ++e) {
+          float weight = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -mc));
+          asm volatile("" : "+v"(weight));  // here, not behind the products
+          x[e / 16][e % 16] = weight;
+          part[e % 4] += weight;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      if (rescale) {
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[d][e] *= f;
       }
-      const float mc = m == -INFINITY ? 0.f : m * c;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[t][i] = exp2_(__builtin_fmaf(x[t][i], c, -mc));
-          sum += x[t][i];
-        }
       if (fix == kCount) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -193,15 +225,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
           }
       }
 #pragma unroll
-      for (int i = 0; i < KS / 16; ++i) {
-        const Frag<T> p = as_operand<T>(x[i / 2], i % 2);
-#pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
-          acc[d] = mma(L::col_frag(vt, 16 * i, 32 * d, l), p, acc[d]);
-      }
+      for (int i = 0; i < KS / 16; ++i) p[i] = as_operand<T>(x[i / 2], i % 2);
     }
+    mfma::wait_vm<0>();
+    mfma::lds_barrier();
+    const T *const last = buf + (2 + (cur ^ 1)) * KS * DP;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      acc[n % (DP / 32)] = mma(value(last, n), p[n / (DP / 32)], acc[n % (DP / 32)]);
     if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
-    const float total = sum + other_half(sum);
+    const float total = half_sum(sum);
     if (qi < lq) {
       const bool none = mine.lo >= mine.hi;
       T *const op = (T *)a.o.p + (rq.start + qi) * a.o.tok_stride + w.head * a.o.head_stride;
@@ -267,8 +300,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
   const int64_t qr = rq.start + min(qi, lq - 1);
   const T *qp = (const T *)a.q.p + qr * a.q.tok_stride + w.head * a.q.head_stride;
   const T *yp = (const T *)a.dy.p + qr * a.dy.tok_stride + w.head * a.dy.head_stride;
-  const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh);
-  const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh);
+  const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh, wave, l);
+  const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh, wave, l);
   Frag<T> q[L::STEPS], dy[L::STEPS];
 #pragma unroll
   for (int i = 0; i < L::STEPS; ++i) {
@@ -291,8 +324,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
     for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
     int cur = 0;
     if (begin < tail.hi) {
-      kc.issue(buf, begin, lk, wave, l, fix);
-      vc.issue(buf + KS * DP, begin, lk, wave, l, kAsIs);
+      kc.issue(buf, begin, lk, a.dh, wave, l, fix);
+      vc.issue(buf + KS * DP, begin, lk, a.dh, wave, l, kAsIs);
     }
     for (int k0 = begin; k0 < tail.hi; k0 += KS) {
       mfma::wait_vm<0>();
@@ -301,8 +334,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
       cur ^= 1;
       if (k0 + KS < tail.hi) {
         T *const next = buf + cur * 2 * KS * DP;
-        kc.issue(next, k0 + KS, lk, wave, l, fix);
-        vc.issue(next + KS * DP, k0 + KS, lk, wave, l, kAsIs);
+        kc.issue(next, k0 + KS, lk, a.dh, wave, l, fix);
+        vc.issue(next + KS * DP, k0 + KS, lk, a.dh, wave, l, kAsIs);
       }
       if (k0 >= wl.hi || k0 + KS <= wf.lo) continue;
       const bool whole = k0 + KS <= wf.hi && k0 >= wl.lo;
@@ -398,14 +431,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) 
   const auto issue = [&](int g, int i0, int b, int fix) __attribute__((always_inline)) {
     const int hd = kv * group + g;
     T *const t = buf + b * 2 * QS * DP;
-    const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + hd * a.q.head_stride, a.q.tok_stride, a.dh);
-    const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride, a.dh);
-    qc.issue(t, i0, lq, wave, l, fix);
-    yc.issue(t + QS * DP, i0, lq, wave, l, fix);
+    const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + hd * a.q.head_stride, a.q.tok_stride, a.dh, wave, l);
+    const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride, a.dh, wave, l);
+    qc.issue(t, i0, lq, a.dh, wave, l, fix);
+    yc.issue(t + QS * DP, i0, lq, a.dh, wave, l, fix);
     if (wave < 2) {
-      const float *src = (wave ? a.delta : a.lse2) + hd * a.n_q + rq.start + min(i0 + l, lq - 1);
-      __builtin_amdgcn_global_load_lds((mfma::gbl_cvoid_t *)src,
-                                       (mfma::lds_void_t *)(stats + (2 * b + wave) * 64), 4, 0, 0);
+      const float *src = (wave ? a.delta : a.lse2) + hd * a.n_q + rq.start;
+      copy_to_lds<4>(src, 4 * (uint32_t)min(i0 + l, lq - 1), stats + (2 * b + wave) * 64);
     }
   };
   f32x16 dk[DP / 32], dv[DP / 32];

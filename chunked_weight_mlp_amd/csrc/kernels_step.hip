@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void k_step(StepArgs a, Plan plan) {
         x[i] = there >> r & 1 ? x[i] : -INFINITY;
         top = fmaxf(top, x[i]);
       }
-      top = fmaxf(top, other_half(top));
+      top = half_max(top);
       const float next = fmaxf(m, top);
       const float base = next == -INFINITY ? 0.f : next;
       const float f = exp2_((m - base) * c);
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void k_step(StepArgs a, Plan plan) {
       }
       __builtin_amdgcn_wave_barrier();
     }
-    sum += other_half(sum);
+    sum = half_sum(sum);
     // the waves' results, joined through LDS
     __syncthreads();
     float *const wm = (float *)smem, *const ws = wm + kWaves * 32, *const wo = ws + kWaves * 32;

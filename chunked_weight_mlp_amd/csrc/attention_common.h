@@ -30,6 +30,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 struct f32x8 {
   float v[8];
 };
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+struct F4x2 {
+  f32x4v x, y;
+};
 template <typename T>
 struct FragOf;
 template <>
@@ -104,35 +108,91 @@ struct Tile {
   }
   __device__ static __forceinline__ int at(int r, int p) { return r * DP + ((p ^ swizzle(r)) * PE); }
 
-  // Operand values: channels 16 s + 8 h .. + 7 of row r.
-  __device__ static __forceinline__ Frag<T> row_frag(const T *tile, int r, int s, int h) {
+};
+
+// Reads of operands from tiles at LDS addresses kept in registers, so that a read costs no
+// arithmetic: an address for each place of the pattern in a row, the rest in the instruction.
+// move() goes to another tile that far away.
+typedef __attribute__((address_space(3))) const char *lds_ptr;
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at, int offset) {
+  return *(__attribute__((address_space(3))) const V *)((lds_ptr)(uintptr_t)at + offset);
+}
+
+// Operand values: channels 16 s + 8 h .. + 7 of row r0 + l % 32 (r0 a multiple of 32).
+template <typename T, int DP>
+struct RowReader {
+  using L = Tile<T, DP>;
+  uint32_t a[L::STEPS];
+  __device__ __forceinline__ RowReader(const T *tile, int l) {
+    const uint32_t base = (uint32_t)(uintptr_t)(mfma::lds_void_t *)tile;
+    const int r = l & 31, h = l >> 5;
+#pragma unroll
+    for (int s = 0; s < L::STEPS; ++s)
+      a[s] = base + L::at(r, sizeof(T) == 2 ? 2 * s + h : 4 * s + 2 * h) * sizeof(T);
+  }
+  __device__ __forceinline__ void move(int bytes) {
+#pragma unroll
+    for (int s = 0; s < L::STEPS; ++s) a[s] += bytes;
+  }
+  __device__ __forceinline__ Frag<T> read(int r0, int s) const {
+    const int off = r0 * DP * (int)sizeof(T);
     if constexpr (std::is_same<T, float>::value) {
-      f32x8 f;
-      *(float4 *)&f.v[0] = *(const float4 *)(tile + at(r, 4 * s + 2 * h));
-      *(float4 *)&f.v[4] = *(const float4 *)(tile + at(r, 4 * s + 2 * h + 1));
-      return f;
+      // the next piece: the tile begins on a multiple of 32 bytes, so its place differs in a bit
+      return __builtin_bit_cast(f32x8, F4x2{lds_read<f32x4v>(a[s], off), lds_read<f32x4v>(a[s] ^ 16, off)});
     } else {
-      return *(const bf16x8 *)(tile + at(r, 2 * s + h));
+      return lds_read<bf16x8>(a[s], off);
     }
   }
-  // Operand values: channel c0 + l % 32 of rows r0 + 8 (j / 4) + 4 h + j % 4, j < 8
-  // (r0 a multiple of 16). In bf16 by two transposing reads: 16 lanes read 4 rows x 16
-  // channels and each gets one channel of the 4 rows.
-  __device__ static __forceinline__ Frag<T> col_frag(const T *tile, int r0, int c0, int l) {
-    if constexpr (std::is_same<T, float>::value) {
-      f32x8 f;
-      const int c = c0 + (l & 31);
+};
+
+// Operand values: channel 32 d + l % 32 of rows r0 + 8 (j / 4) + 4 h + j % 4, j < 8 (r0 a
+// multiple of 16). In bf16 by two transposing reads: 16 lanes read 4 rows x 16 channels and
+// each gets one channel of the 4 rows. The upper rows' swizzle differs by 2 pieces.
+template <typename T, int DP>
+struct ColReader {
+  using L = Tile<T, DP>;
+  uint32_t lo[DP / 32], hi[DP / 32];
+  __device__ __forceinline__ ColReader(const T *tile, int l) {
+    const uint32_t base = (uint32_t)(uintptr_t)(mfma::lds_void_t *)tile;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        f.v[j] = tile[at(r0 + 8 * (j / 4) + 4 * (l >> 5) + j % 4, c / PE) + c % PE];
+    for (int d = 0; d < DP / 32; ++d) {
+      const int r = 4 * (l >> 5) + (sizeof(T) == 2 ? (l & 15) >> 2 : 0);
+      const int c = 32 * d + (sizeof(T) == 2 ? 16 * ((l >> 4) & 1) + 4 * (l & 3) : l & 31);
+      lo[d] = base + (L::at(r, c / L::PE) + c % L::PE) * sizeof(T);
+      hi[d] = base + (L::at(r + 8, c / L::PE) + c % L::PE) * sizeof(T);
+    }
+  }
+  __device__ __forceinline__ void move(int bytes) {
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) {
+      lo[d] += bytes;
+      hi[d] += bytes;
+    }
+  }
+  __device__ __forceinline__ Frag<T> read(int r0, int d) const {
+    const int off = r0 * DP * (int)sizeof(T);
+    if constexpr (std::is_same<T, float>::value) {
+      // row r + j % 4: its swizzle differs from row r's in bits 2 and 3 of the piece
+      f32x8 f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t at = j < 4 ? lo[d] : hi[d];
+        f.v[j] = lds_read<float>(at ^ (swizzle_step(j % 4)), off + (j % 4) * DP * 4);
+      }
       return f;
     } else {
-      const int r = r0 + 4 * (l >> 5) + ((l & 15) >> 2);
-      const int c = c0 + 16 * ((l >> 4) & 1) + 4 * (l & 3);
-      const mfma::v4i16 lo = mfma::ds_read_tr16(tile + at(r, c / 8) + c % 8);
-      const mfma::v4i16 hi = mfma::ds_read_tr16(tile + at(r + 8, c / 8) + c % 8);
-      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      typedef __attribute__((address_space(3))) mfma::v4i16 lds_v4;
+      const mfma::v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_v4 *)((__attribute__((address_space(3))) char *)(uintptr_t)lo[d] + off));
+      const mfma::v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_v4 *)((__attribute__((address_space(3))) char *)(uintptr_t)hi[d] + off));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
+  }
+  // bytes by which the swizzles of rows r and r + j, r a multiple of 4, differ
+  __device__ static constexpr int swizzle_step(int j) {
+    return 16 * (L::NP >= 16 ? j << 2 : (j >> 1) << 2);
   }
 };
 

@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
   using L = Tile<T, DP>;
   constexpr int KS = step_rows<T>(), NT = KS / 32;
   using C = Copier<T, DP, KS, kWaves>;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;  // two tiles of keys, two of values
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const Work w = work_of(a, tiles);
@@ -123,12 +123,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
   float m, sum, mc = 0.f;
   const int begin = head.lo / KS * KS;
   constexpr int N = KS / 16 * (DP / 32), PER = 16 * NT / N;
-  const auto key = [&](const T *kt, int n) __attribute__((always_inline)) {
-    return L::row_frag(kt, 32 * (n % NT) + (l & 31), n / NT, h);
-  };
-  const auto value = [&](const T *vt, int n) __attribute__((always_inline)) {
-    return L::col_frag(vt, 16 * (n / (DP / 32)), 32 * (n % (DP / 32)), l);
-  };
+  constexpr int TILE = KS * DP * (int)sizeof(T);
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
@@ -137,6 +132,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
     m = -INFINITY;
     sum = 0.f;
     int cur = 0;  // this tile's buffers; the other value buffer holds the tile before
+    RowReader<T, DP> kr(buf, l);
+    ColReader<T, DP> vr(buf + 3 * KS * DP, l);
+    const auto key = [&](int n) __attribute__((always_inline)) { return kr.read(32 * (n % NT), n / NT); };
+    const auto value = [&](int n) __attribute__((always_inline)) {
+      return vr.read(16 * (n / (DP / 32)), n % (DP / 32));
+    };
     if (begin < tail.hi) kc.issue(buf, begin, lk, a.dh, wave, l, kAsIs);
     clear(buf + 3 * KS * DP, KS * DP, tid, kThreads);  // no tile before the first
     for (int k0 = begin; k0 < tail.hi; k0 += KS) {
@@ -144,7 +145,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
       // what is overwritten now: the keys and values of the tiles before those
       mfma::wait_vm<0>();
       mfma::lds_barrier();
-      const T *const kt = buf + cur * KS * DP, *const before = buf + (2 + (cur ^ 1)) * KS * DP;
       vc.issue(buf + (2 + cur) * KS * DP, k0, lk, a.dh, wave, l, fix);
       cur ^= 1;
       if (k0 + KS < tail.hi) kc.issue(buf + cur * KS * DP, k0 + KS, lk, a.dh, wave, l, kAsIs);
@@ -156,19 +156,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
         constexpr int M = NT * L::STEPS;
         Frag<T> k[kAhead];
 #pragma unroll
-        for (int n = 0; n < kAhead; ++n) k[n] = key(kt, n);
+        for (int n = 0; n < kAhead; ++n) k[n] = key(n);
 #pragma unroll
         for (int t = 0; t < NT; ++t) x[t] = f32x16{};
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < M; ++n) {
           x[n % NT] = mma(k[n % kAhead], q[n / NT], x[n % NT]);
-          if (n + kAhead < M) k[n % kAhead] = key(kt, n + kAhead);
+          if (n + kAhead < M) k[n % kAhead] = key(n + kAhead);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
 #pragma unroll
-      for (int n = 0; n < kAhead; ++n) v[n] = value(before, n);
+      for (int n = 0; n < kAhead; ++n) v[n] = value(n);
       if (k0 + KS > wf.hi || k0 < wl.lo) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -199,13 +199,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
       for (int n = 0; n < N; ++n) {
         f32x16 &o = acc[n % (DP / 32)];
         o = mma(v[n % kAhead], p[n / (DP / 32)], o);
-        if (n + kAhead < N) v[n % kAhead] = value(before, n + kAhead);
+        if (n + kAhead < N) v[n % kAhead] = value(n + kAhead);
 #pragma unroll
         for (int e = PER * n; e < PER * (n + 1); ++e) {
           float weight = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -mc));
           asm volatile("" : "+v"(weight));  // here, not behind the products
           x[e / 16][e % 16] = weight;
           part[e % 4] += weight;
+          asm volatile("" : "+v"(part[e % 4]));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -226,13 +227,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) 
       }
 #pragma unroll
       for (int i = 0; i < KS / 16; ++i) p[i] = as_operand<T>(x[i / 2], i % 2);
+      kr.move(cur ? TILE : -TILE);
+      vr.move(cur ? -TILE : TILE);
     }
     mfma::wait_vm<0>();
     mfma::lds_barrier();
-    const T *const last = buf + (2 + (cur ^ 1)) * KS * DP;
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      acc[n % (DP / 32)] = mma(value(last, n), p[n / (DP / 32)], acc[n % (DP / 32)]);
+      acc[n % (DP / 32)] = mma(value(n), p[n / (DP / 32)], acc[n % (DP / 32)]);
     if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
     const float total = half_sum(sum);
     if (qi < lq) {
@@ -283,9 +285,9 @@ __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
-  constexpr int KS = step_rows<T>(), NT = KS / 32;
+  constexpr int KS = step_rows<T>(), NT = KS / 32, STAGE = 2 * KS * DP * (int)sizeof(T);
   using C = Copier<T, DP, KS, kWaves>;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;  // [2][K tile, V tile]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const Work w = work_of(a, tiles);
@@ -323,6 +325,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
     int cur = 0;
+    RowReader<T, DP> rows(buf, l);
+    ColReader<T, DP> cols(buf, l);
     if (begin < tail.hi) {
       kc.issue(buf, begin, lk, a.dh, wave, l, fix);
       vc.issue(buf + KS * DP, begin, lk, a.dh, wave, l, kAsIs);
@@ -330,14 +334,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
     for (int k0 = begin; k0 < tail.hi; k0 += KS) {
       mfma::wait_vm<0>();
       mfma::lds_barrier();
-      const T *const kt = buf + cur * 2 * KS * DP, *const vt = kt + KS * DP;
       cur ^= 1;
       if (k0 + KS < tail.hi) {
         T *const next = buf + cur * 2 * KS * DP;
         kc.issue(next, k0 + KS, lk, a.dh, wave, l, fix);
         vc.issue(next + KS * DP, k0 + KS, lk, a.dh, wave, l, kAsIs);
       }
-      if (k0 >= wl.hi || k0 + KS <= wf.lo) continue;
       const bool whole = k0 + KS <= wf.hi && k0 >= wl.lo;
       const int from = k0 + 4 * h - mine.lo;
       const unsigned keys = max(0, mine.hi - mine.lo);
@@ -347,8 +349,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
         f32x16 x{}, dp{};
 #pragma unroll
         for (int i = 0; i < L::STEPS; ++i) {
-          x = mma(L::row_frag(kt, 32 * t + (l & 31), i, h), q[i], x);
-          dp = mma(L::row_frag(vt, 32 * t + (l & 31), i, h), dy[i], dp);
+          x = mma(rows.read(32 * t, i), q[i], x);
+          dp = mma(rows.read(KS + 32 * t, i), dy[i], dp);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = exp2_(__builtin_fmaf(x[i], c, -lse)) * (dp[i] - delta);
@@ -366,9 +368,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
           const Frag<T> ds = as_operand<T>(x, i);
 #pragma unroll
           for (int d = 0; d < DP / 32; ++d)
-            acc[d] = mma(L::col_frag(kt, 32 * t + 16 * i, 32 * d, l), ds, acc[d]);
+            acc[d] = mma(cols.read(32 * t + 16 * i, d), ds, acc[d]);
         }
       }
+      rows.move(cur ? STAGE : -STAGE);
+      cols.move(cur ? STAGE : -STAGE);
     }
     if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
     if (qi < lq)
@@ -384,9 +388,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
-  constexpr int QS = step_rows<T>(), NT = QS / 32;
+  constexpr int QS = step_rows<T>(), NT = QS / 32, STAGE = 2 * QS * DP * (int)sizeof(T);
   using C = Copier<T, DP, QS, kWaves>;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;                            // [2][q tile, dy tile]
   float *const stats = (float *)(buf + 4 * QS * DP);   // [2][lse, delta][64]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
@@ -419,7 +423,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) 
   };
   const int my_from = from(kj), my_to = kj < lk ? to(kj) : 0;
   const int q_from = from(first), q_to = to(min(first + kBlock, lk) - 1);
-  const int w_from = from(k0), w_to = k0 < lk ? to(min(k0 + kRows, lk) - 1) : 0;
   const int all_from = from(k0 + kRows - 1), all_to = k0 + kRows <= lk ? to(k0) : 0;
   const int begin = q_from / QS * QS, steps = q_to > begin ? (q_to - begin + QS - 1) / QS : 0;
   const float c = log2_scale(a.scale);
@@ -445,28 +448,28 @@ __global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) 
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = f32x16{};
     int cur = 0;
+    RowReader<T, DP> rows(buf, l);
+    ColReader<T, DP> cols(buf, l);
     if (steps > 0) issue(0, begin, 0, fix);
     for (int g = 0, n = 0; g < group && steps > 0;) {
       mfma::wait_vm<0>();
       mfma::lds_barrier();
-      const T *const qt = buf + cur * 2 * QS * DP, *const yt = qt + QS * DP;
       const float *const lse = stats + 2 * cur * 64, *const delta = lse + 64;
       cur ^= 1;
       const int i0 = begin + n * QS;
       if (++n == steps) n = 0, ++g;
       if (g < group) issue(g, begin + n * QS, cur, fix);
-      if (i0 >= w_to || i0 + QS <= w_from) continue;
       const bool whole = i0 >= all_from && i0 + QS <= all_to;
       const int rel = i0 + 4 * h - my_from;
-      const unsigned rows = max(0, my_to - my_from);
-      const auto seen = [&](int r) { return (unsigned)(rel + r) < rows; };
+      const unsigned queries = max(0, my_to - my_from);
+      const auto seen = [&](int r) { return (unsigned)(rel + r) < queries; };
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         f32x16 x{}, y{};
 #pragma unroll
         for (int i = 0; i < L::STEPS; ++i) {
-          x = mma(L::row_frag(qt, 32 * t + (l & 31), i, h), k[i], x);
-          y = mma(L::row_frag(yt, 32 * t + (l & 31), i, h), v[i], y);
+          x = mma(rows.read(32 * t, i), k[i], x);
+          y = mma(rows.read(QS + 32 * t, i), v[i], y);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -493,11 +496,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) 
           const Frag<T> p = as_operand<T>(x, i), ds = as_operand<T>(y, i);
 #pragma unroll
           for (int d = 0; d < DP / 32; ++d) {
-            dv[d] = mma(L::col_frag(yt, 32 * t + 16 * i, 32 * d, l), p, dv[d]);
-            dk[d] = mma(L::col_frag(qt, 32 * t + 16 * i, 32 * d, l), ds, dk[d]);
+            dv[d] = mma(cols.read(QS + 32 * t + 16 * i, d), p, dv[d]);
+            dk[d] = mma(cols.read(32 * t + 16 * i, d), ds, dk[d]);
           }
         }
       }
+      rows.move(cur ? STAGE : -STAGE);
+      cols.move(cur ? STAGE : -STAGE);
     }
     if (fix == kAsIs && !__syncthreads_and(all_finite(dk) && all_finite(dv))) continue;
     if (kj < lk) {

@@ -88,9 +88,11 @@ __device__ const uint4 zero_row[kHeadMaxDim * 4 / 16] = {};
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads) void k_step(StepArgs a, Plan plan) {
   using L = Tile<T, DP>;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, h = l >> 5, col = l & 31;
   T *const kt = (T *)smem + wave * 64 * DP, *const vt = kt + 32 * DP;
+  const RowReader<T, DP> rows(kt, l);
+  const ColReader<T, DP> vals(vt, l);
   const int hk = a.cache.k_heads, dh = a.cache.head_dim, ps = a.cache.page_size;
   const int group = a.hq / hk, chunks = chunks_of(a.hq, hk);
   const int block = blockIdx.x, chunk = blockIdx.y;
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void k_step(StepArgs a, Plan plan) {
       __builtin_amdgcn_wave_barrier();
       f32x16 x{};
 #pragma unroll
-      for (int i = 0; i < L::STEPS; ++i) x = mma(L::row_frag(kt, col, i, h), q[i], x);
+      for (int i = 0; i < L::STEPS; ++i) x = mma(rows.read(0, i), q[i], x);
       float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(kThreads) void k_step(StepArgs a, Plan plan) {
         const Frag<T> p = as_operand<T>(x, i);
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
-          acc[d] = mma(L::col_frag(vt, 16 * i, 32 * d, l), p, acc[d]);
+          acc[d] = mma(vals.read(16 * i, d), p, acc[d]);
       }
       __builtin_amdgcn_wave_barrier();
     }

@@ -267,7 +267,7 @@ __device__ __forceinline__ T fixed(T v, int fix) {
 template <int BYTES>
 __device__ __forceinline__ void copy_to_lds(const void *base, uint32_t offset, const void *dst) {
   static_assert(BYTES == 16 || BYTES == 4, "");
-  const uint32_t at = (uint32_t)(uintptr_t)(mfma::lds_void_t *)dst;
+  const uint32_t at = __builtin_amdgcn_readfirstlane((int)(uintptr_t)(mfma::lds_void_t *)dst);
   uint32_t m0;
   if constexpr (BYTES == 16)
     asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
@@ -278,11 +278,21 @@ __device__ __forceinline__ void copy_to_lds(const void *base, uint32_t offset, c
                  "global_load_lds_dword %2, %3\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0) : "s"(at), "v"(offset), "s"(base) : "memory");
 }
+// The same from an address of each lane's own.
+__device__ __forceinline__ void copy_to_lds16(const void *src, const void *dst) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((int)(uintptr_t)(mfma::lds_void_t *)dst);
+  uint32_t m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+               "global_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0) : "s"(at), "v"(src) : "memory");
+}
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
 template <typename T>
 __device__ __forceinline__ const T *uniform(const T *p) {
-  const uint64_t v = (uint64_t)p;
-  return (const T *)((uint64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
-                     (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+  return (const T *)uniform64((uint64_t)p);
 }
 
 // Copies ROWS rows of one head into tiles, WAVES waves together: directly (16 bytes a

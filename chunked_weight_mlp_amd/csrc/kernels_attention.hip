@@ -80,13 +80,17 @@ __device__ __forceinline__ Work work_of(const AttnArgs &a, int64_t tiles) {
 // Rows of the other side a step: two steps' tiles of two blocks fit a CU's LDS.
 template <typename T>
 constexpr int step_rows() { return sizeof(T) == 2 ? 64 : 32; }
+// Blocks a CU that the registers of the forward and of dq must allow: operands of 128 fp32
+// channels take twice the registers, and their products eight times as long.
+template <typename T, int DP>
+constexpr int blocks_a_cu() { return sizeof(T) == 4 && DP > 64 ? 1 : 2; }
 // The running maximum may fall behind by this much (in log2): weights are then up to 2^8,
 // which costs neither bf16 nor fp32 precision, and the sums are seldom rescaled.
 constexpr float kSlack = 8.f;
 constexpr int kAhead = 4;  // operands read from LDS ahead of their products
 
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads, 2) void k_fwd(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
   constexpr int KS = step_rows<T>(), NT = KS / 32;
   using C = Copier<T, DP, KS, kWaves>;
@@ -283,7 +287,7 @@ __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
 
 // dq: a block's queries, over the keys that they see.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
   constexpr int KS = step_rows<T>(), NT = KS / 32, STAGE = 2 * KS * DP * (int)sizeof(T);
   using C = Copier<T, DP, KS, kWaves>;
@@ -383,37 +387,35 @@ __global__ __launch_bounds__(kThreads, 2) void k_dq(AttnArgs a, int64_t tiles) {
   }
 }
 
-// dk and dv: a block's keys, over the queries of the group's heads that see them. The steps
-// of all heads are one sequence of tiles: head g's steps are g n .. g n + n - 1.
-template <typename T, int DP>
-__global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) {
+// dk and dv: a block's keys, over the queries of the group's heads that see them. A wave
+// holds 32 NK keys: their sums and K rows in registers, their V rows in LDS, since both do
+// not fit beside the sums. Each operand read from LDS then serves NK products, which is why
+// a wave has a SIMD to itself: at 32 keys a wave LDS has as much to do as the matrix cores.
+// For 32 queries the products are, with what the vector units do beside them,
+//   scores S = Q K^T;   dP = dY V^T beside P = exp(S - lse);
+//   dV += dY^T P beside dS = P (dP - delta);   dK += Q^T dS.
+template <typename T, int DP, int NK>
+__global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
   constexpr int QS = step_rows<T>(), NT = QS / 32, STAGE = 2 * QS * DP * (int)sizeof(T);
+  constexpr int KB = NK * kBlock, ND = DP / 32, S = L::STEPS;
   using C = Copier<T, DP, QS, kWaves>;
   extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;                            // [2][q tile, dy tile]
-  float *const stats = (float *)(buf + 4 * QS * DP);   // [2][lse, delta][64]
+  T *const vt = buf + 4 * QS * DP;                     // the block's V rows
+  float *const stats = (float *)(vt + KB * DP);        // [2][lse, delta][64]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const int64_t id = blk::block_id();
   const int kv = (int)(id % a.hk);
   const int64_t tile = id / a.hk;
   if (tile >= tiles) return;
-  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.k_off, a.batch, a.n_k, kBlock, tile, l));
+  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.k_off, a.batch, a.n_k, KB, tile, l));
   const Rows rk = rows_of(a.k_off, s, a.batch, a.n_k);
   const Rows rq = s < a.batch ? rows_of(a.q_off, s, a.batch, a.n_q) : Rows{0, 0};
-  const int first = (int)(tile - (rk.start / kBlock + s)) * kBlock;
+  const int first = (int)(tile - (rk.start / KB + s)) * KB;
   if (first >= rk.len) return;
   const int lq = rq.len, lk = rk.len, group = a.hq / a.hk;
-  const int k0 = first + kRows * wave, kj = k0 + (l & 31);
-  const int64_t kr = rk.start + min(kj, lk - 1);
-  const T *kp = (const T *)a.k.p + kr * a.k.tok_stride + kv * a.k.head_stride;
-  const T *vp = (const T *)a.v.p + kr * a.v.tok_stride + kv * a.v.head_stride;
-  Frag<T> k[L::STEPS], v[L::STEPS];
-#pragma unroll
-  for (int i = 0; i < L::STEPS; ++i) {
-    k[i] = with_sign<T>(load_frag<T>(kp, i, h, a.dh), a.scale);
-    v[i] = load_frag<T>(vp, i, h, a.dh);
-  }
+  const int k0 = first + kRows * NK * wave;
   // the queries that see key j: [from(j), to(j))
   const int off = lk - lq;
   const auto from = [&](int j) { return a.causal ? max(0, j - off) : 0; };
@@ -421,93 +423,187 @@ __global__ __launch_bounds__(kThreads, 2) void k_dkv(AttnArgs a, int64_t tiles) 
     if (!a.causal || a.window <= 0) return lq;
     return (int)max((int64_t)0, min((int64_t)lq, (int64_t)j + a.window - off));
   };
-  const int my_from = from(kj), my_to = kj < lk ? to(kj) : 0;
-  const int q_from = from(first), q_to = to(min(first + kBlock, lk) - 1);
-  const int all_from = from(k0 + kRows - 1), all_to = k0 + kRows <= lk ? to(k0) : 0;
+  Frag<T> k[NK][S];
+  int my_from[NK];
+  unsigned queries[NK];
+#pragma unroll
+  for (int j = 0; j < NK; ++j) {
+    const int kj = k0 + 32 * j + (l & 31);
+    const T *kp = (const T *)a.k.p + (rk.start + min(kj, lk - 1)) * a.k.tok_stride + kv * a.k.head_stride;
+#pragma unroll
+    for (int i = 0; i < S; ++i) k[j][i] = with_sign<T>(load_frag<T>(kp, i, h, a.dh), a.scale);
+    my_from[j] = from(kj);
+    queries[j] = kj < lk ? max(0, to(kj) - my_from[j]) : 0;
+  }
+  const int q_from = from(first), q_to = to(min(first + KB, lk) - 1);
+  const int all_from = from(k0 + kRows * NK - 1), all_to = k0 + kRows * NK <= lk ? to(k0) : 0;
   const int begin = q_from / QS * QS, steps = q_to > begin ? (q_to - begin + QS - 1) / QS : 0;
   const float c = log2_scale(a.scale);
   if (a.dh != DP) {
-    clear(buf, 4 * QS * DP, tid, kThreads);
+    clear(buf, (4 * QS + KB) * DP, tid, kThreads);
     __syncthreads();
   }
-  // step n: head n / steps, queries from begin + n % steps * QS
+  const Copier<T, DP, KB, kWaves> vc((const T *)a.v.p + rk.start * a.v.tok_stride + kv * a.v.head_stride,
+                                     a.v.tok_stride, a.dh, wave, l);
+  vc.issue(vt, first, lk, a.dh, wave, l, kAsIs);
+  const RowReader<T, DP> vr(vt + kRows * NK * wave * DP, l);
   const auto issue = [&](int g, int i0, int b, int fix) __attribute__((always_inline)) {
     const int hd = kv * group + g;
     T *const t = buf + b * 2 * QS * DP;
     const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + hd * a.q.head_stride, a.q.tok_stride, a.dh, wave, l);
-    const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride, a.dh, wave, l);
+    const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride, a.dh, wave,
+               l);
     qc.issue(t, i0, lq, a.dh, wave, l, fix);
     yc.issue(t + QS * DP, i0, lq, a.dh, wave, l, fix);
     if (wave < 2) {
       const float *src = (wave ? a.delta : a.lse2) + hd * a.n_q + rq.start;
-      copy_to_lds<4>(src, 4 * (uint32_t)min(i0 + l, lq - 1), stats + (2 * b + wave) * 64);
+      copy_to_lds<4>(uniform(src), 4 * (uint32_t)min(i0 + l, lq - 1), stats + (2 * b + wave) * 64);
     }
   };
-  f32x16 dk[DP / 32], dv[DP / 32];
+  f32x16 dk[NK][ND], dv[NK][ND];
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = f32x16{};
+    for (int j = 0; j < NK; ++j)
+#pragma unroll
+      for (int d = 0; d < ND; ++d) dk[j][d] = dv[j][d] = f32x16{};
     int cur = 0;
     RowReader<T, DP> rows(buf, l);
     ColReader<T, DP> cols(buf, l);
     if (steps > 0) issue(0, begin, 0, fix);
+    // step n of head g: queries from begin + n QS
     for (int g = 0, n = 0; g < group && steps > 0;) {
       mfma::wait_vm<0>();
       mfma::lds_barrier();
-      const float *const lse = stats + 2 * cur * 64, *const delta = lse + 64;
+      const float *const lse = stats + 2 * cur * 64 + 4 * h, *const delta = lse + 64;
       cur ^= 1;
       const int i0 = begin + n * QS;
       if (++n == steps) n = 0, ++g;
       if (g < group) issue(g, begin + n * QS, cur, fix);
       const bool whole = i0 >= all_from && i0 + QS <= all_to;
-      const int rel = i0 + 4 * h - my_from;
-      const unsigned queries = max(0, my_to - my_from);
-      const auto seen = [&](int r) { return (unsigned)(rel + r) < queries; };
+      const auto seen = [&](int j, int r) { return (unsigned)(i0 + 4 * h - my_from[j] + r) < queries[j]; };
+      // the operands of the products in their order: S steps of S and dP, 2 ND of dV and dK
+      constexpr int LEN = 2 * S + 4 * ND;
+      const auto operand = [&](int m) __attribute__((always_inline)) {
+        const int t = m / LEN, r = 32 * t, o = m % LEN;
+        if (o < S) return rows.read(r, o);
+        if (o < 2 * S) return rows.read(QS + r, o - S);
+        const int e = (o - 2 * S) % (2 * ND), q = (o - 2 * S) / (2 * ND);
+        return cols.read((q ? 0 : QS) + r + 16 * (e / ND), e % ND);
+      };
+      Frag<T> f[kAhead], vb[2][NK];
+#pragma unroll
+      for (int m = 0; m < kAhead; ++m) f[m] = operand(m);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        f32x16 x{}, y{};
+        const int m0 = t * LEN;
+        // the next operand, in the place of the one just used
+        const auto refill = [&](int m) __attribute__((always_inline)) {
+          if (m + kAhead < NT * LEN) f[m % kAhead] = operand(m + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        f32x16 x[NK], y[NK];
+        float st[16];
 #pragma unroll
-        for (int i = 0; i < L::STEPS; ++i) {
-          x = mma(rows.read(32 * t, i), k[i], x);
-          y = mma(rows.read(QS + 32 * t, i), v[i], y);
+        for (int i = 0; i < 4; ++i) {
+          const float4 e = *(const float4 *)(lse + 32 * t + 8 * i);
+          st[4 * i] = e.x, st[4 * i + 1] = e.y, st[4 * i + 2] = e.z, st[4 * i + 3] = e.w;
+        }
+#pragma unroll
+        for (int j = 0; j < NK; ++j) x[j] = y[j] = f32x16{};
+#pragma unroll
+        for (int j = 0; j < NK; ++j) vb[0][j] = vr.read(32 * j, 0);
+#pragma unroll
+        for (int o = 0; o < S; ++o) {
+#pragma unroll
+          for (int j = 0; j < NK; ++j) x[j] = mma(f[(m0 + o) % kAhead], k[j][o], x[j]);
+          refill(m0 + o);
+        }
+        constexpr int PB = 16 * NK / S, PC = 16 * NK / (2 * ND);
+#pragma unroll
+        for (int o = 0; o < S; ++o) {
+#pragma unroll
+          for (int j = 0; j < NK; ++j) y[j] = mma(f[(m0 + S + o) % kAhead], vb[o % 2][j], y[j]);
+          if (o + 1 < S) {
+#pragma unroll
+            for (int j = 0; j < NK; ++j) vb[(o + 1) % 2][j] = vr.read(32 * j, o + 1);
+          }
+#pragma unroll
+          for (int e = PB * o; e < PB * (o + 1); ++e) {
+            float p = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -st[e % 16]));
+            asm volatile("" : "+v"(p));  // here, not behind the products
+            x[e / 16][e % 16] = p;
+          }
+          refill(m0 + S + o);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 e = *(const float4 *)(lse + 32 * t + 8 * i + 4 * h);
-          const float4 d = *(const float4 *)(delta + 32 * t + 8 * i + 4 * h);
-          const float ee[4] = {e.x, e.y, e.z, e.w}, dd[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[4 * i + j] = exp2_(__builtin_fmaf(x[4 * i + j], c, -ee[j]));
-            y[4 * i + j] = x[4 * i + j] * (y[4 * i + j] - dd[j]);
-          }
+          const float4 e = *(const float4 *)(delta + 32 * t + 8 * i);
+          st[4 * i] = e.x, st[4 * i + 1] = e.y, st[4 * i + 2] = e.z, st[4 * i + 3] = e.w;
         }
         if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!seen(32 * t + 8 * (i / 4) + i % 4)) x[i] = y[i] = 0.f;
+          for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!seen(j, 32 * t + 8 * (i / 4) + i % 4)) x[j][i] = 0.f;
         }
         if (fix == kCount) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = seen(32 * t + 8 * (i / 4) + i % 4) ? 1.f : 0.f;
+          for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[j][i] = seen(j, 32 * t + 8 * (i / 4) + i % 4) ? 1.f : 0.f;
+        }
+        Frag<T> w[NK][2];
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) w[j][i] = as_operand<T>(x[j], i);
+#pragma unroll
+        for (int o = 0; o < 2 * ND; ++o) {
+#pragma unroll
+          for (int j = 0; j < NK; ++j) dv[j][o % ND] = mma(f[(m0 + 2 * S + o) % kAhead], w[j][o / ND], dv[j][o % ND]);
+#pragma unroll
+          for (int e = PC * o; e < PC * (o + 1); ++e) {
+            float ds = x[e / 16][e % 16] * (y[e / 16][e % 16] - st[e % 16]);
+            asm volatile("" : "+v"(ds));
+            y[e / 16][e % 16] = ds;
+          }
+          refill(m0 + 2 * S + o);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!seen(j, 32 * t + 8 * (i / 4) + i % 4)) y[j][i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Frag<T> p = as_operand<T>(x, i), ds = as_operand<T>(y, i);
+        for (int j = 0; j < NK; ++j)
 #pragma unroll
-          for (int d = 0; d < DP / 32; ++d) {
-            dv[d] = mma(cols.read(QS + 32 * t + 16 * i, d), p, dv[d]);
-            dk[d] = mma(cols.read(32 * t + 16 * i, d), ds, dk[d]);
-          }
+          for (int i = 0; i < 2; ++i) w[j][i] = as_operand<T>(y[j], i);
+#pragma unroll
+        for (int o = 0; o < 2 * ND; ++o) {
+#pragma unroll
+          for (int j = 0; j < NK; ++j)
+            dk[j][o % ND] = mma(f[(m0 + 2 * S + 2 * ND + o) % kAhead], w[j][o / ND], dk[j][o % ND]);
+          refill(m0 + 2 * S + 2 * ND + o);
         }
       }
       rows.move(cur ? STAGE : -STAGE);
       cols.move(cur ? STAGE : -STAGE);
     }
-    if (fix == kAsIs && !__syncthreads_and(all_finite(dk) && all_finite(dv))) continue;
-    if (kj < lk) {
-      store_row<T, DP>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk, a.scale, h, a.dh, kAsIs);
-      store_row<T, DP>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv, 1.f, h, a.dh, fix);
+    bool ok = true;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) ok &= all_finite(dk[j]) && all_finite(dv[j]);
+    if (fix == kAsIs && !__syncthreads_and(ok)) continue;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      const int kj = k0 + 32 * j + here(l & 31);
+      if (kj < lk) {
+        const int64_t kr = rk.start + kj;
+        store_row<T, DP>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk[j], a.scale, h, a.dh, kAsIs);
+        store_row<T, DP>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv[j], 1.f, h, a.dh, fix);
+      }
     }
     if (fix != kCount) break;
     __syncthreads();
@@ -543,8 +639,14 @@ hipError_t attn_backward(const AttnArgs &a, hipStream_t st) {
     constexpr int DP = decltype(dp)::value;
     const size_t lds = 4 * step_rows<T>() * DP * sizeof(T);
     if (a.n_k > 0) {
-      const int64_t tiles = tiles_of(a.n_k, kBlock, a.batch);
-      k_dkv<T, DP><<<blk::grid_of(tiles * a.hk), kThreads, lds + 4 * 64 * sizeof(float), st>>>(a, tiles);
+      const auto go = [&](auto nk) {
+        constexpr int NK = decltype(nk)::value;
+        const int64_t tiles = tiles_of(a.n_k, NK * kBlock, a.batch);
+        const size_t bytes = lds + NK * kBlock * DP * sizeof(T) + 4 * 64 * sizeof(float);
+        k_dkv<T, DP, NK><<<blk::grid_of(tiles * a.hk), kThreads, bytes, st>>>(a, tiles);
+      };
+      if constexpr (sizeof(T) == 2) go(std::integral_constant<int, 2>());
+      else go(std::integral_constant<int, 1>());
     }
     if (a.n_q > 0) {
       const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);

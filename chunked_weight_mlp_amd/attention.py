@@ -24,8 +24,8 @@ from .block import (_DENSE, _call_on, _check, _dense, _dtype_of, _invalid, _is, 
 
 EXPORTS = (
     "ipttt_headnorm_forward", "ipttt_headnorm_append", "ipttt_headnorm_backward_workspace_bytes",
-    "ipttt_headnorm_backward", "ipttt_attention_forward", "ipttt_attention_backward_workspace_bytes",
-    "ipttt_attention_backward", "ipttt_attention_step_workspace_bytes", "ipttt_attention_step",
+    "ipttt_headnorm_backward", "ipttt_attention_forward_workspace_bytes", "ipttt_attention_forward",
+    "ipttt_attention_backward_workspace_bytes", "ipttt_attention_backward", "ipttt_attention_step_workspace_bytes", "ipttt_attention_step",
 )
 
 
@@ -77,7 +77,7 @@ def load() -> ctypes.CDLL:
             "ipttt_headnorm_append": [P(HeadNormDesc), h, h, h, vp, vp, i64, h, P(KVCacheDesc), P(PageTable),
                                       vp],
             "ipttt_headnorm_backward": [P(HeadNormDesc), h, h, vp, h, h, i64, h, h, vp, vp, vp, sz, vp],
-            "ipttt_attention_forward": [P(AttentionDesc), h, h, h, h, vp, vp],
+            "ipttt_attention_forward": [P(AttentionDesc), h, h, h, h, vp, vp, sz, vp],
             "ipttt_attention_backward": [P(AttentionDesc), h, h, h, h, vp, h, h, h, h, vp, sz, vp],
             "ipttt_attention_step": [P(StepDesc), h, P(KVCacheDesc), P(PageTable), vp, h, vp, vp, sz, vp],
         }
@@ -86,6 +86,7 @@ def load() -> ctypes.CDLL:
             f.argtypes, f.restype = args, ctypes.c_int
         for name, args in {
                 "ipttt_headnorm_backward_workspace_bytes": [P(HeadNormDesc), i64],
+                "ipttt_attention_forward_workspace_bytes": [P(AttentionDesc)],
                 "ipttt_attention_backward_workspace_bytes": [P(AttentionDesc)],
                 "ipttt_attention_step_workspace_bytes": [P(StepDesc), P(KVCacheDesc), P(PageTable)]}.items():
             f = getattr(lib, name)
@@ -118,9 +119,13 @@ def ipttt_headnorm_backward(desc, q, k, pos, dq, dk, n, dx_q, dx_k, dq_gamma, dk
                                           workspace_bytes, _stream(stream)))
 
 
-def ipttt_attention_forward(desc, q, k, v, o, lse, stream=None) -> None:
-    _check(load().ipttt_attention_forward(_ref(desc), _ref(q), _ref(k), _ref(v), _ref(o), _p(lse),
-                                          _stream(stream)))
+def ipttt_attention_forward_workspace_bytes(desc) -> int:
+    return load().ipttt_attention_forward_workspace_bytes(_ref(desc))
+
+
+def ipttt_attention_forward(desc, q, k, v, o, lse, workspace, workspace_bytes, stream=None) -> None:
+    _check(load().ipttt_attention_forward(_ref(desc), _ref(q), _ref(k), _ref(v), _ref(o), _p(lse), _p(workspace),
+                                          workspace_bytes, _stream(stream)))
 
 
 def ipttt_attention_backward_workspace_bytes(desc) -> int:
@@ -345,8 +350,11 @@ def attention_forward(q, k, v, offsets=None, k_offsets=None, causal: bool = True
     st = _on(q.device)
     o = torch.empty_like(q, memory_format=_DENSE)
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    _check(load().ipttt_attention_forward(ctypes.byref(desc), *views,
-                                          _heads("o", o, q.shape, q.dtype, q.device), lse.data_ptr(), st))
+    ref = ctypes.byref(desc)
+    need = load().ipttt_attention_forward_workspace_bytes(ref)
+    ws = _temp(need, q.device)
+    _check(load().ipttt_attention_forward(ref, *views, _heads("o", o, q.shape, q.dtype, q.device),
+                                          lse.data_ptr(), ws.data_ptr(), need, st))
     return o, lse
 
 

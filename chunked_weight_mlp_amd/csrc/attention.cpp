@@ -347,12 +347,20 @@ ipttt_status ipttt_headnorm_backward(const ipttt_headnorm_desc *desc, const iptt
       "head norm backward launch");
 }
 
+size_t ipttt_attention_forward_workspace_bytes(const ipttt_attention *desc) {
+  if (check_attn_sizes(desc) != IPTTT_OK) return 0;
+  return attn_q_order(*desc);
+}
+
 ipttt_status ipttt_attention_forward(const ipttt_attention *desc, const ipttt_heads *q,
                                      const ipttt_heads *k, const ipttt_heads *v,
-                                     const ipttt_heads *o, float *lse, void *hip_stream) {
+                                     const ipttt_heads *o, float *lse, void *workspace,
+                                     size_t workspace_bytes, void *hip_stream) {
   TRY(check_attn(desc, q, k, v, o, lse));
   if (desc->n_q == 0) return IPTTT_OK;
-  const AttnArgs a = attn_args(desc, q, k, v, o, lse);
+  TRY(check_workspace(workspace, workspace_bytes, attn_q_order(*desc)));
+  AttnArgs a = attn_args(desc, q, k, v, o, lse);
+  a.q_order = (int32_t *)workspace;
   const hipStream_t st = (hipStream_t)hip_stream;
   return launched(
       desc->dtype == IPTTT_BF16 ? attn_forward<__bf16>(a, st) : attn_forward<float>(a, st),
@@ -360,10 +368,9 @@ ipttt_status ipttt_attention_forward(const ipttt_attention *desc, const ipttt_he
 }
 
 size_t ipttt_attention_backward_workspace_bytes(const ipttt_attention *desc) {
-  if (!desc || desc->q_heads < 1 || desc->q_heads > kMaxHeads || desc->n_q < 0 ||
-      desc->n_q > ((int64_t)1 << 30))
-    return 0;
-  return (size_t)round_up((int64_t)desc->q_heads * desc->n_q * 8 + 1, 256);
+  if (check_attn_sizes(desc) != IPTTT_OK) return 0;
+  return attn_q_order(*desc) + attn_k_order(*desc) +
+         (size_t)round_up((int64_t)desc->q_heads * desc->n_q * 8, 256);
 }
 
 ipttt_status ipttt_attention_backward(const ipttt_attention *desc, const ipttt_heads *q,
@@ -385,7 +392,9 @@ ipttt_status ipttt_attention_backward(const ipttt_attention *desc, const ipttt_h
   a.dq = view(dq, a.n_q, a.hq);
   a.dk = view(dk, a.n_k, a.hk);
   a.dv = view(dv, a.n_k, a.hk);
-  a.delta = (float *)workspace;
+  a.q_order = (int32_t *)workspace;
+  a.k_order = (int32_t *)((char *)workspace + attn_q_order(*desc));
+  a.delta = (float *)((char *)a.k_order + attn_k_order(*desc));
   a.lse2 = a.delta + a.hq * a.n_q;
   const hipStream_t st = (hipStream_t)hip_stream;
   return launched(

@@ -135,24 +135,28 @@ struct RowReader {
 #pragma unroll
     for (int s = 0; s < L::STEPS; ++s) a[s] += bytes;
   }
-  __device__ __forceinline__ Frag<T> read(int r0, int s) const {
+  __device__ __forceinline__ Frag<T> read(int r0, int s) const { return read_from(0, r0, s); }
+  // The same of a tile that many bytes behind this one.
+  __device__ __forceinline__ Frag<T> read_from(int behind, int r0, int s) const {
     const int off = r0 * DP * (int)sizeof(T);
+    const uint32_t at = a[s] + behind;
     if constexpr (std::is_same<T, float>::value) {
       // the next piece: the tile begins on a multiple of 32 bytes, so its place differs in a bit
-      return __builtin_bit_cast(f32x8, F4x2{lds_read<f32x4v>(a[s], off), lds_read<f32x4v>(a[s] ^ 16, off)});
+      return __builtin_bit_cast(f32x8, F4x2{lds_read<f32x4v>(at, off), lds_read<f32x4v>(at ^ 16, off)});
     } else {
-      return lds_read<bf16x8>(a[s], off);
+      return lds_read<bf16x8>(at, off);
     }
   }
 };
 
 // Operand values: channel 32 d + l % 32 of rows r0 + 8 (j / 4) + 4 h + j % 4, j < 8 (r0 a
 // multiple of 16). In bf16 by two transposing reads: 16 lanes read 4 rows x 16 channels and
-// each gets one channel of the 4 rows. The upper rows' swizzle differs by 2 pieces.
+// each gets one channel of the 4 rows. Rows r + 8 have row r's swizzle but for 2 pieces, a bit of
+// the address (tiles begin on multiples of 256 bytes).
 template <typename T, int DP>
 struct ColReader {
   using L = Tile<T, DP>;
-  uint32_t lo[DP / 32], hi[DP / 32];
+  uint32_t lo[DP / 32];
   __device__ __forceinline__ ColReader(const T *tile, int l) {
     const uint32_t base = (uint32_t)(uintptr_t)(mfma::lds_void_t *)tile;
 #pragma unroll
@@ -160,15 +164,11 @@ struct ColReader {
       const int r = 4 * (l >> 5) + (sizeof(T) == 2 ? (l & 15) >> 2 : 0);
       const int c = 32 * d + (sizeof(T) == 2 ? 16 * ((l >> 4) & 1) + 4 * (l & 3) : l & 31);
       lo[d] = base + (L::at(r, c / L::PE) + c % L::PE) * sizeof(T);
-      hi[d] = base + (L::at(r + 8, c / L::PE) + c % L::PE) * sizeof(T);
     }
   }
   __device__ __forceinline__ void move(int bytes) {
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d) {
-      lo[d] += bytes;
-      hi[d] += bytes;
-    }
+    for (int d = 0; d < DP / 32; ++d) lo[d] += bytes;
   }
   __device__ __forceinline__ Frag<T> read(int r0, int d) const {
     const int off = r0 * DP * (int)sizeof(T);
@@ -177,8 +177,8 @@ struct ColReader {
       f32x8 f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t at = j < 4 ? lo[d] : hi[d];
-        f.v[j] = lds_read<float>(at ^ (swizzle_step(j % 4)), off + (j % 4) * DP * 4);
+        const int upper = j < 4 ? 0 : 32;
+        f.v[j] = lds_read<float>(lo[d] ^ (swizzle_step(j % 4) | upper), off + (j % 4 + upper / 4) * DP * 4);
       }
       return f;
     } else {
@@ -186,7 +186,7 @@ struct ColReader {
       const mfma::v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (lds_v4 *)((__attribute__((address_space(3))) char *)(uintptr_t)lo[d] + off));
       const mfma::v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_v4 *)((__attribute__((address_space(3))) char *)(uintptr_t)hi[d] + off));
+          (lds_v4 *)((__attribute__((address_space(3))) char *)(uintptr_t)(lo[d] ^ 32) + off + 8 * DP * 2));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }

@@ -66,15 +66,68 @@ struct Work {
   int64_t tile;
   int head, kv;
 };
-__device__ __forceinline__ Work work_of(const AttnArgs &a, int64_t tiles) {
+__device__ __forceinline__ Work work_of(const AttnArgs &a, const int32_t *order, int64_t tiles) {
   const int64_t id = blk::block_id();
   const int group = a.hq / a.hk;
   Work w;
   w.kv = (int)(id % a.hk);
   const int64_t x = id / a.hk;
   w.head = w.kv * group + (int)(x % group);
-  w.tile = tiles - 1 - x / group;
+  const int64_t rank = x / group;
+  w.tile = rank >= tiles ? -1 : order ? order[rank] : tiles - 1 - rank;
   return w;
+}
+
+// ---- the order of tiles ----------------------------------------------------------------
+// Blocks start in the order of their numbers as others end, so the longest have to come
+// first. Within one sequence that is known; tiles of several are sorted by how much they
+// see, at most kOrderTiles of kOrderBatch sequences (more are so many that their order
+// matters little), and only if they do not all run at once.
+constexpr int kOrderTiles = 2048, kOrderBatch = 1024;
+inline bool ordered(int batch, int64_t tiles, int heads) {
+  return batch > 1 && batch <= kOrderBatch && tiles <= kOrderTiles && tiles * heads > 512;
+}
+
+// order[rank] = tile, by falling numbers of keys (of queries for tiles of keys) that its M
+// rows see (are seen by), those of empty tiles last.
+__global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int tiles, int32_t *order) {
+  __shared__ int mine[kOrderBatch + 1], other[kOrderBatch + 1], work[kOrderTiles];
+  const int32_t *off = keys ? a.k_off : a.q_off, *oth = keys ? a.q_off : a.k_off;
+  const int64_t n = keys ? a.n_k : a.n_q, no = keys ? a.n_q : a.n_k;
+  for (int i = threadIdx.x; i <= a.batch; i += 256) {
+    mine[i] = (int)offset_of(off, i, n);
+    other[i] = (int)offset_of(oth, i, no);
+  }
+  __syncthreads();
+  for (int t = threadIdx.x; t < tiles; t += 256) {
+    int s = 0;
+    for (int step = 1024; step; step >>= 1)
+      if (s + step <= a.batch && mine[s + step] / M + s + step <= t) s += step;
+    const int end = s < a.batch ? mine[s + 1] : (int)n, len = max(0, end - mine[s]);
+    const int r0 = (t - (mine[s] / M + s)) * M, r1 = min(r0 + M, len) - 1;
+    const int lo = s < a.batch ? max(0, other[s + 1] - other[s]) : 0;  // rows of the other side
+    int w = 0;
+    if (r0 < len) {
+      const int d = keys ? len - lo : lo - len;  // keys less queries
+      int from = 0, to = lo;
+      if (a.causal && keys) {
+        from = max(0, r0 - d);
+        if (a.window > 0) to = (int)min((int64_t)lo, (int64_t)r1 + a.window - d);
+      } else if (a.causal) {
+        to = min(lo, r1 + d + 1);
+        if (a.window > 0) from = max(0, r0 + d - a.window + 1);
+      }
+      w = 1 + max(0, to - from);
+    }
+    work[t] = w;
+  }
+  __syncthreads();
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= tiles) return;
+  const int w = work[t];
+  int rank = 0;
+  for (int u = 0; u < tiles; ++u) rank += work[u] > w || (work[u] == w && u < t);
+  order[rank] = t;
 }
 
 // Rows of the other side a step: two steps' tiles of two blocks fit a CU's LDS.
@@ -97,7 +150,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
   extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;  // two tiles of keys, two of values
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
-  const Work w = work_of(a, tiles);
+  const Work w = work_of(a, a.q_order, tiles);
   if (w.tile < 0) return;
   const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l));
   const Rows rq = rows_of(a.q_off, s, a.batch, a.n_q);
@@ -294,7 +347,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
   extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;  // [2][K tile, V tile]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
-  const Work w = work_of(a, tiles);
+  const Work w = work_of(a, a.q_order, tiles);
   if (w.tile < 0) return;
   const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l));
   const Rows rq = rows_of(a.q_off, s, a.batch, a.n_q);
@@ -395,10 +448,11 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
 //   scores S = Q K^T;   dP = dY V^T beside P = exp(S - lse);
 //   dV += dY^T P beside dS = P (dP - delta);   dK += Q^T dS.
 template <typename T, int DP, int NK>
-__global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(AttnArgs a, int64_t tiles) {
   using L = Tile<T, DP>;
-  constexpr int QS = step_rows<T>(), NT = QS / 32, STAGE = 2 * QS * DP * (int)sizeof(T);
+  constexpr int QS = 32, NT = QS / 32, STAGE = 2 * QS * DP * (int)sizeof(T);
   constexpr int KB = NK * kBlock, ND = DP / 32, S = L::STEPS;
+  constexpr int AHEAD = 3;  // operands read from LDS ahead of their products
   using C = Copier<T, DP, QS, kWaves>;
   extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;                            // [2][q tile, dy tile]
@@ -407,8 +461,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const int64_t id = blk::block_id();
   const int kv = (int)(id % a.hk);
-  const int64_t tile = id / a.hk;
-  if (tile >= tiles) return;
+  if (id / a.hk >= tiles) return;
+  const int64_t tile = a.k_order ? a.k_order[id / a.hk] : id / a.hk;
   const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.k_off, a.batch, a.n_k, KB, tile, l));
   const Rows rk = rows_of(a.k_off, s, a.batch, a.n_k);
   const Rows rq = s < a.batch ? rows_of(a.q_off, s, a.batch, a.n_q) : Rows{0, 0};
@@ -424,16 +478,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) 
     return (int)max((int64_t)0, min((int64_t)lq, (int64_t)j + a.window - off));
   };
   Frag<T> k[NK][S];
-  int my_from[NK];
-  unsigned queries[NK];
 #pragma unroll
   for (int j = 0; j < NK; ++j) {
     const int kj = k0 + 32 * j + (l & 31);
     const T *kp = (const T *)a.k.p + (rk.start + min(kj, lk - 1)) * a.k.tok_stride + kv * a.k.head_stride;
 #pragma unroll
     for (int i = 0; i < S; ++i) k[j][i] = with_sign<T>(load_frag<T>(kp, i, h, a.dh), a.scale);
-    my_from[j] = from(kj);
-    queries[j] = kj < lk ? max(0, to(kj) - my_from[j]) : 0;
   }
   const int q_from = from(first), q_to = to(min(first + KB, lk) - 1);
   const int all_from = from(k0 + kRows * NK - 1), all_to = k0 + kRows * NK <= lk ? to(k0) : 0;
@@ -446,18 +496,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) 
   const Copier<T, DP, KB, kWaves> vc((const T *)a.v.p + rk.start * a.v.tok_stride + kv * a.v.head_stride,
                                      a.v.tok_stride, a.dh, wave, l);
   vc.issue(vt, first, lk, a.dh, wave, l, kAsIs);
-  const RowReader<T, DP> vr(vt + kRows * NK * wave * DP, l);
   const auto issue = [&](int g, int i0, int b, int fix) __attribute__((always_inline)) {
-    const int hd = kv * group + g;
+    const int hd = kv * group + g, ln = here(l);  // no registers for the copies' offsets
     T *const t = buf + b * 2 * QS * DP;
-    const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + hd * a.q.head_stride, a.q.tok_stride, a.dh, wave, l);
+    const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + hd * a.q.head_stride, a.q.tok_stride, a.dh, wave, ln);
     const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride, a.dh, wave,
-               l);
-    qc.issue(t, i0, lq, a.dh, wave, l, fix);
-    yc.issue(t + QS * DP, i0, lq, a.dh, wave, l, fix);
+               ln);
+    qc.issue(t, i0, lq, a.dh, wave, ln, fix);
+    yc.issue(t + QS * DP, i0, lq, a.dh, wave, ln, fix);
     if (wave < 2) {
       const float *src = (wave ? a.delta : a.lse2) + hd * a.n_q + rq.start;
-      copy_to_lds<4>(uniform(src), 4 * (uint32_t)min(i0 + l, lq - 1), stats + (2 * b + wave) * 64);
+      copy_to_lds<4>(uniform(src), 4 * (uint32_t)min(i0 + ln, lq - 1), stats + (2 * b + wave) * 64);
     }
   };
   f32x16 dk[NK][ND], dv[NK][ND];
@@ -469,18 +518,33 @@ __global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) 
     int cur = 0;
     RowReader<T, DP> rows(buf, l);
     ColReader<T, DP> cols(buf, l);
-    if (steps > 0) issue(0, begin, 0, fix);
-    // step n of head g: queries from begin + n QS
+    // Step n of head g, from the last queries to the first: the blocks of a key head that
+    // run at once then read the same queries at about the same time, from L2.
+    const auto queries_of = [&](int n) { return begin + (steps - 1 - n) * QS; };
+    if (steps > 0) issue(0, queries_of(0), 0, fix);
     for (int g = 0, n = 0; g < group && steps > 0;) {
       mfma::wait_vm<0>();
       mfma::lds_barrier();
       const float *const lse = stats + 2 * cur * 64 + 4 * h, *const delta = lse + 64;
+      // from this step's tiles to the wave's V rows
+      const int to_v = (2 - cur) * STAGE + kRows * NK * wave * DP * (int)sizeof(T);
       cur ^= 1;
-      const int i0 = begin + n * QS;
+      const int i0 = queries_of(n);
       if (++n == steps) n = 0, ++g;
-      if (g < group) issue(g, begin + n * QS, cur, fix);
+      if (g < group) issue(g, queries_of(n), cur, fix);
       const bool whole = i0 >= all_from && i0 + QS <= all_to;
-      const auto seen = [&](int j, int r) { return (unsigned)(i0 + 4 * h - my_from[j] + r) < queries[j]; };
+      // f(e, whether the lane's key of tile j is seen by the query of result e), for e < 16 NK
+      const auto each_seen = [&](int t, auto f) __attribute__((always_inline)) {
+        const int ln = here(l);
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          const int kj = k0 + 32 * j + (ln & 31), first = from(kj);
+          const unsigned queries = kj < lk ? max(0, to(kj) - first) : 0;
+          const int rel = i0 + 32 * t + 4 * (ln >> 5) - first;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f(16 * j + i, (unsigned)(rel + 8 * (i / 4) + i % 4) < queries);
+        }
+      };
       // the operands of the products in their order: S steps of S and dP, 2 ND of dV and dK
       constexpr int LEN = 2 * S + 4 * ND;
       const auto operand = [&](int m) __attribute__((always_inline)) {
@@ -490,69 +554,57 @@ __global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) 
         const int e = (o - 2 * S) % (2 * ND), q = (o - 2 * S) / (2 * ND);
         return cols.read((q ? 0 : QS) + r + 16 * (e / ND), e % ND);
       };
-      Frag<T> f[kAhead], vb[2][NK];
+      Frag<T> f[AHEAD], vb[NK];
 #pragma unroll
-      for (int m = 0; m < kAhead; ++m) f[m] = operand(m);
+      for (int m = 0; m < AHEAD; ++m) f[m] = operand(m);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int m0 = t * LEN;
         // the next operand, in the place of the one just used
         const auto refill = [&](int m) __attribute__((always_inline)) {
-          if (m + kAhead < NT * LEN) f[m % kAhead] = operand(m + kAhead);
+          if (m + AHEAD < NT * LEN) f[m % AHEAD] = operand(m + AHEAD);
           __builtin_amdgcn_sched_barrier(0);
         };
         f32x16 x[NK], y[NK];
-        float st[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 e = *(const float4 *)(lse + 32 * t + 8 * i);
-          st[4 * i] = e.x, st[4 * i + 1] = e.y, st[4 * i + 2] = e.z, st[4 * i + 3] = e.w;
-        }
+        f32x4v st;
+        // a statistic of the rows of results e .. e + 3
+        const auto stat = [&](const float *p, int e) __attribute__((always_inline)) {
+          return *(const f32x4v *)(p + 32 * t + 2 * (e % 16));
+        };
 #pragma unroll
         for (int j = 0; j < NK; ++j) x[j] = y[j] = f32x16{};
 #pragma unroll
-        for (int j = 0; j < NK; ++j) vb[0][j] = vr.read(32 * j, 0);
+        for (int j = 0; j < NK; ++j) vb[j] = rows.read_from(to_v, 32 * j, 0);
 #pragma unroll
         for (int o = 0; o < S; ++o) {
 #pragma unroll
-          for (int j = 0; j < NK; ++j) x[j] = mma(f[(m0 + o) % kAhead], k[j][o], x[j]);
+          for (int j = 0; j < NK; ++j) x[j] = mma(f[(m0 + o) % AHEAD], k[j][o], x[j]);
           refill(m0 + o);
         }
         constexpr int PB = 16 * NK / S, PC = 16 * NK / (2 * ND);
 #pragma unroll
         for (int o = 0; o < S; ++o) {
 #pragma unroll
-          for (int j = 0; j < NK; ++j) y[j] = mma(f[(m0 + S + o) % kAhead], vb[o % 2][j], y[j]);
+          for (int j = 0; j < NK; ++j) y[j] = mma(f[(m0 + S + o) % AHEAD], vb[j], y[j]);
           if (o + 1 < S) {
 #pragma unroll
-            for (int j = 0; j < NK; ++j) vb[(o + 1) % 2][j] = vr.read(32 * j, o + 1);
+            for (int j = 0; j < NK; ++j) vb[j] = rows.read_from(to_v, 32 * j, o + 1);
           }
 #pragma unroll
           for (int e = PB * o; e < PB * (o + 1); ++e) {
-            float p = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -st[e % 16]));
+            if (e % 4 == 0) st = stat(lse, e);
+            float p = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -st[e % 4]));
             asm volatile("" : "+v"(p));  // here, not behind the products
             x[e / 16][e % 16] = p;
           }
           refill(m0 + S + o);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 e = *(const float4 *)(delta + 32 * t + 8 * i);
-          st[4 * i] = e.x, st[4 * i + 1] = e.y, st[4 * i + 2] = e.z, st[4 * i + 3] = e.w;
-        }
-        if (!whole) {
-#pragma unroll
-          for (int j = 0; j < NK; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!seen(j, 32 * t + 8 * (i / 4) + i % 4)) x[j][i] = 0.f;
-        }
-        if (fix == kCount) {
-#pragma unroll
-          for (int j = 0; j < NK; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[j][i] = seen(j, 32 * t + 8 * (i / 4) + i % 4) ? 1.f : 0.f;
-        }
+        if (!whole)
+          each_seen(t, [&](int e, bool ok) __attribute__((always_inline)) {
+            if (!ok) x[e / 16][e % 16] = 0.f;
+          });
+        if (fix == kCount)
+          each_seen(t, [&](int e, bool ok) __attribute__((always_inline)) { x[e / 16][e % 16] = ok ? 1.f : 0.f; });
         Frag<T> w[NK][2];
 #pragma unroll
         for (int j = 0; j < NK; ++j)
@@ -561,22 +613,20 @@ __global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) 
 #pragma unroll
         for (int o = 0; o < 2 * ND; ++o) {
 #pragma unroll
-          for (int j = 0; j < NK; ++j) dv[j][o % ND] = mma(f[(m0 + 2 * S + o) % kAhead], w[j][o / ND], dv[j][o % ND]);
+          for (int j = 0; j < NK; ++j) dv[j][o % ND] = mma(f[(m0 + 2 * S + o) % AHEAD], w[j][o / ND], dv[j][o % ND]);
 #pragma unroll
           for (int e = PC * o; e < PC * (o + 1); ++e) {
-            float ds = x[e / 16][e % 16] * (y[e / 16][e % 16] - st[e % 16]);
+            if (e % 4 == 0) st = stat(delta, e);
+            float ds = x[e / 16][e % 16] * (y[e / 16][e % 16] - st[e % 4]);
             asm volatile("" : "+v"(ds));
             y[e / 16][e % 16] = ds;
           }
           refill(m0 + 2 * S + o);
         }
-        if (!whole) {
-#pragma unroll
-          for (int j = 0; j < NK; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!seen(j, 32 * t + 8 * (i / 4) + i % 4)) y[j][i] = 0.f;
-        }
+        if (!whole)
+          each_seen(t, [&](int e, bool ok) __attribute__((always_inline)) {
+            if (!ok) y[e / 16][e % 16] = 0.f;
+          });
 #pragma unroll
         for (int j = 0; j < NK; ++j)
 #pragma unroll
@@ -585,7 +635,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_dkv(AttnArgs a, int64_t tiles) 
         for (int o = 0; o < 2 * ND; ++o) {
 #pragma unroll
           for (int j = 0; j < NK; ++j)
-            dk[j][o % ND] = mma(f[(m0 + 2 * S + 2 * ND + o) % kAhead], w[j][o / ND], dk[j][o % ND]);
+            dk[j][o % ND] = mma(f[(m0 + 2 * S + 2 * ND + o) % AHEAD], w[j][o / ND], dk[j][o % ND]);
           refill(m0 + 2 * S + 2 * ND + o);
         }
       }
@@ -615,14 +665,36 @@ void by_width(int dh, F f) {
   if (dh <= 64) f(std::integral_constant<int, 64>()); else f(std::integral_constant<int, 128>());
 }
 
+// Rows of a tile of keys.
+template <typename T>
+constexpr int key_rows() { return kBlock; }
+
+// Fills the order of tiles of M rows, or says that it is not used.
+int32_t *order_tiles(const AttnArgs &a, bool keys, int M, int32_t *order, hipStream_t st) {
+  const int64_t tiles = tiles_of(keys ? a.n_k : a.n_q, M, a.batch);
+  if (!ordered(a.batch, tiles, keys ? a.hk : a.hq)) return nullptr;
+  k_order<<<(int)(tiles + 255) / 256, 256, 0, st>>>(a, keys, M, (int)tiles, order);
+  return order;
+}
+
 }  // namespace
 
 bool attn_size_ok(int hq, int batch, int64_t n) {
   return tiles_of(n, kBlock, batch) * hq < ((int64_t)1 << 31);
 }
+size_t attn_q_order(const ipttt_attention &d) {
+  const int64_t tiles = tiles_of(d.n_q, kBlock, d.batch);
+  return ordered(d.batch, tiles, d.q_heads) ? round_up(tiles * 4, 256) : 256;
+}
+size_t attn_k_order(const ipttt_attention &d) {
+  const int64_t tiles = tiles_of(d.n_k, kBlock, d.batch);  // of the smallest tiles
+  return round_up((tiles < kOrderTiles ? tiles : kOrderTiles) * 4, 256);
+}
 
 template <typename T>
-hipError_t attn_forward(const AttnArgs &a, hipStream_t st) {
+hipError_t attn_forward(const AttnArgs &args, hipStream_t st) {
+  AttnArgs a = args;
+  a.q_order = order_tiles(a, false, kBlock, a.q_order, st);
   by_width<T>(a.dh, [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
     const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);
@@ -633,20 +705,19 @@ hipError_t attn_forward(const AttnArgs &a, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t attn_backward(const AttnArgs &a, hipStream_t st) {
+hipError_t attn_backward(const AttnArgs &args, hipStream_t st) {
+  AttnArgs a = args;
+  a.q_order = order_tiles(a, false, kBlock, a.q_order, st);
+  a.k_order = order_tiles(a, true, key_rows<T>(), a.k_order, st);
   if (a.n_q > 0) k_delta<T><<<blk::grid_of((a.n_q * a.hq + 15) / 16), 256, 0, st>>>(a);
   by_width<T>(a.dh, [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
     const size_t lds = 4 * step_rows<T>() * DP * sizeof(T);
     if (a.n_k > 0) {
-      const auto go = [&](auto nk) {
-        constexpr int NK = decltype(nk)::value;
-        const int64_t tiles = tiles_of(a.n_k, NK * kBlock, a.batch);
-        const size_t bytes = lds + NK * kBlock * DP * sizeof(T) + 4 * 64 * sizeof(float);
-        k_dkv<T, DP, NK><<<blk::grid_of(tiles * a.hk), kThreads, bytes, st>>>(a, tiles);
-      };
-      if constexpr (sizeof(T) == 2) go(std::integral_constant<int, 2>());
-      else go(std::integral_constant<int, 1>());
+      constexpr int KB = key_rows<T>();
+      const int64_t tiles = tiles_of(a.n_k, KB, a.batch);
+      k_dkv<T, DP, KB / kBlock><<<blk::grid_of(tiles * a.hk), kThreads,
+                                  (4 * 32 + KB) * DP * sizeof(T) + 4 * 64 * sizeof(float), st>>>(a, tiles);
     }
     if (a.n_q > 0) {
       const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);

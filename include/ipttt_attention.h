@@ -135,10 +135,13 @@ typedef struct {
   const int32_t *q_offsets, *k_offsets;  /* [batch + 1], device memory, or NULL */
 } ipttt_attention;
 
-/* o: heads of n_q rows. lse: [q_heads][n_q] fp32, or NULL. */
+/* o: heads of n_q rows. lse: [q_heads][n_q] fp32, or NULL. The workspace must be 256-byte
+ * aligned; pointers of desc are not read for its size. */
+size_t ipttt_attention_forward_workspace_bytes(const ipttt_attention *desc);
 ipttt_status ipttt_attention_forward(const ipttt_attention *desc, const ipttt_heads *q,
                                      const ipttt_heads *k, const ipttt_heads *v,
-                                     const ipttt_heads *o, float *lse, void *hip_stream);
+                                     const ipttt_heads *o, float *lse, void *workspace,
+                                     size_t workspace_bytes, void *hip_stream);
 
 /* Gradients from dy = dL/do, with p_j = exp(a_j - lse):
  *   dv_j = sum p_j dy, dp_j = dy.v_j, ds_j = p_j (dp_j - sum(dy o)),

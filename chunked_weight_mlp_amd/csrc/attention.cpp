@@ -369,7 +369,7 @@ ipttt_status ipttt_attention_forward(const ipttt_attention *desc, const ipttt_he
 
 size_t ipttt_attention_backward_workspace_bytes(const ipttt_attention *desc) {
   if (check_attn_sizes(desc) != IPTTT_OK) return 0;
-  return attn_q_order(*desc) + attn_k_order(*desc) +
+  return attn_q_order(*desc) + attn_k_order(*desc) + attn_parts(*desc) +
          (size_t)round_up((int64_t)desc->q_heads * desc->n_q * 8, 256);
 }
 
@@ -394,7 +394,8 @@ ipttt_status ipttt_attention_backward(const ipttt_attention *desc, const ipttt_h
   a.dv = view(dv, a.n_k, a.hk);
   a.q_order = (int32_t *)workspace;
   a.k_order = (int32_t *)((char *)workspace + attn_q_order(*desc));
-  a.delta = (float *)((char *)a.k_order + attn_k_order(*desc));
+  a.part = (float *)((char *)a.k_order + attn_k_order(*desc));
+  a.delta = (float *)((char *)a.part + attn_parts(*desc));
   a.lse2 = a.delta + a.hq * a.n_q;
   const hipStream_t st = (hipStream_t)hip_stream;
   return launched(

@@ -50,10 +50,12 @@ struct AttnArgs {
   ipttt_heads dy, dq, dk, dv;  // backward
   float *delta, *lse2;     // backward: [hq][n_q], sum(dy o) and lse in units of log2
   int32_t *q_order, *k_order;  // workspace for the order of the tiles of queries, of keys
+  float *part;             // and for partial dk and dv
 };
-// Bytes of those orders.
+// Bytes of those.
 size_t attn_q_order(const ipttt_attention &d);
 size_t attn_k_order(const ipttt_attention &d);
+size_t attn_parts(const ipttt_attention &d);
 // Whether the tiles of such a call can be counted in 31 bits.
 bool attn_size_ok(int hq, int batch, int64_t n);
 template <typename T>

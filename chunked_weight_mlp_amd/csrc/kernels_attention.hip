@@ -398,36 +398,93 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
         vc.issue(next + KS * DP, k0 + KS, lk, a.dh, wave, l, kAsIs);
       }
       const bool whole = k0 + KS <= wf.hi && k0 >= wl.lo;
-      const int from = k0 + 4 * h - mine.lo;
-      const unsigned keys = max(0, mine.hi - mine.lo);
-      const auto sees = [&](int j) { return (unsigned)(from + j) < keys; };
+      const auto each_seen = [&](int t, auto f) __attribute__((always_inline)) {
+        const int rel = k0 + 32 * t + 4 * h - mine.lo;
+        const unsigned keys = max(0, mine.hi - mine.lo);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f(i, (unsigned)(rel + 8 * (i / 4) + i % 4) < keys);
+      };
+      // For each 32 keys S and dP, then the sums for all of them; what the vector units do
+      // goes beside the products that do not wait for it:
+      //   S(t) beside dS(t - 1), dP(t) beside P(t), the first sums beside the last dS.
+      constexpr int S = L::STEPS, ND = DP / 32, LEN = NT * (2 * S + 2 * ND);
+      const auto operand = [&](int m) __attribute__((always_inline)) {
+        if (m >= 2 * S * NT) {
+          const int e = m - 2 * S * NT;
+          return cols.read(16 * (e / ND), e % ND);
+        }
+        const int t = m / (2 * S), o = m % (2 * S);
+        return rows.read((o < S ? 0 : KS) + 32 * t, o % S);
+      };
+      Frag<T> f[kAhead];
+#pragma unroll
+      for (int m = 0; m < kAhead; ++m) f[m] = operand(m);
+      const auto refill = [&](int m) __attribute__((always_inline)) {
+        if (m + kAhead < LEN) f[m % kAhead] = operand(m + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      f32x16 x[NT], y[NT];
+      Frag<T> ds[NT][2];
+      // elements e0 .. e1 - 1 of dS(t), in x
+      const auto grad = [&](int t, int e0, int e1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = e0; e < e1; ++e) {
+          float v = x[t][e] * (y[t][e] - delta);
+          asm volatile("" : "+v"(v));  // here, not behind the products
+          x[t][e] = v;
+        }
+      };
+      const auto finish = [&](int t) __attribute__((always_inline)) {
+        if (!whole)
+          each_seen(t, [&](int i, bool ok) __attribute__((always_inline)) {
+            if (!ok) x[t][i] = 0.f;
+          });
+        if (fix == kCount)
+          each_seen(t, [&](int i, bool ok) __attribute__((always_inline)) { x[t][i] = ok ? 1.f : 0.f; });
+        ds[t][0] = as_operand<T>(x[t], 0);
+        ds[t][1] = as_operand<T>(x[t], 1);
+      };
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        f32x16 x{}, dp{};
+        x[t] = y[t] = f32x16{};
 #pragma unroll
-        for (int i = 0; i < L::STEPS; ++i) {
-          x = mma(rows.read(32 * t, i), q[i], x);
-          dp = mma(rows.read(KS + 32 * t, i), dy[i], dp);
+        for (int o = 0; o < S; ++o) {
+          const int m = 2 * S * t + o;
+          x[t] = mma(f[m % kAhead], q[o], x[t]);
+          if (t > 0) grad(t - 1, 16 / S * o, 16 / S * (o + 1));
+          refill(m);
         }
+        if (t > 0) finish(t - 1);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = exp2_(__builtin_fmaf(x[i], c, -lse)) * (dp[i] - delta);
-        if (!whole) {
+        for (int o = 0; o < S; ++o) {
+          const int m = 2 * S * t + S + o;
+          y[t] = mma(f[m % kAhead], dy[o], y[t]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!sees(32 * t + 8 * (i / 4) + i % 4)) x[i] = 0.f;
-        }
-        if (fix == kCount) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = sees(32 * t + 8 * (i / 4) + i % 4) ? 1.f : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Frag<T> ds = as_operand<T>(x, i);
-#pragma unroll
-          for (int d = 0; d < DP / 32; ++d)
-            acc[d] = mma(cols.read(32 * t + 16 * i, d), ds, acc[d]);
+          for (int e = 16 / S * o; e < 16 / S * (o + 1); ++e) {
+            float v = exp2_(__builtin_fmaf(x[t][e], c, -lse));
+            asm volatile("" : "+v"(v));
+            x[t][e] = v;
+          }
+          refill(m);
         }
       }
+      if constexpr (NT == 1) {
+        grad(0, 0, 16);
+        finish(0);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int o = 0; o < 2 * ND; ++o) {
+          const int m = 2 * S * NT + 2 * ND * t + o;
+          acc[o % ND] = mma(f[m % kAhead], ds[t][o / ND], acc[o % ND]);
+          if (NT > 1 && t == 0) {
+            constexpr int PER = 16 / (2 * ND);
+            grad(NT - 1, PER * o, PER * (o + 1));
+          }
+          refill(m);
+          if (NT > 1 && t == 0 && o == 2 * ND - 1) finish(NT - 1);
+        }
       rows.move(cur ? STAGE : -STAGE);
       cols.move(cur ? STAGE : -STAGE);
     }
@@ -447,8 +504,10 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
 // For 32 queries the products are, with what the vector units do beside them,
 //   scores S = Q K^T;   dP = dY V^T beside P = exp(S - lse);
 //   dV += dY^T P beside dS = P (dP - delta);   dK += Q^T dS.
+// Where the key tiles are few, `parts` blocks share a tile's steps (part blockIdx.z) and
+// leave partial sums, which k_dkv_join adds up.
 template <typename T, int DP, int NK>
-__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(AttnArgs a, int64_t tiles, int parts) {
   using L = Tile<T, DP>;
   constexpr int QS = 32, NT = QS / 32, STAGE = 2 * QS * DP * (int)sizeof(T);
   constexpr int KB = NK * kBlock, ND = DP / 32, S = L::STEPS;
@@ -521,8 +580,12 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
     // Step n of head g, from the last queries to the first: the blocks of a key head that
     // run at once then read the same queries at about the same time, from L2.
     const auto queries_of = [&](int n) { return begin + (steps - 1 - n) * QS; };
-    if (steps > 0) issue(0, queries_of(0), 0, fix);
-    for (int g = 0, n = 0; g < group && steps > 0;) {
+    const int64_t all = (int64_t)group * steps;
+    const int64_t stop = all * (blockIdx.z + 1) / parts;
+    int64_t at = all * blockIdx.z / parts;
+    int g = steps ? (int)(at / steps) : 0, n = steps ? (int)(at - (int64_t)g * steps) : 0;
+    if (at < stop) issue(g, queries_of(n), 0, fix);
+    for (; at < stop; ++at) {
       mfma::wait_vm<0>();
       mfma::lds_barrier();
       const float *const lse = stats + 2 * cur * 64 + 4 * h, *const delta = lse + 64;
@@ -531,7 +594,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
       cur ^= 1;
       const int i0 = queries_of(n);
       if (++n == steps) n = 0, ++g;
-      if (g < group) issue(g, queries_of(n), cur, fix);
+      if (at + 1 < stop) issue(g, queries_of(n), cur, fix);
       const bool whole = i0 >= all_from && i0 + QS <= all_to;
       // f(e, whether the lane's key of tile j is seen by the query of result e), for e < 16 NK
       const auto each_seen = [&](int t, auto f) __attribute__((always_inline)) {
@@ -651,6 +714,12 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
       const int kj = k0 + 32 * j + here(l & 31);
       if (kj < lk) {
         const int64_t kr = rk.start + kj;
+        if (parts > 1) {
+          float *const pk = a.part + ((((int64_t)blockIdx.z * a.n_k + kr) * a.hk + kv) * 2) * a.dh;
+          store_row<float, DP>(pk, dk[j], a.scale, h, a.dh, kAsIs);
+          store_row<float, DP>(pk + a.dh, dv[j], 1.f, h, a.dh, fix);
+          continue;
+        }
         store_row<T, DP>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk[j], a.scale, h, a.dh, kAsIs);
         store_row<T, DP>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv[j], 1.f, h, a.dh, fix);
       }
@@ -658,6 +727,19 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
     if (fix != kCount) break;
     __syncthreads();
   }
+}
+
+// dk and dv from the parts' sums [parts][n_k][hk][dk, dv][dh], in their order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dkv_join(AttnArgs a, int parts) {
+  const int64_t i = blk::block_id() * 256 + threadIdx.x, size = a.n_k * a.hk * 2 * a.dh;
+  if (i >= size) return;
+  float v = 0.f;
+  for (int p = 0; p < parts; ++p) v += a.part[p * size + i];
+  const int64_t row = i / a.dh, kr = row / (2 * a.hk);
+  const int c = (int)(i - row * a.dh), x = (int)(row - kr * 2 * a.hk);
+  const ipttt_heads &out = x % 2 ? a.dv : a.dk;
+  ((T *)out.p)[kr * out.tok_stride + x / 2 * out.head_stride + c] = (T)v;
 }
 
 template <typename T, class F>
@@ -668,6 +750,16 @@ void by_width(int dh, F f) {
 // Rows of a tile of keys.
 template <typename T>
 constexpr int key_rows() { return kBlock; }
+
+// Blocks that share a tile of keys: as many as bring the grid to two blocks a CU, while each
+// has four steps of 32 queries of one head or more.
+int parts_of(int hq, int hk, int64_t n_q, int64_t n_k, int batch) {
+  const int64_t blocks = tiles_of(n_k, kBlock, batch) * hk;
+  if (blocks >= 384 || n_k == 0) return 1;
+  const int64_t most = (int64_t)(hq / hk) * (n_q / 32) / 4;
+  const int64_t p = 512 / blocks;
+  return (int)(p < most ? (p < 1 ? 1 : p) : most < 1 ? 1 : most);
+}
 
 // Fills the order of tiles of M rows, or says that it is not used.
 int32_t *order_tiles(const AttnArgs &a, bool keys, int M, int32_t *order, hipStream_t st) {
@@ -686,8 +778,12 @@ size_t attn_q_order(const ipttt_attention &d) {
   const int64_t tiles = tiles_of(d.n_q, kBlock, d.batch);
   return ordered(d.batch, tiles, d.q_heads) ? round_up(tiles * 4, 256) : 256;
 }
+size_t attn_parts(const ipttt_attention &d) {
+  const int parts = parts_of(d.q_heads, d.k_heads, d.n_q, d.n_k, d.batch);
+  return parts > 1 ? round_up(parts * d.n_k * d.k_heads * 2 * d.head_dim * 4, 256) : 0;
+}
 size_t attn_k_order(const ipttt_attention &d) {
-  const int64_t tiles = tiles_of(d.n_k, kBlock, d.batch);  // of the smallest tiles
+  const int64_t tiles = tiles_of(d.n_k, kBlock, d.batch);
   return round_up((tiles < kOrderTiles ? tiles : kOrderTiles) * 4, 256);
 }
 
@@ -709,6 +805,7 @@ hipError_t attn_backward(const AttnArgs &args, hipStream_t st) {
   AttnArgs a = args;
   a.q_order = order_tiles(a, false, kBlock, a.q_order, st);
   a.k_order = order_tiles(a, true, key_rows<T>(), a.k_order, st);
+  const int parts = parts_of(a.hq, a.hk, a.n_q, a.n_k, a.batch);
   if (a.n_q > 0) k_delta<T><<<blk::grid_of((a.n_q * a.hq + 15) / 16), 256, 0, st>>>(a);
   by_width<T>(a.dh, [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
@@ -716,8 +813,11 @@ hipError_t attn_backward(const AttnArgs &args, hipStream_t st) {
     if (a.n_k > 0) {
       constexpr int KB = key_rows<T>();
       const int64_t tiles = tiles_of(a.n_k, KB, a.batch);
-      k_dkv<T, DP, KB / kBlock><<<blk::grid_of(tiles * a.hk), kThreads,
-                                  (4 * 32 + KB) * DP * sizeof(T) + 4 * 64 * sizeof(float), st>>>(a, tiles);
+      dim3 grid = blk::grid_of(tiles * a.hk);
+      grid.z = parts;
+      k_dkv<T, DP, KB / kBlock><<<grid, kThreads, (4 * 32 + KB) * DP * sizeof(T) + 4 * 64 * sizeof(float), st>>>(
+          a, tiles, parts);
+      if (parts > 1) k_dkv_join<T><<<blk::grid_of((a.n_k * a.hk * 2 * a.dh + 255) / 256), 256, 0, st>>>(a, parts);
     }
     if (a.n_q > 0) {
       const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);

@@ -27,6 +27,10 @@ using mfma::f32x16;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// The running maximum may fall behind by this much (in log2): weights are then up to 2^8,
+// which costs neither bf16 nor fp32 precision, and the sums are seldom rescaled.
+constexpr float kSlack = 8.f;
+
 struct f32x8 {
   float v[8];
 };
@@ -359,6 +363,37 @@ template <typename T>
 __device__ __forceinline__ void clear(T *tiles, int elems, int tid, int threads) {
   for (int i = tid; i < elems * (int)sizeof(T) / 16; i += threads)
     ((uint4 *)tiles)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// A lane's results x scale to its row of dh channels in memory. kCount leaves NaN there where
+// something was counted and zero elsewhere, and kFinite adds to that.
+template <typename T, int DP>
+__device__ __forceinline__ void store_row(T *row, const f32x16 (&x)[DP / 32], float scale, int half,
+                                          int width, int fix) {
+  const int h = here(half), dh = here(width);
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = 32 * d + 8 * g + 4 * h;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = x[d][4 * g + e] * scale;
+      if (fix != kAsIs) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (fix == kCount) v[e] = x[d][4 * g + e] != 0.f ? NAN : 0.f;
+          else if (c + e < dh) v[e] += (float)row[c + e];
+        }
+      }
+      if (c + 4 <= dh) {
+        blk::store_pack<T, 4>(row + c, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < dh) row[c + e] = (T)v[e];
+      }
+    }
 }
 
 // ---- the sequences of a packed batch -------------------------------------------------

@@ -29,37 +29,6 @@ __device__ __forceinline__ bool all_finite(const f32x16 (&x)[N]) {
   return z == 0.f;
 }
 
-// A lane's results x scale to its row of dh channels in memory. kCount leaves NaN there where
-// something was counted and zero elsewhere, and kFinite adds to that.
-template <typename T, int DP>
-__device__ __forceinline__ void store_row(T *row, const f32x16 (&x)[DP / 32], float scale, int half,
-                                          int width, int fix) {
-  const int h = here(half), dh = here(width);
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int c = 32 * d + 8 * g + 4 * h;
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = x[d][4 * g + e] * scale;
-      if (fix != kAsIs) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (fix == kCount) v[e] = x[d][4 * g + e] != 0.f ? NAN : 0.f;
-          else if (c + e < dh) v[e] += (float)row[c + e];
-        }
-      }
-      if (c + 4 <= dh) {
-        blk::store_pack<T, 4>(row + c, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < dh) row[c + e] = (T)v[e];
-      }
-    }
-}
-
 // Block of a (tile, head): heads of one key head on one XCD (consecutive blocks go to the
 // 8 XCDs in turn), tiles from the last, whose queries see the most keys, to the first.
 struct Work {
@@ -137,9 +106,6 @@ constexpr int step_rows() { return sizeof(T) == 2 ? 64 : 32; }
 // channels take twice the registers, and their products eight times as long.
 template <typename T, int DP>
 constexpr int blocks_a_cu() { return sizeof(T) == 4 && DP > 64 ? 1 : 2; }
-// The running maximum may fall behind by this much (in log2): weights are then up to 2^8,
-// which costs neither bf16 nor fp32 precision, and the sums are seldom rescaled.
-constexpr float kSlack = 8.f;
 constexpr int kAhead = 4;  // operands read from LDS ahead of their products
 
 template <typename T, int DP>

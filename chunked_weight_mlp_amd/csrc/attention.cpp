@@ -360,7 +360,7 @@ ipttt_status ipttt_attention_forward(const ipttt_attention *desc, const ipttt_he
   if (desc->n_q == 0) return IPTTT_OK;
   TRY(check_workspace(workspace, workspace_bytes, attn_q_order(*desc)));
   AttnArgs a = attn_args(desc, q, k, v, o, lse);
-  a.q_order = (int32_t *)workspace;
+  a.q_order = (TilePlace *)workspace;
   const hipStream_t st = (hipStream_t)hip_stream;
   return launched(
       desc->dtype == IPTTT_BF16 ? attn_forward<__bf16>(a, st) : attn_forward<float>(a, st),
@@ -392,8 +392,8 @@ ipttt_status ipttt_attention_backward(const ipttt_attention *desc, const ipttt_h
   a.dq = view(dq, a.n_q, a.hq);
   a.dk = view(dk, a.n_k, a.hk);
   a.dv = view(dv, a.n_k, a.hk);
-  a.q_order = (int32_t *)workspace;
-  a.k_order = (int32_t *)((char *)workspace + attn_q_order(*desc));
+  a.q_order = (TilePlace *)workspace;
+  a.k_order = (TilePlace *)((char *)workspace + attn_q_order(*desc));
   a.part = (float *)((char *)a.k_order + attn_k_order(*desc));
   a.delta = (float *)((char *)a.part + attn_parts(*desc));
   a.lse2 = a.delta + a.hq * a.n_q;

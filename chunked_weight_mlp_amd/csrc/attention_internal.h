@@ -39,6 +39,11 @@ template <typename T>
 hipError_t heads_backward(const HeadArgs &a, hipStream_t st);
 
 // ---- attention over packed prompts (kernels_attention.hip) --------------------------
+// A tile of one sequence's rows: the first of them in the sequence, and where its queries
+// and keys are.
+struct TilePlace {
+  int32_t first, q_start, lq, k_start, lk, pad[3];
+};
 struct AttnArgs {
   int hq, hk, dh, batch;
   int causal, window;
@@ -49,7 +54,7 @@ struct AttnArgs {
   float *lse;              // [hq][n_q]; or null in the forward
   ipttt_heads dy, dq, dk, dv;  // backward
   float *delta, *lse2;     // backward: [hq][n_q], sum(dy o) and lse in units of log2
-  int32_t *q_order, *k_order;  // workspace for the order of the tiles of queries, of keys
+  TilePlace *q_order, *k_order;  // workspace for the order of the tiles of queries, of keys
   float *part;             // and for partial dk and dv
 };
 // Bytes of those.

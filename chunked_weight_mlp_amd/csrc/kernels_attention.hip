@@ -32,19 +32,30 @@ __device__ __forceinline__ bool all_finite(const f32x16 (&x)[N]) {
 // Block of a (tile, head): heads of one key head on one XCD (consecutive blocks go to the
 // 8 XCDs in turn), tiles from the last, whose queries see the most keys, to the first.
 struct Work {
-  int64_t tile;
+  int64_t rank;  // the tile's place in the order
   int head, kv;
 };
-__device__ __forceinline__ Work work_of(const AttnArgs &a, const int32_t *order, int64_t tiles) {
+__device__ __forceinline__ Work work_of(const AttnArgs &a) {
   const int64_t id = blk::block_id();
   const int group = a.hq / a.hk;
   Work w;
   w.kv = (int)(id % a.hk);
   const int64_t x = id / a.hk;
   w.head = w.kv * group + (int)(x % group);
-  const int64_t rank = x / group;
-  w.tile = rank >= tiles ? -1 : order ? order[rank] : tiles - 1 - rank;
+  w.rank = x / group;
   return w;
+}
+// Tile number `tile` of M queries (keys); first is behind the sequence's end where the tile
+// is empty.
+__device__ __forceinline__ TilePlace tile_place(const AttnArgs &a, bool keys, int M, int64_t tile, int lane) {
+  const int32_t *off = keys ? a.k_off : a.q_off;
+  const int64_t n = keys ? a.n_k : a.n_q;
+  const int s = __builtin_amdgcn_readfirstlane(sequence_of(off, a.batch, n, M, tile, lane));
+  const Rows mine = rows_of(off, s, a.batch, n);
+  const Rows other = s < a.batch ? rows_of(keys ? a.q_off : a.k_off, s, a.batch, keys ? a.n_q : a.n_k) : Rows{0, 0};
+  const int first = (int)(tile - (mine.start / M + s)) * M;
+  if (keys) return TilePlace{first, (int)other.start, other.len, (int)mine.start, mine.len, {}};
+  return TilePlace{first, (int)mine.start, mine.len, (int)other.start, other.len, {}};
 }
 
 // ---- the order of tiles ----------------------------------------------------------------
@@ -57,9 +68,9 @@ inline bool ordered(int batch, int64_t tiles, int heads) {
   return batch > 1 && batch <= kOrderBatch && tiles <= kOrderTiles && tiles * heads > 512;
 }
 
-// order[rank] = tile, by falling numbers of keys (of queries for tiles of keys) that its M
-// rows see (are seen by), those of empty tiles last.
-__global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int tiles, int32_t *order) {
+// order[rank] = a tile's place, by falling numbers of keys (of queries for tiles of keys)
+// that its M rows see (are seen by), empty tiles last.
+__global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int tiles, TilePlace *order) {
   __shared__ int mine[kOrderBatch + 1], other[kOrderBatch + 1], work[kOrderTiles];
   const int32_t *off = keys ? a.k_off : a.q_off, *oth = keys ? a.q_off : a.k_off;
   const int64_t n = keys ? a.n_k : a.n_q, no = keys ? a.n_q : a.n_k;
@@ -68,6 +79,7 @@ __global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int
     other[i] = (int)offset_of(oth, i, no);
   }
   __syncthreads();
+  TilePlace place{};  // of tile 256 blockIdx.x + threadIdx.x
   for (int t = threadIdx.x; t < tiles; t += 256) {
     int s = 0;
     for (int step = 1024; step; step >>= 1)
@@ -89,6 +101,10 @@ __global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int
       w = 1 + max(0, to - from);
     }
     work[t] = w;
+    if (t / 256 == (int)blockIdx.x) {
+      const int other0 = s < a.batch ? other[s] : 0;
+      place = keys ? TilePlace{r0, other0, lo, mine[s], len, {}} : TilePlace{r0, mine[s], len, other0, lo, {}};
+    }
   }
   __syncthreads();
   const int t = blockIdx.x * 256 + threadIdx.x;
@@ -96,7 +112,7 @@ __global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int
   const int w = work[t];
   int rank = 0;
   for (int u = 0; u < tiles; ++u) rank += work[u] > w || (work[u] == w && u < t);
-  order[rank] = t;
+  order[rank] = place;
 }
 
 // Rows of the other side a step: two steps' tiles of two blocks fit a CU's LDS.
@@ -116,12 +132,11 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
   extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;  // two tiles of keys, two of values
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
-  const Work w = work_of(a, a.q_order, tiles);
-  if (w.tile < 0) return;
-  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l));
-  const Rows rq = rows_of(a.q_off, s, a.batch, a.n_q);
-  const Rows rk = s < a.batch ? rows_of(a.k_off, s, a.batch, a.n_k) : Rows{0, 0};
-  const int first = (int)(w.tile - (rq.start / kBlock + s)) * kBlock;  // the block's first query
+  const Work w = work_of(a);
+  if (w.rank >= tiles) return;
+  const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, kBlock, tiles - 1 - w.rank, l);
+  const Rows rq{at.q_start, at.lq}, rk{at.k_start, at.lk};
+  const int first = at.first;
   if (first >= rq.len) return;
   const int lq = rq.len, lk = rk.len;
   const int q0 = first + kRows * wave, qi = q0 + (l & 31);
@@ -313,12 +328,11 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
   extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;  // [2][K tile, V tile]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
-  const Work w = work_of(a, a.q_order, tiles);
-  if (w.tile < 0) return;
-  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.q_off, a.batch, a.n_q, kBlock, w.tile, l));
-  const Rows rq = rows_of(a.q_off, s, a.batch, a.n_q);
-  const Rows rk = s < a.batch ? rows_of(a.k_off, s, a.batch, a.n_k) : Rows{0, 0};
-  const int first = (int)(w.tile - (rq.start / kBlock + s)) * kBlock;
+  const Work w = work_of(a);
+  if (w.rank >= tiles) return;
+  const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, kBlock, tiles - 1 - w.rank, l);
+  const Rows rq{at.q_start, at.lq}, rk{at.k_start, at.lk};
+  const int first = at.first;
   if (first >= rq.len) return;
   const int lq = rq.len, lk = rk.len;
   const int q0 = first + kRows * wave, qi = q0 + (l & 31);
@@ -487,11 +501,9 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
   const int64_t id = blk::block_id();
   const int kv = (int)(id % a.hk);
   if (id / a.hk >= tiles) return;
-  const int64_t tile = a.k_order ? a.k_order[id / a.hk] : id / a.hk;
-  const int s = __builtin_amdgcn_readfirstlane(sequence_of(a.k_off, a.batch, a.n_k, KB, tile, l));
-  const Rows rk = rows_of(a.k_off, s, a.batch, a.n_k);
-  const Rows rq = s < a.batch ? rows_of(a.q_off, s, a.batch, a.n_q) : Rows{0, 0};
-  const int first = (int)(tile - (rk.start / KB + s)) * KB;
+  const TilePlace place = a.k_order ? a.k_order[id / a.hk] : tile_place(a, true, KB, id / a.hk, l);
+  const Rows rq{place.q_start, place.lq}, rk{place.k_start, place.lk};
+  const int first = place.first;
   if (first >= rk.len) return;
   const int lq = rq.len, lk = rk.len, group = a.hq / a.hk;
   const int k0 = first + kRows * NK * wave;
@@ -728,7 +740,7 @@ int parts_of(int hq, int hk, int64_t n_q, int64_t n_k, int batch) {
 }
 
 // Fills the order of tiles of M rows, or says that it is not used.
-int32_t *order_tiles(const AttnArgs &a, bool keys, int M, int32_t *order, hipStream_t st) {
+TilePlace *order_tiles(const AttnArgs &a, bool keys, int M, TilePlace *order, hipStream_t st) {
   const int64_t tiles = tiles_of(keys ? a.n_k : a.n_q, M, a.batch);
   if (!ordered(a.batch, tiles, keys ? a.hk : a.hq)) return nullptr;
   k_order<<<(int)(tiles + 255) / 256, 256, 0, st>>>(a, keys, M, (int)tiles, order);
@@ -742,7 +754,7 @@ bool attn_size_ok(int hq, int batch, int64_t n) {
 }
 size_t attn_q_order(const ipttt_attention &d) {
   const int64_t tiles = tiles_of(d.n_q, kBlock, d.batch);
-  return ordered(d.batch, tiles, d.q_heads) ? round_up(tiles * 4, 256) : 256;
+  return ordered(d.batch, tiles, d.q_heads) ? round_up(tiles * sizeof(TilePlace), 256) : 256;
 }
 size_t attn_parts(const ipttt_attention &d) {
   const int parts = parts_of(d.q_heads, d.k_heads, d.n_q, d.n_k, d.batch);
@@ -750,7 +762,7 @@ size_t attn_parts(const ipttt_attention &d) {
 }
 size_t attn_k_order(const ipttt_attention &d) {
   const int64_t tiles = tiles_of(d.n_k, kBlock, d.batch);
-  return round_up((tiles < kOrderTiles ? tiles : kOrderTiles) * 4, 256);
+  return ordered(d.batch, tiles, d.k_heads) ? round_up(tiles * sizeof(TilePlace), 256) : 256;
 }
 
 template <typename T>

@@ -124,9 +124,8 @@ template <typename T, int DP>
 constexpr int blocks_a_cu() { return sizeof(T) == 4 && DP > 64 ? 1 : 2; }
 constexpr int kAhead = 4;  // operands read from LDS ahead of their products
 
-template <typename T, int DP>
+template <typename T, int DP, int CH>
 __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnArgs a, int64_t tiles) {
-  using L = Tile<T, DP>;
   constexpr int KS = step_rows<T>(), NT = KS / 32;
   using C = Copier<T, DP, KS, kWaves>;
   extern __shared__ __align__(1024) char smem[];
@@ -144,9 +143,9 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
   const T *qp = (const T *)a.q.p + (rq.start + qr) * a.q.tok_stride + w.head * a.q.head_stride;
   const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh, wave, l);
   const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh, wave, l);
-  Frag<T> q[L::STEPS];
+  Frag<T> q[CH / 16];
 #pragma unroll
-  for (int i = 0; i < L::STEPS; ++i) q[i] = with_sign<T>(load_frag<T>(qp, i, h, a.dh), a.scale);
+  for (int i = 0; i < CH / 16; ++i) q[i] = with_sign<T>(load_frag<T>(qp, i, h, a.dh), a.scale);
   const Seen mine = seen_by(a, qi, lq, lk);
   const Seen head = seen_by(a, first, lq, lk), tail = seen_by(a, min(first + kBlock, lq) - 1, lq, lk);
   // what all, and what some, of this wave's rows see (those behind the last are not stored)
@@ -156,15 +155,15 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
     clear(buf, 4 * KS * DP, tid, kThreads);
     __syncthreads();
   }
-  f32x16 acc[DP / 32], x[NT];
+  f32x16 acc[CH / 32], x[NT];
   Frag<T> p[KS / 16], v[kAhead];
   float m, sum, mc = 0.f;
   const int begin = head.lo / KS * KS;
-  constexpr int N = KS / 16 * (DP / 32), PER = 16 * NT / N;
+  constexpr int N = KS / 16 * (CH / 32), E = 16 * NT;
   constexpr int TILE = KS * DP * (int)sizeof(T);
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
+    for (int d = 0; d < CH / 32; ++d) acc[d] = f32x16{};
 #pragma unroll
     for (int i = 0; i < KS / 16; ++i) p[i] = zero_frag<T>();
     m = -INFINITY;
@@ -174,7 +173,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
     ColReader<T, DP> vr(buf + 3 * KS * DP, l);
     const auto key = [&](int n) __attribute__((always_inline)) { return kr.read(32 * (n % NT), n / NT); };
     const auto value = [&](int n) __attribute__((always_inline)) {
-      return vr.read(16 * (n / (DP / 32)), n % (DP / 32));
+      return vr.read(16 * (n / (CH / 32)), n % (CH / 32));
     };
     if (begin < tail.hi) kc.issue(buf, begin, lk, a.dh, wave, l, kAsIs);
     clear(buf + 3 * KS * DP, KS * DP, tid, kThreads);  // no tile before the first
@@ -191,7 +190,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
       const unsigned keys = max(0, mine.hi - mine.lo);
       const auto sees = [&](int j) { return (unsigned)(from + j) < keys; };
       {
-        constexpr int M = NT * L::STEPS;
+        constexpr int M = NT * CH / 16;
         Frag<T> k[kAhead];
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) k[n] = key(n);
@@ -235,11 +234,11 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
       float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        f32x16 &o = acc[n % (DP / 32)];
-        o = mma(v[n % kAhead], p[n / (DP / 32)], o);
+        f32x16 &o = acc[n % (CH / 32)];
+        o = mma(v[n % kAhead], p[n / (CH / 32)], o);
         if (n + kAhead < N) v[n % kAhead] = value(n + kAhead);
 #pragma unroll
-        for (int e = PER * n; e < PER * (n + 1); ++e) {
+        for (int e = E * n / N; e < E * (n + 1) / N; ++e) {
           float weight = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -mc));
           asm volatile("" : "+v"(weight));  // here, not behind the products
           x[e / 16][e % 16] = weight;
@@ -251,7 +250,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
       sum += (part[0] + part[1]) + (part[2] + part[3]);
       if (rescale) {
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
+        for (int d = 0; d < CH / 32; ++d)
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[d][e] *= f;
       }
@@ -272,7 +271,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
     mfma::lds_barrier();
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      acc[n % (DP / 32)] = mma(value(n), p[n / (DP / 32)], acc[n % (DP / 32)]);
+      acc[n % (CH / 32)] = mma(value(n), p[n / (CH / 32)], acc[n % (CH / 32)]);
     if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
     const float total = half_sum(sum);
     if (qi < lq) {
@@ -280,9 +279,9 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
       T *const op = (T *)a.o.p + (rq.start + qi) * a.o.tok_stride + w.head * a.o.head_stride;
       if (none) {
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
+        for (int d = 0; d < CH / 32; ++d) acc[d] = f32x16{};
       }
-      store_row<T, DP>(op, acc, none ? 0.f : 1.f / total, h, a.dh, fix);
+      store_row<T, CH>(op, acc, none ? 0.f : 1.f / total, h, a.dh, fix);
       if (a.lse && h == 0)
         a.lse[w.head * a.n_q + rq.start + qi] = none ? -INFINITY : (m * c + log2f(total)) * kLn2;
     }
@@ -320,9 +319,8 @@ __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
 }
 
 // dq: a block's queries, over the keys that they see.
-template <typename T, int DP>
+template <typename T, int DP, int CH>
 __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArgs a, int64_t tiles) {
-  using L = Tile<T, DP>;
   constexpr int KS = step_rows<T>(), NT = KS / 32, STAGE = 2 * KS * DP * (int)sizeof(T);
   using C = Copier<T, DP, KS, kWaves>;
   extern __shared__ __align__(1024) char smem[];
@@ -341,9 +339,9 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
   const T *yp = (const T *)a.dy.p + qr * a.dy.tok_stride + w.head * a.dy.head_stride;
   const C kc((const T *)a.k.p + rk.start * a.k.tok_stride + w.kv * a.k.head_stride, a.k.tok_stride, a.dh, wave, l);
   const C vc((const T *)a.v.p + rk.start * a.v.tok_stride + w.kv * a.v.head_stride, a.v.tok_stride, a.dh, wave, l);
-  Frag<T> q[L::STEPS], dy[L::STEPS];
+  Frag<T> q[CH / 16], dy[CH / 16];
 #pragma unroll
-  for (int i = 0; i < L::STEPS; ++i) {
+  for (int i = 0; i < CH / 16; ++i) {
     q[i] = with_sign<T>(load_frag<T>(qp, i, h, a.dh), a.scale);
     dy[i] = load_frag<T>(yp, i, h, a.dh);
   }
@@ -357,10 +355,10 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
     __syncthreads();
   }
   const int begin = head.lo / KS * KS;
-  f32x16 acc[DP / 32];
+  f32x16 acc[CH / 32];
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d) acc[d] = f32x16{};
+    for (int d = 0; d < CH / 32; ++d) acc[d] = f32x16{};
     int cur = 0;
     RowReader<T, DP> rows(buf, l);
     ColReader<T, DP> cols(buf, l);
@@ -387,7 +385,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
       // For each 32 keys S and dP, then the sums for all of them; what the vector units do
       // goes beside the products that do not wait for it:
       //   S(t) beside dS(t - 1), dP(t) beside P(t), the first sums beside the last dS.
-      constexpr int S = L::STEPS, ND = DP / 32, LEN = NT * (2 * S + 2 * ND);
+      constexpr int S = CH / 16, ND = CH / 32, LEN = NT * (2 * S + 2 * ND);
       const auto operand = [&](int m) __attribute__((always_inline)) {
         if (m >= 2 * S * NT) {
           const int e = m - 2 * S * NT;
@@ -431,7 +429,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
         for (int o = 0; o < S; ++o) {
           const int m = 2 * S * t + o;
           x[t] = mma(f[m % kAhead], q[o], x[t]);
-          if (t > 0) grad(t - 1, 16 / S * o, 16 / S * (o + 1));
+          if (t > 0) grad(t - 1, 16 * o / S, 16 * (o + 1) / S);
           refill(m);
         }
         if (t > 0) finish(t - 1);
@@ -440,7 +438,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
           const int m = 2 * S * t + S + o;
           y[t] = mma(f[m % kAhead], dy[o], y[t]);
 #pragma unroll
-          for (int e = 16 / S * o; e < 16 / S * (o + 1); ++e) {
+          for (int e = 16 * o / S; e < 16 * (o + 1) / S; ++e) {
             float v = exp2_(__builtin_fmaf(x[t][e], c, -lse));
             asm volatile("" : "+v"(v));
             x[t][e] = v;
@@ -459,8 +457,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
           const int m = 2 * S * NT + 2 * ND * t + o;
           acc[o % ND] = mma(f[m % kAhead], ds[t][o / ND], acc[o % ND]);
           if (NT > 1 && t == 0) {
-            constexpr int PER = 16 / (2 * ND);
-            grad(NT - 1, PER * o, PER * (o + 1));
+            grad(NT - 1, 16 * o / (2 * ND), 16 * (o + 1) / (2 * ND));
           }
           refill(m);
           if (NT > 1 && t == 0 && o == 2 * ND - 1) finish(NT - 1);
@@ -470,7 +467,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
     }
     if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
     if (qi < lq)
-      store_row<T, DP>((T *)a.dq.p + (rq.start + qi) * a.dq.tok_stride + w.head * a.dq.head_stride, acc, a.scale,
+      store_row<T, CH>((T *)a.dq.p + (rq.start + qi) * a.dq.tok_stride + w.head * a.dq.head_stride, acc, a.scale,
                        h, a.dh, fix);
     if (fix != kCount) break;
     __syncthreads();
@@ -486,11 +483,10 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
 //   dV += dY^T P beside dS = P (dP - delta);   dK += Q^T dS.
 // Where the key tiles are few, `parts` blocks share a tile's steps (part blockIdx.z) and
 // leave partial sums, which k_dkv_join adds up.
-template <typename T, int DP, int NK>
+template <typename T, int DP, int CH, int NK>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(AttnArgs a, int64_t tiles, int parts) {
-  using L = Tile<T, DP>;
   constexpr int QS = 32, NT = QS / 32, STAGE = 2 * QS * DP * (int)sizeof(T);
-  constexpr int KB = NK * kBlock, ND = DP / 32, S = L::STEPS;
+  constexpr int KB = NK * kBlock, ND = CH / 32, S = CH / 16;
   constexpr int AHEAD = 3;  // operands read from LDS ahead of their products
   using C = Copier<T, DP, QS, kWaves>;
   extern __shared__ __align__(1024) char smem[];
@@ -610,7 +606,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
         f32x4v st;
         // a statistic of the rows of results e .. e + 3
         const auto stat = [&](const float *p, int e) __attribute__((always_inline)) {
-          return *(const f32x4v *)(p + 32 * t + 2 * (e % 16));
+          return *(const f32x4v *)(p + 32 * t + 8 * (e % 16 / 4));
         };
 #pragma unroll
         for (int j = 0; j < NK; ++j) x[j] = y[j] = f32x16{};
@@ -622,7 +618,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
           for (int j = 0; j < NK; ++j) x[j] = mma(f[(m0 + o) % AHEAD], k[j][o], x[j]);
           refill(m0 + o);
         }
-        constexpr int PB = 16 * NK / S, PC = 16 * NK / (2 * ND);
+        constexpr int E = 16 * NK;
 #pragma unroll
         for (int o = 0; o < S; ++o) {
 #pragma unroll
@@ -632,8 +628,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
             for (int j = 0; j < NK; ++j) vb[j] = rows.read_from(to_v, 32 * j, o + 1);
           }
 #pragma unroll
-          for (int e = PB * o; e < PB * (o + 1); ++e) {
-            if (e % 4 == 0) st = stat(lse, e);
+          for (int e = E * o / S; e < E * (o + 1) / S; ++e) {
+            if (e % 4 == 0 || e == E * o / S) st = stat(lse, e);
             float p = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -st[e % 4]));
             asm volatile("" : "+v"(p));  // here, not behind the products
             x[e / 16][e % 16] = p;
@@ -656,8 +652,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
 #pragma unroll
           for (int j = 0; j < NK; ++j) dv[j][o % ND] = mma(f[(m0 + 2 * S + o) % AHEAD], w[j][o / ND], dv[j][o % ND]);
 #pragma unroll
-          for (int e = PC * o; e < PC * (o + 1); ++e) {
-            if (e % 4 == 0) st = stat(delta, e);
+          for (int e = E * o / (2 * ND); e < E * (o + 1) / (2 * ND); ++e) {
+            if (e % 4 == 0 || e == E * o / (2 * ND)) st = stat(delta, e);
             float ds = x[e / 16][e % 16] * (y[e / 16][e % 16] - st[e % 4]);
             asm volatile("" : "+v"(ds));
             y[e / 16][e % 16] = ds;
@@ -694,12 +690,12 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
         const int64_t kr = rk.start + kj;
         if (parts > 1) {
           float *const pk = a.part + ((((int64_t)blockIdx.z * a.n_k + kr) * a.hk + kv) * 2) * a.dh;
-          store_row<float, DP>(pk, dk[j], a.scale, h, a.dh, kAsIs);
-          store_row<float, DP>(pk + a.dh, dv[j], 1.f, h, a.dh, fix);
+          store_row<float, CH>(pk, dk[j], a.scale, h, a.dh, kAsIs);
+          store_row<float, CH>(pk + a.dh, dv[j], 1.f, h, a.dh, fix);
           continue;
         }
-        store_row<T, DP>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk[j], a.scale, h, a.dh, kAsIs);
-        store_row<T, DP>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv[j], 1.f, h, a.dh, fix);
+        store_row<T, CH>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk[j], a.scale, h, a.dh, kAsIs);
+        store_row<T, CH>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv[j], 1.f, h, a.dh, fix);
       }
     }
     if (fix != kCount) break;
@@ -720,9 +716,14 @@ __global__ __launch_bounds__(256) void k_dkv_join(AttnArgs a, int parts) {
   ((T *)out.p)[kr * out.tok_stride + x / 2 * out.head_stride + c] = (T)v;
 }
 
+// f(channels a row has in LDS, channels that are computed): rows of 65 to 96 channels leave
+// out a quarter of the products.
 template <typename T, class F>
 void by_width(int dh, F f) {
-  if (dh <= 64) f(std::integral_constant<int, 64>()); else f(std::integral_constant<int, 128>());
+  using std::integral_constant;
+  if (dh <= 64) f(integral_constant<int, 64>(), integral_constant<int, 64>());
+  else if (dh <= 96) f(integral_constant<int, 128>(), integral_constant<int, 96>());
+  else f(integral_constant<int, 128>(), integral_constant<int, 128>());
 }
 
 // Rows of a tile of keys.
@@ -769,10 +770,10 @@ template <typename T>
 hipError_t attn_forward(const AttnArgs &args, hipStream_t st) {
   AttnArgs a = args;
   a.q_order = order_tiles(a, false, kBlock, a.q_order, st);
-  by_width<T>(a.dh, [&](auto dp) {
-    constexpr int DP = decltype(dp)::value;
+  by_width<T>(a.dh, [&](auto dp, auto ch) {
+    constexpr int DP = decltype(dp)::value, CH = decltype(ch)::value;
     const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);
-    k_fwd<T, DP><<<blk::grid_of(tiles * a.hq), kThreads, 4 * step_rows<T>() * DP * sizeof(T), st>>>(
+    k_fwd<T, DP, CH><<<blk::grid_of(tiles * a.hq), kThreads, 4 * step_rows<T>() * DP * sizeof(T), st>>>(
         a, tiles);
   });
   return hipGetLastError();
@@ -785,21 +786,21 @@ hipError_t attn_backward(const AttnArgs &args, hipStream_t st) {
   a.k_order = order_tiles(a, true, key_rows<T>(), a.k_order, st);
   const int parts = parts_of(a.hq, a.hk, a.n_q, a.n_k, a.batch);
   if (a.n_q > 0) k_delta<T><<<blk::grid_of((a.n_q * a.hq + 15) / 16), 256, 0, st>>>(a);
-  by_width<T>(a.dh, [&](auto dp) {
-    constexpr int DP = decltype(dp)::value;
+  by_width<T>(a.dh, [&](auto dp, auto ch) {
+    constexpr int DP = decltype(dp)::value, CH = decltype(ch)::value;
     const size_t lds = 4 * step_rows<T>() * DP * sizeof(T);
     if (a.n_k > 0) {
       constexpr int KB = key_rows<T>();
       const int64_t tiles = tiles_of(a.n_k, KB, a.batch);
       dim3 grid = blk::grid_of(tiles * a.hk);
       grid.z = parts;
-      k_dkv<T, DP, KB / kBlock><<<grid, kThreads, (4 * 32 + KB) * DP * sizeof(T) + 4 * 64 * sizeof(float), st>>>(
+      k_dkv<T, DP, CH, KB / kBlock><<<grid, kThreads, (4 * 32 + KB) * DP * sizeof(T) + 4 * 64 * sizeof(float), st>>>(
           a, tiles, parts);
       if (parts > 1) k_dkv_join<T><<<blk::grid_of((a.n_k * a.hk * 2 * a.dh + 255) / 256), 256, 0, st>>>(a, parts);
     }
     if (a.n_q > 0) {
       const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);
-      k_dq<T, DP><<<blk::grid_of(tiles * a.hq), kThreads, lds, st>>>(a, tiles);
+      k_dq<T, DP, CH><<<blk::grid_of(tiles * a.hq), kThreads, lds, st>>>(a, tiles);
     }
   });
   return hipGetLastError();

@@ -300,9 +300,12 @@ ipttt_status ipttt_headnorm_append(const ipttt_headnorm_desc *desc, const ipttt_
 }
 
 size_t ipttt_headnorm_backward_workspace_bytes(const ipttt_headnorm_desc *desc, int64_t n) {
-  if (!desc || desc->head_dim < 1 || desc->head_dim > kHeadMaxDim || n < 0 || n > INT32_MAX)
+  if (!desc || check_head_counts(desc->q_heads, desc->k_heads, desc->head_dim) != IPTTT_OK || n < 0 ||
+      n > INT32_MAX)
     return 0;
-  return (size_t)round_up((int64_t)heads_bwd_blocks(n) * 2 * desc->head_dim * 4, 256);
+  const int all = desc->q_heads + desc->k_heads;
+  const int64_t rows = heads_bwd_blocks(desc->q_heads, all, n) + heads_bwd_blocks(desc->k_heads, all, n);
+  return (size_t)round_up(rows * desc->head_dim * 4, 256);
 }
 
 ipttt_status ipttt_headnorm_backward(const ipttt_headnorm_desc *desc, const ipttt_heads *q,

@@ -27,10 +27,10 @@ struct HeadArgs {
   ipttt_kv_cache cache;    // append
   ipttt_page_table table;  // append
   float *dq_gamma, *dk_gamma;  // [dh] or null
-  float *part;             // backward: [heads_bwd_blocks][2][dh] partial sums
+  float *part;             // backward: [blocks of q and of k][dh] partial sums
 };
-// Blocks (and partial sums) of the backward.
-int heads_bwd_blocks(int64_t n);
+// Blocks (and rows of partial sums) of the backward for `heads` of all its heads.
+int heads_bwd_blocks(int heads, int all, int64_t n);
 template <typename T>
 hipError_t heads_forward(const HeadArgs &a, hipStream_t st);
 template <typename T>

@@ -230,41 +230,46 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a, Split s, int sli
   }
 }
 
-// Each wave goes over tokens and keeps its lanes' part of the weights' gradients; a
-// block adds up its waves' and leaves one row of partial sums for each weight.
+// A block goes over tokens of the queries, or of the keys (from block `q_blocks` on): each
+// wave keeps its lanes' part of the weight's gradient, and the block leaves one row of
+// partial sums. The next heads' rows are loaded beside this one's arithmetic.
 template <typename T, int W, bool IL>
-__global__ __launch_bounds__(kThreads) void k_heads_bwd(HeadArgs a, Split s) {
+__global__ __launch_bounds__(kThreads) void k_heads_bwd(HeadArgs a, Split s, int q_blocks) {
   __shared__ float2 cs[kThreads];
-  __shared__ float sums[kWaves][2][kHeadMaxDim];
+  __shared__ float sums[kWaves][kHeadMaxDim];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool keys = (int)blockIdx.x >= q_blocks;
+  const int block = keys ? blockIdx.x - q_blocks : blockIdx.x;
+  const int blocks = keys ? gridDim.x - q_blocks : q_blocks;
+  const ipttt_heads x = keys ? a.k : a.q, dy = keys ? a.dk : a.dq, dx = keys ? a.k_out : a.q_out;
+  const T *const gamma = (const T *)(keys ? a.k_gamma : a.q_gamma);
+  const bool normed = gamma != nullptr;
   const Place<W, IL> p(s, a.dh, lane);
-  float gq[2][W], gk[2][W], sq[2][W], sk[2][W];
-  load_gamma<T, W, IL>((const T *)a.q_gamma, p, gq[0], gq[1]);
-  load_gamma<T, W, IL>((const T *)a.k_gamma, p, gk[0], gk[1]);
+  float g[2][W], sum_g[2][W];
+  load_gamma<T, W, IL>(gamma, p, g[0], g[1]);
 #pragma unroll
-  for (int e = 0; e < W; ++e) sq[0][e] = sq[1][e] = sk[0][e] = sk[1][e] = 0.f;
-  const int at_once = 64 / s.lanes, sub = lane / s.lanes, rows = a.hq + a.hk;
+  for (int e = 0; e < W; ++e) sum_g[0][e] = sum_g[1][e] = 0.f;
+  const int at_once = 64 / s.lanes, sub = lane / s.lanes, rows = keys ? a.hk : a.hq;
   const float inv_d = 1.f / (float)a.dh;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.n; t += (int64_t)gridDim.x * kWaves) {
-    float c[W], sn[W];
-    angles<W>(a.inv_freq, s.r2, a.pos[t], lane, p.pair, cs + 64 * wave, c, sn);
-    for (int base = 0; base < rows; base += at_once) {
-      const int h = base + sub;
-      const bool live = h < rows, is_q = h < a.hq;
-      const int hh = is_q ? h : h - a.hq;
-      float xa[W], xb[W], ya[W], yb[W];
-      T *dst = nullptr;
-      if (live) {
-        const ipttt_heads &x = is_q ? a.q : a.k, &dy = is_q ? a.dq : a.dk;
-        const ipttt_heads &dx = is_q ? a.q_out : a.k_out;
-        load_pairs<T, W, IL>((const T *)x.p + t * x.tok_stride + hh * x.head_stride, p, xa, xb);
-        load_pairs<T, W, IL>((const T *)dy.p + t * dy.tok_stride + hh * dy.head_stride, p, ya, yb);
-        dst = (T *)dx.p + t * dx.tok_stride + hh * dx.head_stride;
+  for (int64_t t = (int64_t)block * kWaves + wave; t < a.n; t += (int64_t)blocks * kWaves) {
+    // x and dy of head h (zero behind the last)
+    const auto load = [&](int h, float (&x0)[W], float (&x1)[W], float (&y0)[W], float (&y1)[W])
+                          __attribute__((always_inline)) {
+      if (h < rows) {
+        load_pairs<T, W, IL>((const T *)x.p + t * x.tok_stride + h * x.head_stride, p, x0, x1);
+        load_pairs<T, W, IL>((const T *)dy.p + t * dy.tok_stride + h * dy.head_stride, p, y0, y1);
       } else {
 #pragma unroll
-        for (int e = 0; e < W; ++e) xa[e] = xb[e] = ya[e] = yb[e] = 0.f;
+        for (int e = 0; e < W; ++e) x0[e] = x1[e] = y0[e] = y1[e] = 0.f;
       }
-      const bool normed = is_q ? a.q_gamma != nullptr : a.k_gamma != nullptr;
+    };
+    float xa[W], xb[W], ya[W], yb[W], na[W], nb[W], ma[W], mb[W], c[W], sn[W];
+    load(sub, na, nb, ma, mb);
+    angles<W>(a.inv_freq, s.r2, a.pos[t], lane, p.pair, cs + 64 * wave, c, sn);
+    for (int h = sub; h - sub < rows; h += at_once) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) xa[e] = na[e], xb[e] = nb[e], ya[e] = ma[e], yb[e] = mb[e];
+      load(h + at_once, na, nb, ma, mb);
       float sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int e = 0; e < W; ++e) {
@@ -272,71 +277,66 @@ __global__ __launch_bounds__(kThreads) void k_heads_bwd(HeadArgs a, Split s) {
         const float ga = ya[e] * c[e] + yb[e] * sn[e], gb = yb[e] * c[e] - ya[e] * sn[e];
         ya[e] = ga;
         yb[e] = gb;
-        dot += ga * (is_q ? gq[0][e] : gk[0][e]) * xa[e] + gb * (is_q ? gq[1][e] : gk[1][e]) * xb[e];
+        dot += ga * g[0][e] * xa[e] + gb * g[1][e] * xb[e];
       }
-      sum = head_sum(sum, s.lanes);
-      dot = head_sum(dot, s.lanes);
-      if (!live) continue;  // whole heads drop out: no sum is split
-      const float r = 1.f / sqrtf(sum * inv_d + a.eps);
-      const float k = dot * r * r * r * inv_d;
       if (normed) {
+        sum = head_sum(sum, s.lanes);
+        dot = head_sum(dot, s.lanes);
+      }
+      if (h >= rows) continue;  // whole heads drop out: no sum is split
+      if (normed) {
+        const float r = 1.f / sqrtf(sum * inv_d + a.eps);
+        const float k = dot * r * r * r * inv_d;
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          const float za = ya[e] * xa[e] * r, zb = yb[e] * xb[e] * r;
-          sq[0][e] += is_q ? za : 0.f;
-          sq[1][e] += is_q ? zb : 0.f;
-          sk[0][e] += is_q ? 0.f : za;
-          sk[1][e] += is_q ? 0.f : zb;
-          ya[e] = ya[e] * (is_q ? gq[0][e] : gk[0][e]) * r - xa[e] * k;
-          yb[e] = yb[e] * (is_q ? gq[1][e] : gk[1][e]) * r - xb[e] * k;
+          sum_g[0][e] += ya[e] * xa[e] * r;
+          sum_g[1][e] += yb[e] * xb[e] * r;
+          ya[e] = ya[e] * g[0][e] * r - xa[e] * k;
+          yb[e] = yb[e] * g[1][e] * r - xb[e] * k;
         }
       }
-      store_pairs<T, W, IL>(dst, p, ya, yb);
+      store_pairs<T, W, IL>((T *)dx.p + t * dx.tok_stride + h * dx.head_stride, p, ya, yb);
     }
   }
   if (!a.part) return;
   // over the lanes that hold the same pairs, then over the waves
   for (int m = s.lanes; m < 64; m <<= 1)
 #pragma unroll
-    for (int e = 0; e < W; ++e)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        sq[b][e] += __shfl_xor(sq[b][e], m, 64);
-        sk[b][e] += __shfl_xor(sk[b][e], m, 64);
-      }
-  if (sub == 0) {
-    store_pairs<float, W, IL>(sums[wave][0], p, sq[0], sq[1]);
-    store_pairs<float, W, IL>(sums[wave][1], p, sk[0], sk[1]);
-  }
+    for (int e = 0; e < W; ++e) {
+      sum_g[0][e] += __shfl_xor(sum_g[0][e], m, 64);
+      sum_g[1][e] += __shfl_xor(sum_g[1][e], m, 64);
+    }
+  if (sub == 0) store_pairs<float, W, IL>(sums[wave], p, sum_g[0], sum_g[1]);
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.dh; i += kThreads) {
-    const int which = i / a.dh, ch = i - which * a.dh;
+  for (int i = threadIdx.x; i < a.dh; i += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += sums[w][which][ch];
-    a.part[(int64_t)blockIdx.x * 2 * a.dh + i] = v;
+    for (int w = 0; w < kWaves; ++w) v += sums[w][i];
+    a.part[(int64_t)blockIdx.x * a.dh + i] = v;
   }
 }
 
 // Column sums of the blocks' partial rows, in a fixed order: 32 columns a block, 32
-// threads a column.
-__global__ __launch_bounds__(1024) void k_heads_gamma(const float *part, int blocks, int dh,
+// threads a column. blockIdx.y: the queries' or the keys' rows.
+__global__ __launch_bounds__(1024) void k_heads_gamma(const float *part, int q_blocks, int k_blocks, int dh,
                                                       float *dq_gamma, float *dk_gamma) {
   __shared__ float sums[32][33];
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
+  const float *const first = part + (blockIdx.y ? (int64_t)q_blocks * dh : 0);
+  const int blocks = blockIdx.y ? k_blocks : q_blocks;
   float v = 0.f;
-  if (col < 2 * dh) {
+  if (col < dh) {
 #pragma unroll 8
-    for (int b = row; b < blocks; b += 32) v += part[(int64_t)b * 2 * dh + col];
+    for (int b = row; b < blocks; b += 32) v += first[(int64_t)b * dh + col];
   }
   sums[row][threadIdx.x & 31] = v;
   __syncthreads();
-  if (row == 0 && col < 2 * dh) {
+  if (row == 0 && col < dh) {
     v = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v += sums[i][threadIdx.x];
-    float *out = col < dh ? dq_gamma : dk_gamma;
-    if (out) out[col < dh ? col : col - dh] = v;
+    float *out = blockIdx.y ? dk_gamma : dq_gamma;
+    if (out) out[col] = v;
   }
 }
 
@@ -375,9 +375,9 @@ hipError_t launch_heads(const HeadArgs &a, hipStream_t st) {
 
 }  // namespace
 
-int heads_bwd_blocks(int64_t n) {
-  const int64_t b = (n + kWaves - 1) / kWaves;
-  return (int)(b < 1 ? 1 : b > 2048 ? 2048 : b);
+int heads_bwd_blocks(int heads, int all, int64_t n) {
+  const int64_t b = (n + kWaves - 1) / kWaves, most = (int64_t)2048 * heads / all;
+  return (int)(b < 1 ? 1 : b > most ? (most < 1 ? 1 : most) : b);
 }
 
 template <typename T>
@@ -390,13 +390,13 @@ hipError_t heads_append(const HeadArgs &a, hipStream_t st) {
 }
 template <typename T>
 hipError_t heads_backward(const HeadArgs &a, hipStream_t st) {
-  const int blocks = heads_bwd_blocks(a.n);
+  const int qb = heads_bwd_blocks(a.hq, a.hq + a.hk, a.n), kb = heads_bwd_blocks(a.hk, a.hq + a.hk, a.n);
   by_layout<T>(a, [&](auto w, auto il) {
     constexpr int W = decltype(w)::value;
-    k_heads_bwd<T, W, decltype(il)::value><<<blocks, kThreads, 0, st>>>(a, split_of(a, W));
+    k_heads_bwd<T, W, decltype(il)::value><<<qb + kb, kThreads, 0, st>>>(a, split_of(a, W), qb);
   });
   if (a.part)
-    k_heads_gamma<<<(2 * a.dh + 31) / 32, 1024, 0, st>>>(a.part, blocks, a.dh, a.dq_gamma, a.dk_gamma);
+    k_heads_gamma<<<dim3((a.dh + 31) / 32, 2), 1024, 0, st>>>(a.part, qb, kb, a.dh, a.dq_gamma, a.dk_gamma);
   return hipGetLastError();
 }
 

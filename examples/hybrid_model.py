@@ -2,7 +2,8 @@
 framework's operators.
 
 Each block is two residual branches in pre-norm form:
-  h += W_out mix(W_mix norm(h))   the gated linear recurrence as token mixer
+  h += W_out mix(W_mix norm(h))   the gated linear recurrence as token mixer, or causal
+                                  attention in the blocks listed in `attend`
   h += mlp(norm(h))               the gated feed-forward block, or the fast-weight
                                   layer in the blocks listed in `fast`
 The residual add of a branch runs inside the next norm. Projections and the
@@ -20,17 +21,18 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from chunked_weight_mlp_amd import Layer, block  # noqa: E402
+from chunked_weight_mlp_amd import Layer, attention, block  # noqa: E402
 
 BF16 = torch.bfloat16
 
 
 class HybridModel:
     def __init__(self, vocab=256, d=128, d_ff=256, blocks=2, fast=(1,), chunk=64, max_batch=2,
-                 max_seq_len=512, eta=1e-3, device="cuda", seed=0):
+                 max_seq_len=512, eta=1e-3, device="cuda", seed=0, attend=(), heads=4, k_heads=2):
         g = torch.Generator().manual_seed(seed)
         self.d, self.chunk, self.fast, self.blocks, self.eta = d, chunk, set(fast), blocks, eta
         self.max_batch, self.max_seq_len, self.device = max_batch, max_seq_len, device
+        self.attend, self.hq, self.hk, self.dh = set(attend), heads, k_heads, d // heads
 
         def draw(*shape, std):
             return (torch.randn(*shape, generator=g) * std).to(device)
@@ -42,7 +44,12 @@ class HybridModel:
             for n in ("mix", "mlp"):
                 p[f"{i}.{n}.gamma"] = torch.ones(d, device=device)
                 p[f"{i}.{n}.beta"] = torch.zeros(d, device=device)
-            p[f"{i}.w_mix"] = draw(2 * d, d, std=d ** -0.5)
+            if i in self.attend:
+                p[f"{i}.w_mix"] = draw((heads + 2 * k_heads) * self.dh, d, std=d ** -0.5)
+                for n in ("q_gamma", "k_gamma"):
+                    p[f"{i}.{n}"] = torch.ones(self.dh, device=device)
+            else:
+                p[f"{i}.w_mix"] = draw(2 * d, d, std=d ** -0.5)
             p[f"{i}.w_out"] = draw(d, d, std=0.5 * d ** -0.5)
             p[f"{i}.w_gate"], p[f"{i}.w_up"] = draw(d_ff, d, std=d ** -0.5), draw(d_ff, d, std=d ** -0.5)
             p[f"{i}.w_down"] = draw(d, d_ff, std=0.5 * d_ff ** -0.5)
@@ -56,6 +63,9 @@ class HybridModel:
         w = self.w = {k: v.to(BF16) for k, v in self.params.items()}
         self.norms = {k[: -len(".gamma")]: block.Norm(w[k], w[k[: -len("gamma")] + "beta"])
                       for k in w if k.endswith(".gamma")}
+        inv_freq = 1e4 ** (-torch.arange(0, self.dh, 2, dtype=torch.float64, device=self.device) / self.dh)
+        self.head_norms = {i: attention.HeadNorm(w[f"{i}.q_gamma"], w[f"{i}.k_gamma"], inv_freq)
+                           for i in self.attend}
         self.mlps = {}
         for i in range(self.blocks):
             if i in self.fast:
@@ -67,6 +77,11 @@ class HybridModel:
             else:
                 self.mlps[i] = block.FeedForward(w[f"{i}.w_gate"], w[f"{i}.w_up"], w[f"{i}.w_down"])
 
+    def _heads(self, qkv):
+        """Queries, keys and values of a fused projection, [tokens, heads, dh] each."""
+        n = qkv.shape[-1] // self.dh
+        return qkv.view(-1, n, self.dh).split([self.hq, self.hk, self.hk], 1)
+
     # ---- training ----------------------------------------------------------------------
 
     def loss_and_grads(self, tokens, targets, starts=None):
@@ -76,10 +91,26 @@ class HybridModel:
         d, w = self.d, self.w
         e = w["embed"][tokens].contiguous()
         h, res, saved = e, None, []
+        if self.attend:
+            # the rows one after another: a sequence at each row's and each document's beginning
+            first = torch.zeros(tokens.shape, dtype=torch.bool, device=self.device)
+            first[:, 0] = True
+            first = (first if starts is None else first | (starts != 0)).flatten()
+            begin = first.nonzero()[:, 0]
+            offsets = torch.cat([begin, begin.new_tensor([first.numel()])]).to(torch.int32)
+            pos = (torch.arange(first.numel(), device=self.device)
+                   - begin[first.cumsum(0) - 1]).to(torch.int32)
         for i in range(self.blocks):
             y1, h1, m1, r1 = self.norms[f"{i}.mix"].forward(h, res)
             gv = y1 @ w[f"{i}.w_mix"].t()
-            s, _ = block.recurrence_forward(gv[..., :d], gv[..., d:], starts=starts)
+            if i in self.attend:
+                q, k, v = self._heads(gv)
+                qr, kr = self.head_norms[i].forward(q, k, pos)
+                o, lse = attention.attention_forward(qr, kr, v, offsets=offsets)
+                s, seen = o.view(tokens.shape + (d,)), (q, k, v, qr, kr, o, lse)
+            else:
+                s, _ = block.recurrence_forward(gv[..., :d], gv[..., d:], starts=starts)
+                seen = None
             y2, h2, m2, r2 = self.norms[f"{i}.mlp"].forward(h1, s @ w[f"{i}.w_out"].t())
             mlp, a, u = self.mlps[i], None, None
             if i in self.fast:
@@ -87,7 +118,7 @@ class HybridModel:
                 res = mlp.prefill(y2, e).to(BF16)
             else:
                 res, a, u = mlp.forward(y2, save=True)
-            saved.append((y1, h1, m1, r1, gv, s, y2, h2, m2, r2, a, u))
+            saved.append((y1, h1, m1, r1, gv, s, y2, h2, m2, r2, a, u, seen))
             h = h2
         y, hf, mf, rf = self.norms["final"].forward(h, res)
         logits = (y.float() @ w["embed"].float().t())
@@ -104,7 +135,7 @@ class HybridModel:
         dh = g["dx"]              # gradient of the residual stream and of the last branch
         de = torch.zeros_like(e, dtype=torch.float32)
         for i in reversed(range(self.blocks)):
-            y1, h1, m1, r1, gv, s, y2, h2, m2, r2, a, u = saved[i]
+            y1, h1, m1, r1, gv, s, y2, h2, m2, r2, a, u, seen = saved[i]
             mlp = self.mlps[i]
             if i in self.fast:
                 g = mlp.backward(y2, e, dh.float())
@@ -125,8 +156,16 @@ class HybridModel:
             grads[f"{i}.w_out"] = flat.float().t() @ s.float().flatten(0, 1)
             ds = dh @ w[f"{i}.w_out"]
             dgv = torch.empty_like(gv)
-            block.recurrence_backward(gv[..., :d], gv[..., d:], s, ds, starts=starts, dg=dgv[..., :d],
-                                      dv=dgv[..., d:])
+            if i in self.attend:
+                q, k, v, qr, kr, o, lse = seen
+                g = attention.attention_backward(qr, kr, v, o, lse, ds.view_as(o), offsets=offsets)
+                n = self.head_norms[i].backward(q, k, pos, g["dq"], g["dk"])
+                grads[f"{i}.q_gamma"], grads[f"{i}.k_gamma"] = n["dq_gamma"], n["dk_gamma"]
+                for part, grad in zip(self._heads(dgv), (n["dq"], n["dk"], g["dv"])):
+                    part.copy_(grad)
+            else:
+                block.recurrence_backward(gv[..., :d], gv[..., d:], s, ds, starts=starts, dg=dgv[..., :d],
+                                          dv=dgv[..., d:])
             grads[f"{i}.w_mix"] = dgv.float().flatten(0, 1).t() @ y1.float().flatten(0, 1)
             g = self.norms[f"{i}.mix"].backward(h1, m1, r1, dgv @ w[f"{i}.w_mix"], dh)
             grads[f"{i}.mix.gamma"], grads[f"{i}.mix.beta"] = g["dgamma"], g["dbeta"]
@@ -152,17 +191,34 @@ class HybridModel:
         d, w = self.d, self.w
         e = w["embed"][tokens].contiguous()
         self.states, h, res = {}, e, None
+        batch, length = tokens.shape
+        if self.attend:
+            # a page table for max_seq_len tokens a sequence, which every block's cache shares
+            page = 16
+            width = -(-self.max_seq_len // page)
+            self.table = torch.arange(batch * width, dtype=torch.int32, device=self.device).view(batch, width)
+            self.lens = torch.full((batch,), length, dtype=torch.int32, device=self.device)
+            seqs = torch.arange(batch, dtype=torch.int32, device=self.device).repeat_interleave(length)
+            pos = torch.arange(length, dtype=torch.int32, device=self.device).repeat(batch)
+            offsets = torch.arange(batch + 1, dtype=torch.int32, device=self.device) * length
+            self.caches = {i: attention.KVCache.empty(batch * width, self.hk, page, self.dh, BF16, self.device)
+                           for i in self.attend}
         for i in range(self.blocks):
             y, h, _, _ = self.norms[f"{i}.mix"].forward(h, res)
             gv = y @ w[f"{i}.w_mix"].t()
-            s, self.states[i] = block.recurrence_forward(gv[..., :d], gv[..., d:])
+            if i in self.attend:
+                q, k, v = self._heads(gv)
+                self.head_norms[i].append(q, k, v, pos, self.caches[i], self.table, seqs)
+                qr, kr = self.head_norms[i].forward(q, k, pos)
+                s = attention.attention_forward(qr, kr, v, offsets=offsets)[0].view(batch, length, d)
+            else:
+                s, self.states[i] = block.recurrence_forward(gv[..., :d], gv[..., d:])
             y, h, _, _ = self.norms[f"{i}.mlp"].forward(h, s @ w[f"{i}.w_out"].t())
             if i in self.fast:
                 self.mlps[i].reset()
                 res = self.mlps[i].prefill(y, e).to(BF16)
             else:
                 res = self.mlps[i].forward(y)
-        batch = tokens.shape[0]
         self.pos = 0
         # the fast-weight layers' chunk in progress
         self.chunk_x = {i: torch.zeros(batch, self.chunk, d, dtype=BF16, device=self.device)
@@ -179,7 +235,12 @@ class HybridModel:
         for i in range(self.blocks):
             y, h, _, _ = self.norms[f"{i}.mix"].forward(h, res)
             gv = y @ w[f"{i}.w_mix"].t()
-            s, _ = block.recurrence_step(gv[:, :d], gv[:, d:], self.states[i], out=self.states[i])
+            if i in self.attend:
+                q, k, v = self._heads(gv)
+                qr = self.head_norms[i].append(q, k, v, self.lens, self.caches[i], self.table)
+                s = attention.attention_step(qr, self.caches[i], self.table, self.lens + 1).view(-1, d)
+            else:
+                s, _ = block.recurrence_step(gv[:, :d], gv[:, d:], self.states[i], out=self.states[i])
             y, h, _, _ = self.norms[f"{i}.mlp"].forward(h, s @ w[f"{i}.w_out"].t())
             if i in self.fast:
                 self.chunk_x[i][:, self.pos] = y
@@ -187,6 +248,8 @@ class HybridModel:
             else:
                 res = self.mlps[i].forward(y)
         self.pos = (self.pos + 1) % self.chunk
+        if self.attend:
+            self.lens += 1
         return self.norms["final"].forward(h, res)[0] @ w["embed"].t()
 
 

@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
   }
   f32x16 acc[CH / 32], x[NT];
   Frag<T> p[KS / 16], v[kAhead];
-  float m, sum, mc = 0.f;
+  float m, sum, base = 0.f, mc = 0.f;  // base: m, or 0 before any key
   const int begin = head.lo / KS * KS;
   constexpr int N = KS / 16 * (CH / 32), E = 16 * NT;
   constexpr int TILE = KS * DP * (int)sizeof(T);
@@ -226,7 +226,8 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
         const float next = fmaxf(m, top);
         f = next == -INFINITY ? 1.f : exp2_((m - next) * c);
         m = next;
-        mc = m == -INFINITY ? 0.f : m * c;
+        base = m == -INFINITY ? 0.f : m;
+        mc = base * c;
         sum *= f;
       }
       // The tile before is added to the values while this one's scores become weights: the
@@ -239,7 +240,9 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
         if (n + kAhead < N) v[n % kAhead] = value(n + kAhead);
 #pragma unroll
         for (int e = E * n / N; e < E * (n + 1) / N; ++e) {
-          float weight = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -mc));
+          // (fp32 as written: a query's only key then has the weight 1 to the bit)
+          float weight = exp2_(sizeof(T) == 4 ? (x[e / 16][e % 16] - base) * c
+                                              : __builtin_fmaf(x[e / 16][e % 16], c, -mc));
           asm volatile("" : "+v"(weight));  // here, not behind the products
           x[e / 16][e % 16] = weight;
           part[e % 4] += weight;
@@ -290,28 +293,44 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
   }
 }
 
-// delta = sum(dy o) of each query and head, and the forward's lse in units of log2: 16
-// lanes a row. A row with an infinite score has no softmax: its gradients are NaN.
-template <typename T>
+// delta = sum(dy o) of each query and head, and the forward's lse in units of log2. A row
+// with an infinite score has no softmax: its gradients are NaN. The sums are the diagonal of
+// a 32 x 32 product of o and dy, so that they are added in the order in which the backward's
+// products add dP = dy V: a query that sees one key, whose o is that key's v, then has
+// dP = delta to the bit, and gradients of zero. A wave takes 32 tokens of one head.
+template <typename T, int DP, int CH>
 __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
-  const int64_t row = (blk::block_id() * 256 + threadIdx.x) / 16;  // token-major
-  const int64_t t = row / a.hq;
-  const int hd = (int)(row - t * a.hq);
-  if (t >= a.n_q) return;
-  const T *o = (const T *)a.o.p + t * a.o.tok_stride + hd * a.o.head_stride;
-  const T *dy = (const T *)a.dy.p + t * a.dy.tok_stride + hd * a.dy.head_stride;
-  float v = 0.f;
-  T x[8], y[8];
-  const int c = 8 * (threadIdx.x & 15);
-  if (c < a.dh) {
-    load_some<T, 8>(o, c, a.dh, x);
-    load_some<T, 8>(dy, c, a.dh, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v += (float)x[e] * (float)y[e];
+  extern __shared__ __align__(1024) char smem[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5, q = l & 31;
+  const int64_t unit = (int64_t)uniform64(blk::block_id()) * 4 + wave;
+  const int64_t t0 = unit / a.hq * 32;
+  const int hd = (int)(unit % a.hq);
+  if (t0 >= a.n_q) return;
+  T *const ot = (T *)smem + wave * 64 * DP, *const yt = ot + 32 * DP;
+  if (a.dh != DP) {
+    clear(ot, 64 * DP, l, 64);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
+  const int left = (int)(a.n_q - t0 < 32 ? a.n_q - t0 : 32);
+  const Copier<T, DP, 32, 1> oc((const T *)a.o.p + t0 * a.o.tok_stride + hd * a.o.head_stride, a.o.tok_stride, a.dh,
+                                0, l);
+  const Copier<T, DP, 32, 1> yc((const T *)a.dy.p + t0 * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride,
+                                a.dh, 0, l);
+  oc.issue(ot, 0, left, a.dh, 0, l, kAsIs);
+  yc.issue(yt, 0, left, a.dh, 0, l, kAsIs);
+  mfma::wait_vm<0>();
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // one wave's own tiles
+  const RowReader<T, DP> rows(ot, l);
+  f32x16 x{};
 #pragma unroll
-  for (int k = 8; k >= 1; k >>= 1) v += __shfl_xor(v, k, 64);
-  if ((threadIdx.x & 15) == 0) {
+  for (int i = 0; i < CH / 16; ++i) x = mma(rows.read(0, i), rows.read(32, i), x);
+  const int64_t t = t0 + q;
+  // row q of column q
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (8 * (i / 4) + i % 4 == (q & ~4)) v = x[i];
+  if ((q >> 2 & 1) == h && q < left) {
     const float lse = a.lse[hd * a.n_q + t];
     a.delta[hd * a.n_q + t] = v;
     a.lse2[hd * a.n_q + t] = lse == INFINITY ? NAN : lse * kLog2e;
@@ -785,10 +804,11 @@ hipError_t attn_backward(const AttnArgs &args, hipStream_t st) {
   a.q_order = order_tiles(a, false, kBlock, a.q_order, st);
   a.k_order = order_tiles(a, true, key_rows<T>(), a.k_order, st);
   const int parts = parts_of(a.hq, a.hk, a.n_q, a.n_k, a.batch);
-  if (a.n_q > 0) k_delta<T><<<blk::grid_of((a.n_q * a.hq + 15) / 16), 256, 0, st>>>(a);
   by_width<T>(a.dh, [&](auto dp, auto ch) {
     constexpr int DP = decltype(dp)::value, CH = decltype(ch)::value;
     const size_t lds = 4 * step_rows<T>() * DP * sizeof(T);
+    if (a.n_q > 0) 
+      k_delta<T, DP, CH><<<blk::grid_of(((a.n_q + 31) / 32 * a.hq + 3) / 4), 256, 4 * 64 * DP * sizeof(T), st>>>(a);
     if (a.n_k > 0) {
       constexpr int KB = key_rows<T>();
       const int64_t tiles = tiles_of(a.n_k, KB, a.batch);

@@ -349,6 +349,23 @@ def test_prompt_what_is_not_seen_does_not_count(window, dtype, value):
             assert not torch.isfinite(got[x][seen_by][:, 1]).all(-1).any(), (t, x)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("hq,hk,dh", [(4, 2, 128), (2, 1, 64), (3, 3, 72), (2, 2, 33)])
+def test_prompt_one_key(hq, hk, dh, dtype):
+    """A query that sees one key: o is its v and the gradients through the softmax are zero, to
+    the bit, in sequences of one token, behind a window of one and in the first row."""
+    q, k, v, dy, lq, lk, how = prompt(([1] * 5 + [70], None, hq, hk, dh, True, 1), dtype)
+    o, lse = A.attention_forward(q, k, v, **how)
+    assert torch.equal(o, v.repeat_interleave(hq // hk, 1))
+    got = A.attention_backward(q, k, v, o, lse, dy, **how)
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+    how["window"] = 0
+    o, lse = A.attention_forward(q, k, v, **how)
+    got = A.attention_backward(q, k, v, o, lse, dy, **how)
+    assert (got["dq"][:6] == 0).all() and (got["dk"][:5] == 0).all()
+    assert torch.equal(o[:6], v[:6].repeat_interleave(hq // hk, 1))
+
+
 def test_prompt_large_scores():
     """Scores far from zero, rising along the keys: the running maximum moves all the time."""
     n, dh = 700, 64

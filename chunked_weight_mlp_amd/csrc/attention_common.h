@@ -310,16 +310,20 @@ struct Copier {
   static constexpr int RPI = 64 / L::NP;              // rows an instruction fills
   static constexpr int NI = ROWS / (RPI * WAVES);     // instructions a wave
   static_assert(ROWS % (RPI * WAVES) == 0, "rows must split evenly over the waves");
+  // Instructions' rows that lie a multiple of 16 apart have the same swizzle: one register
+  // then holds the lane's offset for all of them.
+  static constexpr int STEP = WAVES * RPI, NO = STEP % 16 == 0 ? 1 : NI;
   const T *base;
   int64_t stride;
-  uint32_t offset[NI];  // of this lane's piece from the tile's first row
+  uint32_t offset[NO];  // of this lane's piece from the tile's first row
   bool direct;
-  __device__ __forceinline__ Copier(const T *p, int64_t tok_stride, int dh, int wave, int lane)
+  // shift: what issue()'s shift is a multiple of
+  __device__ __forceinline__ Copier(const T *p, int64_t tok_stride, int dh, int wave, int lane, int64_t shift = 0)
       : base(uniform(p)), stride(tok_stride) {
     direct = dh % L::PE == 0 && (uintptr_t)p % 16 == 0 && tok_stride * sizeof(T) % 16 == 0 &&
-             tok_stride < (1 << 30) / ROWS / (int)sizeof(T);
+             shift * sizeof(T) % 16 == 0 && tok_stride < (1 << 30) / ROWS / (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    for (int i = 0; i < NO; ++i) {
       const int r = row(i, wave, lane);
       offset[i] = (r * (uint32_t)stride + piece(r, lane) * L::PE) * sizeof(T);
     }
@@ -330,13 +334,14 @@ struct Copier {
   __device__ static __forceinline__ int piece(int r, int lane) { return (lane % L::NP) ^ L::swizzle(r); }
   // wave must be wave-uniform
   __device__ __forceinline__ void issue(T *tile, int first, int end, int dh, int wave, int lane,
-                                        int fix) const {
+                                        int fix, int64_t shift = 0) const {
+    const T *const from_base = base + shift;
     if (direct && fix == kAsIs) {
-      const T *const p0 = base + (int64_t)first * stride;
+      const T *const p0 = from_base + (int64_t)first * stride;
       const bool over = first + ROWS > end;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        uint32_t at = offset[i];
+        uint32_t at = NO == 1 ? offset[0] + i * (STEP * (uint32_t)stride * (uint32_t)sizeof(T)) : offset[i % NO];
         if (over) {
           const int r = row(i, wave, here(lane));
           at -= max(0, first + r - (end - 1)) * (uint32_t)stride * (uint32_t)sizeof(T);
@@ -351,7 +356,7 @@ struct Copier {
         const int r = row(i, wave, ln), p = ln % L::NP;
         const int from = first + r < end ? first + r : end - 1;
         T v[L::PE];
-        load_some<T, L::PE>(base + from * stride, p * L::PE, width, v);
+        load_some<T, L::PE>(from_base + from * stride, p * L::PE, width, v);
 #pragma unroll
         for (int e = 0; e < L::PE; ++e) tile[L::at(r, p) + e] = fixed(v[e], fix);
       }

@@ -548,17 +548,17 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
   const Copier<T, DP, KB, kWaves> vc((const T *)a.v.p + rk.start * a.v.tok_stride + kv * a.v.head_stride,
                                      a.v.tok_stride, a.dh, wave, l);
   vc.issue(vt, first, lk, a.dh, wave, l, kAsIs);
+  const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + (int64_t)kv * group * a.q.head_stride, a.q.tok_stride,
+             a.dh, wave, l, a.q.head_stride);
+  const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + (int64_t)kv * group * a.dy.head_stride,
+             a.dy.tok_stride, a.dh, wave, l, a.dy.head_stride);
   const auto issue = [&](int g, int i0, int b, int fix) __attribute__((always_inline)) {
-    const int hd = kv * group + g, ln = here(l);  // no registers for the copies' offsets
     T *const t = buf + b * 2 * QS * DP;
-    const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + hd * a.q.head_stride, a.q.tok_stride, a.dh, wave, ln);
-    const C yc((const T *)a.dy.p + rq.start * a.dy.tok_stride + hd * a.dy.head_stride, a.dy.tok_stride, a.dh, wave,
-               ln);
-    qc.issue(t, i0, lq, a.dh, wave, ln, fix);
-    yc.issue(t + QS * DP, i0, lq, a.dh, wave, ln, fix);
+    qc.issue(t, i0, lq, a.dh, wave, l, fix, g * a.q.head_stride);
+    yc.issue(t + QS * DP, i0, lq, a.dh, wave, l, fix, g * a.dy.head_stride);
     if (wave < 2) {
-      const float *src = (wave ? a.delta : a.lse2) + hd * a.n_q + rq.start;
-      copy_to_lds<4>(uniform(src), 4 * (uint32_t)min(i0 + ln, lq - 1), stats + (2 * b + wave) * 64);
+      const float *src = (wave ? a.delta : a.lse2) + (kv * group + g) * a.n_q + rq.start;
+      copy_to_lds<4>(uniform(src), 4 * (uint32_t)min(i0 + here(l), lq - 1), stats + (2 * b + wave) * 64);
     }
   };
   f32x16 dk[NK][ND], dv[NK][ND];

@@ -163,6 +163,12 @@ def _heads(name, t, shape, dtype, device):
     return Heads(t.data_ptr(), tok, head)
 
 
+def _int32(name, v):
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise _invalid(f"{name}={v} does not fit 32 bits")
+    return v
+
+
 def _three(name, t):
     if t.dim() != 3 or 0 in t.shape[1:]:
         raise _invalid(f"{name} must be [tokens, heads, head_dim], the last two > 0")
@@ -183,7 +189,7 @@ class KVCache:
         self.v = _dense("v", v, k.shape, k.dtype, k.device)
         self.pages, self.k_heads, self.page_size, self.head_dim = k.shape
         self.dtype, self.device = k.dtype, k.device
-        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, self.k_heads,
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), _int32("pages", self.pages), self.page_size, self.k_heads,
                                 self.head_dim, dt)
         self._ref = ctypes.byref(self.desc)
 
@@ -332,7 +338,7 @@ def _attention(q, k, v, offsets, k_offsets, causal, window, scale):
         _dense("k_offsets", k_offsets, offsets.shape, torch.int32, dev)
         batch = offsets.numel() - 1
     scale = dh ** -0.5 if scale is None else scale
-    return AttentionDesc(hq, hk, dh, batch, bool(causal), window, dt, scale, n, nk, _p(offsets),
+    return AttentionDesc(hq, hk, dh, batch, bool(causal), _int32("window", window), dt, scale, n, nk, _p(offsets),
                          _p(k_offsets)), views
 
 
@@ -396,7 +402,7 @@ def attention_step(q, cache, table, lens, window: int = 0, scale=None, stream=No
     _dense("lens", lens, (n,), torch.int32, dev)
     st = _on(dev)
     o = torch.empty_like(q, memory_format=_DENSE)
-    desc = ctypes.byref(StepDesc(hq, window, dh ** -0.5 if scale is None else scale))
+    desc = ctypes.byref(StepDesc(hq, _int32("window", window), dh ** -0.5 if scale is None else scale))
     need = load().ipttt_attention_step_workspace_bytes(desc, cache._ref, tab)
     ws = _temp(need, dev)
     _check(load().ipttt_attention_step(desc, qh, cache._ref, tab, lens.data_ptr(),

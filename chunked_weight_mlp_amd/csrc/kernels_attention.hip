@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
   const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, kBlock, tiles - 1 - w.rank, l);
   const Rows rq{at.q_start, at.lq}, rk{at.k_start, at.lk};
   const int first = at.first;
-  if (first >= rq.len) return;
+  if (first < 0 || first >= rq.len) return;  // (below 0: offsets that fall)
   const int lq = rq.len, lk = rk.len;
   const int q0 = first + kRows * wave, qi = q0 + (l & 31);
   const int qr = min(qi, lq - 1);
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
   const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, kBlock, tiles - 1 - w.rank, l);
   const Rows rq{at.q_start, at.lq}, rk{at.k_start, at.lk};
   const int first = at.first;
-  if (first >= rq.len) return;
+  if (first < 0 || first >= rq.len) return;  // (below 0: offsets that fall)
   const int lq = rq.len, lk = rk.len;
   const int q0 = first + kRows * wave, qi = q0 + (l & 31);
   const int64_t qr = rq.start + min(qi, lq - 1);
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
   const TilePlace place = a.k_order ? a.k_order[id / a.hk] : tile_place(a, true, KB, id / a.hk, l);
   const Rows rq{place.q_start, place.lq}, rk{place.k_start, place.lk};
   const int first = place.first;
-  if (first >= rk.len) return;
+  if (first < 0 || first >= rk.len) return;
   const int lq = rq.len, lk = rk.len, group = a.hq / a.hk;
   const int k0 = first + kRows * NK * wave;
   // the queries that see key j: [from(j), to(j))

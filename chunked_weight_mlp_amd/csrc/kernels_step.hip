@@ -67,8 +67,7 @@ __device__ __forceinline__ Span span_of(const StepArgs &a, int b) {
   s.hi = min(max(a.lens[b], 0), most);
   s.lo = a.window > 0 ? max(0, s.hi - a.window) : 0;
   s.first = s.lo / kKeys;
-  s.n = (s.hi + kKeys - 1) / kKeys - s.first;
-  if (s.hi == 0) s.n = 0;
+  s.n = s.hi == 0 ? 0 : (s.hi - 1) / kKeys + 1 - s.first;
   return s;
 }
 

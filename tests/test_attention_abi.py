@@ -293,6 +293,8 @@ def test_tensor_refusals_on_the_host():
     refused(INV, A.attention_forward, q, k, k, off[:0], off[:0])
     refused(INV, A.attention_forward, q, k, k, off.long())
     refused(UNS, A.attention_forward, q.half(), k.half(), k.half())
+    for w in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        refused(INV, lambda: A.attention_forward(q, k, k, window=w), text="32 bits")
     refused(INV, A.attention_backward, q, k, k, q, torch.ones(3, 2), q, text="lse")
     refused(INV, A.attention_backward, q, k, k, q[:2], torch.ones(2, 3), q)
 

@@ -427,9 +427,22 @@ def test_prompt_offsets_that_are_no_offsets():
     o, _ = A.attention_forward(q, k, v, offsets=off)
     want, _ = A.attention_forward(q, k, v, offsets=torch.tensor([0, 30, 50], dtype=torch.int32, device=DEV))
     assert torch.equal(o, want)
-    off = torch.tensor([0, 40, 20, -5], dtype=torch.int32, device=DEV)
-    A.attention_forward(q, k, v, offsets=off)
-    torch.cuda.synchronize()
+    n = 2000
+    q, k, v = rand((n, 2, 64), 1, BF16), rand((n, 1, 64), 2, BF16), rand((n, 1, 64), 3, BF16)
+    for off in ([0, 40, 20, -5], [0, 1000, 0, 1000], [0, 2000, 1000, 3000, 0, 1], [5, 4, 3, 2, 1, 0]):
+        off = torch.tensor(off, dtype=torch.int32, device=DEV)
+        o, lse = A.attention_forward(q, k, v, offsets=off)
+        A.attention_backward(q, k, v, o, lse, q, offsets=off)
+        torch.cuda.synchronize()
+
+
+def test_prompt_no_sequence():
+    """Offsets of no sequence: every row is behind the last one."""
+    q, k = rand((300, 2, 64), 1, BF16), rand((300, 1, 64), 2, BF16)
+    off = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, lse = A.attention_forward(q, k, k, offsets=off)
+    assert (o == 0).all() and (lse == -math.inf).all()
+    assert all((t == 0).all() for t in A.attention_backward(q, k, k, o, lse, q, offsets=off).values())
 
 
 def test_prompt_empty():
@@ -514,6 +527,18 @@ def test_step_pages_that_are_none(dtype):
     far = torch.tensor([100, 2 ** 31 - 1, 1000, -3], dtype=torch.int32, device=DEV)
     o = A.attention_step(q, cache, table, far)
     assert torch.equal(o[0], A.attention_step(q, cache, table, n)[0]) and (o[1] == 0).all() and (o[3] == 0).all()
+
+
+def test_step_at_the_last_place_that_32_bits_count():
+    """Lengths to 2^31 - 2 through a table that names the same pages again and again."""
+    page, width, dh = 49981, 42966, 64      # their product is 2^31 - 2
+    cache = A.KVCache(rand((3, 1, page, dh), 1, BF16), rand((3, 1, page, dh), 2, BF16))
+    table = (torch.arange(width, device=DEV) % 3).to(torch.int32)[None].repeat(2, 1)
+    n = torch.tensor([page * width, 2 ** 31 - 40], dtype=torch.int32, device=DEV)
+    q = rand((2, 4, dh), 3, BF16, 2.0)
+    for window in (1, 31, 1000):
+        want, bound = R.step(q, cache.k, cache.v, table, n, window)
+        within("step far", A.attention_step(q, cache, table, n, window=window), want, bound)
 
 
 def test_step_lse():

@@ -1,4 +1,16 @@
 // Attention over packed prompts (gfx950): forward and backward.
+//
+// A block of four waves takes 128 queries of one head (the forward, dq) or 128 keys of one
+// key head (dk, dv) and goes over the other side in tiles that are copied into LDS a step
+// ahead. Two blocks share a CU, so that one's products run beside the other's softmax; the
+// 256 registers that leaves a wave are what its sums, its own rows and the operands in
+// flight need (128 channels bf16: forward 233, dq 250, dk and dv all), and none may go to
+// memory: a reload waits for every copy in flight before it. Products and the arithmetic
+// that does not wait for them are interleaved in the source; sched_barrier keeps the order.
+//
+// What bounds it: of the forward's cycles the matrix cores are busy half and the vector units
+// issue in half (32768 tokens of 32/8 heads of 128 bf16: 8.5 ms, 1037 TFLOP/s; 16384 of
+// 16/8: 1.2 ms, 918, and the backward 3.74 ms, 735).
 #include "attention_common.h"
 
 namespace ipttt {
@@ -45,9 +57,10 @@ __device__ __forceinline__ Work work_of(const AttnArgs &a) {
   w.rank = x / group;
   return w;
 }
-// Tile number `tile` of M queries (keys); first is behind the sequence's end where the tile
+// Tile number `tile` of queries (keys); first is behind the sequence's end where the tile
 // is empty.
-__device__ __forceinline__ TilePlace tile_place(const AttnArgs &a, bool keys, int M, int64_t tile, int lane) {
+__device__ __forceinline__ TilePlace tile_place(const AttnArgs &a, bool keys, int64_t tile, int lane) {
+  constexpr int M = kBlock;
   const int32_t *off = keys ? a.k_off : a.q_off;
   const int64_t n = keys ? a.n_k : a.n_q;
   const int s = __builtin_amdgcn_readfirstlane(sequence_of(off, a.batch, n, M, tile, lane));
@@ -62,15 +75,17 @@ __device__ __forceinline__ TilePlace tile_place(const AttnArgs &a, bool keys, in
 // Blocks start in the order of their numbers as others end, so the longest have to come
 // first. Within one sequence that is known; tiles of several are sorted by how much they
 // see, at most kOrderTiles of kOrderBatch sequences (more are so many that their order
-// matters little), and only if they do not all run at once.
+// matters little), and only if they do not all run at once. (16384 tokens in six documents,
+// 16/8 heads of 128 bf16: forward 290 us as they come, 272 sorted; dq 388, 364. Sorting 4 to 7.)
 constexpr int kOrderTiles = 2048, kOrderBatch = 1024;
 inline bool ordered(int batch, int64_t tiles, int heads) {
   return batch > 1 && batch <= kOrderBatch && tiles <= kOrderTiles && tiles * heads > 512;
 }
 
 // order[rank] = a tile's place, by falling numbers of keys (of queries for tiles of keys)
-// that its M rows see (are seen by), empty tiles last.
-__global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int tiles, TilePlace *order) {
+// that its rows see (are seen by), empty tiles last.
+__global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int tiles, TilePlace *order) {
+  constexpr int M = kBlock;
   __shared__ int mine[kOrderBatch + 1], other[kOrderBatch + 1], work[kOrderTiles];
   const int32_t *off = keys ? a.k_off : a.q_off, *oth = keys ? a.q_off : a.k_off;
   const int64_t n = keys ? a.n_k : a.n_q, no = keys ? a.n_q : a.n_k;
@@ -119,7 +134,8 @@ __global__ __launch_bounds__(256) void k_order(AttnArgs a, bool keys, int M, int
 template <typename T>
 constexpr int step_rows() { return sizeof(T) == 2 ? 64 : 32; }
 // Blocks a CU that the registers of the forward and of dq must allow: operands of 128 fp32
-// channels take twice the registers, and their products eight times as long.
+// channels take twice the registers, and their products eight times as long. (4096 tokens of 8
+// heads of 128 fp32: 902 us with two blocks, whose registers go to memory, 663 with one.)
 template <typename T, int DP>
 constexpr int blocks_a_cu() { return sizeof(T) == 4 && DP > 64 ? 1 : 2; }
 constexpr int kAhead = 4;  // operands read from LDS ahead of their products
@@ -133,7 +149,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const Work w = work_of(a);
   if (w.rank >= tiles) return;
-  const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, kBlock, tiles - 1 - w.rank, l);
+  const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, tiles - 1 - w.rank, l);
   const Rows rq{at.q_start, at.lq}, rk{at.k_start, at.lk};
   const int first = at.first;
   if (first < 0 || first >= rq.len) return;  // (below 0: offsets that fall)
@@ -347,7 +363,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const Work w = work_of(a);
   if (w.rank >= tiles) return;
-  const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, kBlock, tiles - 1 - w.rank, l);
+  const TilePlace at = a.q_order ? a.q_order[w.rank] : tile_place(a, false, tiles - 1 - w.rank, l);
   const Rows rq{at.q_start, at.lq}, rk{at.k_start, at.lk};
   const int first = at.first;
   if (first < 0 || first >= rq.len) return;  // (below 0: offsets that fall)
@@ -494,34 +510,35 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
 }
 
 // dk and dv: a block's keys, over the queries of the group's heads that see them. A wave
-// holds 32 NK keys: their sums and K rows in registers, their V rows in LDS, since both do
-// not fit beside the sums. Each operand read from LDS then serves NK products, which is why
-// a wave has a SIMD to itself: at 32 keys a wave LDS has as much to do as the matrix cores.
+// holds 32 keys: their sums and K rows in registers, their V rows in LDS, since both do not
+// fit beside the sums. (64 keys a wave halve the LDS reads of a product, but leave a SIMD one
+// wave, which does not cover its own waits: 1090 us for 16384 tokens in six documents of 16/8
+// heads of 128 bf16, where this takes 590.)
 // For 32 queries the products are, with what the vector units do beside them,
 //   scores S = Q K^T;   dP = dY V^T beside P = exp(S - lse);
 //   dV += dY^T P beside dS = P (dP - delta);   dK += Q^T dS.
 // Where the key tiles are few, `parts` blocks share a tile's steps (part blockIdx.z) and
 // leave partial sums, which k_dkv_join adds up.
-template <typename T, int DP, int CH, int NK>
+template <typename T, int DP, int CH>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(AttnArgs a, int64_t tiles, int parts) {
   constexpr int QS = 32, NT = QS / 32, STAGE = 2 * QS * DP * (int)sizeof(T);
-  constexpr int KB = NK * kBlock, ND = CH / 32, S = CH / 16;
+  constexpr int ND = CH / 32, S = CH / 16;
   constexpr int AHEAD = 3;  // operands read from LDS ahead of their products
   using C = Copier<T, DP, QS, kWaves>;
   extern __shared__ __align__(1024) char smem[];
   T *const buf = (T *)smem;                            // [2][q tile, dy tile]
   T *const vt = buf + 4 * QS * DP;                     // the block's V rows
-  float *const stats = (float *)(vt + KB * DP);        // [2][lse, delta][64]
+  float *const stats = (float *)(vt + kBlock * DP);    // [2][lse, delta][64]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, h = l >> 5;
   const int64_t id = blk::block_id();
   const int kv = (int)(id % a.hk);
   if (id / a.hk >= tiles) return;
-  const TilePlace place = a.k_order ? a.k_order[id / a.hk] : tile_place(a, true, KB, id / a.hk, l);
+  const TilePlace place = a.k_order ? a.k_order[id / a.hk] : tile_place(a, true, id / a.hk, l);
   const Rows rq{place.q_start, place.lq}, rk{place.k_start, place.lk};
   const int first = place.first;
   if (first < 0 || first >= rk.len) return;
   const int lq = rq.len, lk = rk.len, group = a.hq / a.hk;
-  const int k0 = first + kRows * NK * wave;
+  const int k0 = first + kRows * wave;
   // the queries that see key j: [from(j), to(j))
   const int off = lk - lq;
   const auto from = [&](int j) { return a.causal ? max(0, j - off) : 0; };
@@ -529,24 +546,23 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
     if (!a.causal || a.window <= 0) return lq;
     return (int)max((int64_t)0, min((int64_t)lq, (int64_t)j + a.window - off));
   };
-  Frag<T> k[NK][S];
-#pragma unroll
-  for (int j = 0; j < NK; ++j) {
-    const int kj = k0 + 32 * j + (l & 31);
+  Frag<T> k[S];
+  {
+    const int kj = k0 + (l & 31);
     const T *kp = (const T *)a.k.p + (rk.start + min(kj, lk - 1)) * a.k.tok_stride + kv * a.k.head_stride;
 #pragma unroll
-    for (int i = 0; i < S; ++i) k[j][i] = with_sign<T>(load_frag<T>(kp, i, h, a.dh), a.scale);
+    for (int i = 0; i < S; ++i) k[i] = with_sign<T>(load_frag<T>(kp, i, h, a.dh), a.scale);
   }
-  const int q_from = from(first), q_to = to(min(first + KB, lk) - 1);
-  const int all_from = from(k0 + kRows * NK - 1), all_to = k0 + kRows * NK <= lk ? to(k0) : 0;
+  const int q_from = from(first), q_to = to(min(first + kBlock, lk) - 1);
+  const int all_from = from(k0 + kRows - 1), all_to = k0 + kRows <= lk ? to(k0) : 0;
   const int begin = q_from / QS * QS, steps = q_to > begin ? (q_to - begin + QS - 1) / QS : 0;
   const float c = log2_scale(a.scale);
   if (a.dh != DP) {
-    clear(buf, (4 * QS + KB) * DP, tid, kThreads);
+    clear(buf, (4 * QS + kBlock) * DP, tid, kThreads);
     __syncthreads();
   }
-  const Copier<T, DP, KB, kWaves> vc((const T *)a.v.p + rk.start * a.v.tok_stride + kv * a.v.head_stride,
-                                     a.v.tok_stride, a.dh, wave, l);
+  const Copier<T, DP, kBlock, kWaves> vc((const T *)a.v.p + rk.start * a.v.tok_stride + kv * a.v.head_stride,
+                                         a.v.tok_stride, a.dh, wave, l);
   vc.issue(vt, first, lk, a.dh, wave, l, kAsIs);
   const C qc((const T *)a.q.p + rq.start * a.q.tok_stride + (int64_t)kv * group * a.q.head_stride, a.q.tok_stride,
              a.dh, wave, l, a.q.head_stride);
@@ -561,12 +577,10 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
       copy_to_lds<4>(uniform(src), 4 * (uint32_t)min(i0 + here(l), lq - 1), stats + (2 * b + wave) * 64);
     }
   };
-  f32x16 dk[NK][ND], dv[NK][ND];
+  f32x16 dk[ND], dv[ND];
   for (int fix = kAsIs;; ++fix) {
 #pragma unroll
-    for (int j = 0; j < NK; ++j)
-#pragma unroll
-      for (int d = 0; d < ND; ++d) dk[j][d] = dv[j][d] = f32x16{};
+    for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f32x16{};
     int cur = 0;
     RowReader<T, DP> rows(buf, l);
     ColReader<T, DP> cols(buf, l);
@@ -583,23 +597,20 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
       mfma::lds_barrier();
       const float *const lse = stats + 2 * cur * 64 + 4 * h, *const delta = lse + 64;
       // from this step's tiles to the wave's V rows
-      const int to_v = (2 - cur) * STAGE + kRows * NK * wave * DP * (int)sizeof(T);
+      const int to_v = (2 - cur) * STAGE + kRows * wave * DP * (int)sizeof(T);
       cur ^= 1;
       const int i0 = queries_of(n);
       if (++n == steps) n = 0, ++g;
       if (at + 1 < stop) issue(g, queries_of(n), cur, fix);
       const bool whole = i0 >= all_from && i0 + QS <= all_to;
-      // f(e, whether the lane's key of tile j is seen by the query of result e), for e < 16 NK
+      // f(e, whether the lane's key is seen by the query of result e), for e < 16
       const auto each_seen = [&](int t, auto f) __attribute__((always_inline)) {
         const int ln = here(l);
+        const int kj = k0 + (ln & 31), first = from(kj);
+        const unsigned queries = kj < lk ? max(0, to(kj) - first) : 0;
+        const int rel = i0 + 32 * t + 4 * (ln >> 5) - first;
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          const int kj = k0 + 32 * j + (ln & 31), first = from(kj);
-          const unsigned queries = kj < lk ? max(0, to(kj) - first) : 0;
-          const int rel = i0 + 32 * t + 4 * (ln >> 5) - first;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f(16 * j + i, (unsigned)(rel + 8 * (i / 4) + i % 4) < queries);
-        }
+        for (int i = 0; i < 16; ++i) f(i, (unsigned)(rel + 8 * (i / 4) + i % 4) < queries);
       };
       // the operands of the products in their order: S steps of S and dP, 2 ND of dV and dK
       constexpr int LEN = 2 * S + 4 * ND;
@@ -610,7 +621,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
         const int e = (o - 2 * S) % (2 * ND), q = (o - 2 * S) / (2 * ND);
         return cols.read((q ? 0 : QS) + r + 16 * (e / ND), e % ND);
       };
-      Frag<T> f[AHEAD], vb[NK];
+      Frag<T> f[AHEAD], vb;
 #pragma unroll
       for (int m = 0; m < AHEAD; ++m) f[m] = operand(m);
 #pragma unroll
@@ -621,100 +632,76 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 2 : 1)) void k_dkv(Attn
           if (m + AHEAD < NT * LEN) f[m % AHEAD] = operand(m + AHEAD);
           __builtin_amdgcn_sched_barrier(0);
         };
-        f32x16 x[NK], y[NK];
+        f32x16 x{}, y{};
         f32x4v st;
         // a statistic of the rows of results e .. e + 3
         const auto stat = [&](const float *p, int e) __attribute__((always_inline)) {
-          return *(const f32x4v *)(p + 32 * t + 8 * (e % 16 / 4));
+          return *(const f32x4v *)(p + 32 * t + 8 * (e / 4));
         };
-#pragma unroll
-        for (int j = 0; j < NK; ++j) x[j] = y[j] = f32x16{};
-#pragma unroll
-        for (int j = 0; j < NK; ++j) vb[j] = rows.read_from(to_v, 32 * j, 0);
+        vb = rows.read_from(to_v, 0, 0);
 #pragma unroll
         for (int o = 0; o < S; ++o) {
-#pragma unroll
-          for (int j = 0; j < NK; ++j) x[j] = mma(f[(m0 + o) % AHEAD], k[j][o], x[j]);
+          x = mma(f[(m0 + o) % AHEAD], k[o], x);
           refill(m0 + o);
         }
-        constexpr int E = 16 * NK;
 #pragma unroll
         for (int o = 0; o < S; ++o) {
+          y = mma(f[(m0 + S + o) % AHEAD], vb, y);
+          if (o + 1 < S) vb = rows.read_from(to_v, 0, o + 1);
 #pragma unroll
-          for (int j = 0; j < NK; ++j) y[j] = mma(f[(m0 + S + o) % AHEAD], vb[j], y[j]);
-          if (o + 1 < S) {
-#pragma unroll
-            for (int j = 0; j < NK; ++j) vb[j] = rows.read_from(to_v, 32 * j, o + 1);
-          }
-#pragma unroll
-          for (int e = E * o / S; e < E * (o + 1) / S; ++e) {
-            if (e % 4 == 0 || e == E * o / S) st = stat(lse, e);
-            float p = exp2_(__builtin_fmaf(x[e / 16][e % 16], c, -st[e % 4]));
+          for (int e = 16 * o / S; e < 16 * (o + 1) / S; ++e) {
+            if (e % 4 == 0 || e == 16 * o / S) st = stat(lse, e);
+            float p = exp2_(__builtin_fmaf(x[e], c, -st[e % 4]));
             asm volatile("" : "+v"(p));  // here, not behind the products
-            x[e / 16][e % 16] = p;
+            x[e] = p;
           }
           refill(m0 + S + o);
         }
         if (!whole)
           each_seen(t, [&](int e, bool ok) __attribute__((always_inline)) {
-            if (!ok) x[e / 16][e % 16] = 0.f;
+            if (!ok) x[e] = 0.f;
           });
         if (fix == kCount)
-          each_seen(t, [&](int e, bool ok) __attribute__((always_inline)) { x[e / 16][e % 16] = ok ? 1.f : 0.f; });
-        Frag<T> w[NK][2];
-#pragma unroll
-        for (int j = 0; j < NK; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) w[j][i] = as_operand<T>(x[j], i);
+          each_seen(t, [&](int e, bool ok) __attribute__((always_inline)) { x[e] = ok ? 1.f : 0.f; });
+        Frag<T> w[2] = {as_operand<T>(x, 0), as_operand<T>(x, 1)};
 #pragma unroll
         for (int o = 0; o < 2 * ND; ++o) {
+          dv[o % ND] = mma(f[(m0 + 2 * S + o) % AHEAD], w[o / ND], dv[o % ND]);
 #pragma unroll
-          for (int j = 0; j < NK; ++j) dv[j][o % ND] = mma(f[(m0 + 2 * S + o) % AHEAD], w[j][o / ND], dv[j][o % ND]);
-#pragma unroll
-          for (int e = E * o / (2 * ND); e < E * (o + 1) / (2 * ND); ++e) {
-            if (e % 4 == 0 || e == E * o / (2 * ND)) st = stat(delta, e);
-            float ds = x[e / 16][e % 16] * (y[e / 16][e % 16] - st[e % 4]);
+          for (int e = 16 * o / (2 * ND); e < 16 * (o + 1) / (2 * ND); ++e) {
+            if (e % 4 == 0 || e == 16 * o / (2 * ND)) st = stat(delta, e);
+            float ds = x[e] * (y[e] - st[e % 4]);
             asm volatile("" : "+v"(ds));
-            y[e / 16][e % 16] = ds;
+            y[e] = ds;
           }
           refill(m0 + 2 * S + o);
         }
         if (!whole)
           each_seen(t, [&](int e, bool ok) __attribute__((always_inline)) {
-            if (!ok) y[e / 16][e % 16] = 0.f;
+            if (!ok) y[e] = 0.f;
           });
-#pragma unroll
-        for (int j = 0; j < NK; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) w[j][i] = as_operand<T>(y[j], i);
+        w[0] = as_operand<T>(y, 0);
+        w[1] = as_operand<T>(y, 1);
 #pragma unroll
         for (int o = 0; o < 2 * ND; ++o) {
-#pragma unroll
-          for (int j = 0; j < NK; ++j)
-            dk[j][o % ND] = mma(f[(m0 + 2 * S + 2 * ND + o) % AHEAD], w[j][o / ND], dk[j][o % ND]);
+          dk[o % ND] = mma(f[(m0 + 2 * S + 2 * ND + o) % AHEAD], w[o / ND], dk[o % ND]);
           refill(m0 + 2 * S + 2 * ND + o);
         }
       }
       rows.move(cur ? STAGE : -STAGE);
       cols.move(cur ? STAGE : -STAGE);
     }
-    bool ok = true;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) ok &= all_finite(dk[j]) && all_finite(dv[j]);
-    if (fix == kAsIs && !__syncthreads_and(ok)) continue;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) {
-      const int kj = k0 + 32 * j + here(l & 31);
-      if (kj < lk) {
-        const int64_t kr = rk.start + kj;
-        if (parts > 1) {
-          float *const pk = a.part + ((((int64_t)blockIdx.z * a.n_k + kr) * a.hk + kv) * 2) * a.dh;
-          store_row<float, CH>(pk, dk[j], a.scale, h, a.dh, kAsIs);
-          store_row<float, CH>(pk + a.dh, dv[j], 1.f, h, a.dh, fix);
-          continue;
-        }
-        store_row<T, CH>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk[j], a.scale, h, a.dh, kAsIs);
-        store_row<T, CH>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv[j], 1.f, h, a.dh, fix);
+    if (fix == kAsIs && !__syncthreads_and(all_finite(dk) && all_finite(dv))) continue;
+    const int kj = k0 + here(l & 31);
+    if (kj < lk) {
+      const int64_t kr = rk.start + kj;
+      if (parts > 1) {
+        float *const pk = a.part + ((((int64_t)blockIdx.z * a.n_k + kr) * a.hk + kv) * 2) * a.dh;
+        store_row<float, CH>(pk, dk, a.scale, h, a.dh, kAsIs);
+        store_row<float, CH>(pk + a.dh, dv, 1.f, h, a.dh, fix);
+      } else {
+        store_row<T, CH>((T *)a.dk.p + kr * a.dk.tok_stride + kv * a.dk.head_stride, dk, a.scale, h, a.dh, kAsIs);
+        store_row<T, CH>((T *)a.dv.p + kr * a.dv.tok_stride + kv * a.dv.head_stride, dv, 1.f, h, a.dh, fix);
       }
     }
     if (fix != kCount) break;
@@ -736,7 +723,7 @@ __global__ __launch_bounds__(256) void k_dkv_join(AttnArgs a, int parts) {
 }
 
 // f(channels a row has in LDS, channels that are computed): rows of 65 to 96 channels leave
-// out a quarter of the products.
+// out a quarter of the products (16384 tokens of 16/8 heads of 96 bf16: 1.20 -> 0.93 ms).
 template <typename T, class F>
 void by_width(int dh, F f) {
   using std::integral_constant;
@@ -745,12 +732,9 @@ void by_width(int dh, F f) {
   else f(integral_constant<int, 128>(), integral_constant<int, 128>());
 }
 
-// Rows of a tile of keys.
-template <typename T>
-constexpr int key_rows() { return kBlock; }
-
 // Blocks that share a tile of keys: as many as bring the grid to two blocks a CU, while each
-// has four steps of 32 queries of one head or more.
+// has four steps of 32 queries of one head or more. (512 tokens of 8/2 heads of 128 bf16, 12
+// blocks of their own: backward 142 us, shared 58.)
 int parts_of(int hq, int hk, int64_t n_q, int64_t n_k, int batch) {
   const int64_t blocks = tiles_of(n_k, kBlock, batch) * hk;
   if (blocks >= 384 || n_k == 0) return 1;
@@ -759,11 +743,11 @@ int parts_of(int hq, int hk, int64_t n_q, int64_t n_k, int batch) {
   return (int)(p < most ? (p < 1 ? 1 : p) : most < 1 ? 1 : most);
 }
 
-// Fills the order of tiles of M rows, or says that it is not used.
-TilePlace *order_tiles(const AttnArgs &a, bool keys, int M, TilePlace *order, hipStream_t st) {
-  const int64_t tiles = tiles_of(keys ? a.n_k : a.n_q, M, a.batch);
+// Fills the order of tiles, or says that it is not used.
+TilePlace *order_tiles(const AttnArgs &a, bool keys, TilePlace *order, hipStream_t st) {
+  const int64_t tiles = tiles_of(keys ? a.n_k : a.n_q, kBlock, a.batch);
   if (!ordered(a.batch, tiles, keys ? a.hk : a.hq)) return nullptr;
-  k_order<<<(int)(tiles + 255) / 256, 256, 0, st>>>(a, keys, M, (int)tiles, order);
+  k_order<<<(int)(tiles + 255) / 256, 256, 0, st>>>(a, keys, (int)tiles, order);
   return order;
 }
 
@@ -788,7 +772,7 @@ size_t attn_k_order(const ipttt_attention &d) {
 template <typename T>
 hipError_t attn_forward(const AttnArgs &args, hipStream_t st) {
   AttnArgs a = args;
-  a.q_order = order_tiles(a, false, kBlock, a.q_order, st);
+  a.q_order = order_tiles(a, false, a.q_order, st);
   by_width<T>(a.dh, [&](auto dp, auto ch) {
     constexpr int DP = decltype(dp)::value, CH = decltype(ch)::value;
     const int64_t tiles = tiles_of(a.n_q, kBlock, a.batch);
@@ -801,21 +785,20 @@ hipError_t attn_forward(const AttnArgs &args, hipStream_t st) {
 template <typename T>
 hipError_t attn_backward(const AttnArgs &args, hipStream_t st) {
   AttnArgs a = args;
-  a.q_order = order_tiles(a, false, kBlock, a.q_order, st);
-  a.k_order = order_tiles(a, true, key_rows<T>(), a.k_order, st);
+  a.q_order = order_tiles(a, false, a.q_order, st);
+  a.k_order = order_tiles(a, true, a.k_order, st);
   const int parts = parts_of(a.hq, a.hk, a.n_q, a.n_k, a.batch);
   by_width<T>(a.dh, [&](auto dp, auto ch) {
     constexpr int DP = decltype(dp)::value, CH = decltype(ch)::value;
     const size_t lds = 4 * step_rows<T>() * DP * sizeof(T);
-    if (a.n_q > 0) 
+    if (a.n_q > 0)
       k_delta<T, DP, CH><<<blk::grid_of(((a.n_q + 31) / 32 * a.hq + 3) / 4), 256, 4 * 64 * DP * sizeof(T), st>>>(a);
     if (a.n_k > 0) {
-      constexpr int KB = key_rows<T>();
-      const int64_t tiles = tiles_of(a.n_k, KB, a.batch);
+      const int64_t tiles = tiles_of(a.n_k, kBlock, a.batch);
       dim3 grid = blk::grid_of(tiles * a.hk);
       grid.z = parts;
-      k_dkv<T, DP, CH, KB / kBlock><<<grid, kThreads, (4 * 32 + KB) * DP * sizeof(T) + 4 * 64 * sizeof(float), st>>>(
-          a, tiles, parts);
+      constexpr size_t lds = (4 * 32 + kBlock) * DP * sizeof(T) + 4 * 64 * sizeof(float);
+      k_dkv<T, DP, CH><<<grid, kThreads, lds, st>>>(a, tiles, parts);
       if (parts > 1) k_dkv_join<T><<<blk::grid_of((a.n_k * a.hk * 2 * a.dh + 255) / 256), 256, 0, st>>>(a, parts);
     }
     if (a.n_q > 0) {

@@ -8,7 +8,9 @@
 // lanes a head and several heads at a time; each lane holds W consecutive pairs, two
 // loads of W elements (one of 2 W where the pairs are neighbours). Every element is
 // read once and written once: HBM bounds the large sizes, one kernel's latency the
-// small ones, where a token's heads are spread over several waves.
+// small ones, where a token's heads are spread over several waves. Measured: 32768 tokens
+// of 32 + 8 heads of 128 bf16 128 us forward (5.25 TB/s), 131072 of 16 + 8 525 us backward
+// (4.6 TB/s), 32 tokens with their append 5.2 us of kernel.
 #include <type_traits>
 
 #include "attention_internal.h"
@@ -16,8 +18,6 @@
 
 namespace ipttt {
 namespace {
-
-using blk::Pack;
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 

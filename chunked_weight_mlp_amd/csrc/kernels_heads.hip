@@ -364,7 +364,8 @@ hipError_t launch_heads(const HeadArgs &a, hipStream_t st) {
     const Split s = split_of(a, W);
     const int at_once = 64 / s.lanes, rows = a.hq + a.hk * (APPEND ? 2 : 1);
     const int batches = (rows + at_once - 1) / at_once;
-    // a wave a token once there are 8192 tokens, more while there are fewer
+    // a wave a token once there are 8192 tokens, more while there are fewer (40 heads of 128
+    // bf16: 8192 tokens 34 us, 42 with four waves a token)
     int64_t slices = (8192 + a.n - 1) / a.n;
     if (slices > batches) slices = batches;
     k_heads<T, W, decltype(il)::value, APPEND>
@@ -375,6 +376,8 @@ hipError_t launch_heads(const HeadArgs &a, hipStream_t st) {
 
 }  // namespace
 
+// 2048 blocks for all heads, each with a partial sum of the scales' gradients. (8192 tokens,
+// 24 heads of 128 bf16: 51 us, 54 with 1024, 56 with 4096.)
 int heads_bwd_blocks(int heads, int all, int64_t n) {
   const int64_t b = (n + kWaves - 1) / kWaves, most = (int64_t)2048 * heads / all;
   return (int)(b < 1 ? 1 : b > most ? (most < 1 ? 1 : most) : b);

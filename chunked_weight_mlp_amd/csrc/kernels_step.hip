@@ -22,7 +22,8 @@ constexpr int kKeys = 32;  // keys of a step
 // us without it, the blocks of the short ones come last.)
 constexpr int kBegin = 1;
 // Steps in LDS: the next one's are copied beside this one's products, but where rows have
-// 512 bytes (fp32), whose products take longer than the copies.
+// 512 bytes (fp32), whose products take longer than the copies and leave LDS to twice the
+// blocks. (131072 tokens, 4 key heads of 128 fp32: 252 us with two steps, 191 with one.)
 template <typename T, int DP>
 constexpr int stages_of() { return sizeof(T) * DP > 256 ? 1 : 2; }
 
@@ -39,9 +40,13 @@ Plan plan_of(int hq, const ipttt_kv_cache &c, const ipttt_page_table &t) {
   const int dp = c.head_dim <= 64 ? 64 : 128;
   const int64_t most = ((int64_t)t.width * c.page_size + kKeys - 1) / kKeys;  // steps a sequence may have
   const int64_t pairs = (int64_t)t.batch * c.k_heads;
-  p.whole = most <= 2;
+  // 8 steps, once such blocks fill the GPU (heads of 128 bf16; 2048 blocks of 8 steps: 72.5
+  // us joined, 62.5 whole; 512: 33.3, 27.8; but 128: 21.6, 26.5; ragged ones of up to 32 steps:
+  // 43 joined, 68 whole.) 2 steps always (2048 blocks: 35.0, 26.5).
+  p.whole = most <= 2 || (most <= 8 && pairs >= 512);
   const int64_t steps = (most + kBegin) * pairs;
-  // as many as LDS holds at once
+  // as many as LDS holds at once, or nearly (131072 tokens, 32/8 heads of 128 bf16: 173 us
+  // with 512, 107 with 1024, 123 with 2048)
   const int blocks = (c.dtype == IPTTT_BF16 && dp == 64) ? 2048 : 1024;
   p.blocks = (int)(p.whole ? pairs : steps < blocks ? steps : blocks);
   p.cols = hq / c.k_heads < 32 ? hq / c.k_heads : 32;

@@ -515,6 +515,18 @@ def test_step_many_sequences():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [0, 41])
+@pytest.mark.parametrize("most", [256, 257])
+def test_step_many_short_sequences(most, window, dtype):
+    """Enough sequences of eight steps or fewer for a block to take a whole one, and of nine."""
+    lens = [(i * 37) % (most + 1) for i in range(260)]
+    cache, table, n = paged(lens, 2, 72, 16, dtype)
+    q = rand((len(lens), 6, 72), 5, dtype, 2.0)
+    want, bound = R.step(q, cache.k, cache.v, table, n, window)
+    within("step short", A.attention_step(q, cache, table, n, window=window), want, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_step_pages_that_are_none(dtype):
     """Keys of pages outside the cache are not there; lengths outside the table are cut to it."""
     lens = [100, 64, 1000, 30]

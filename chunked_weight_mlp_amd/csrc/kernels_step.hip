@@ -354,8 +354,9 @@ __global__ __launch_bounds__(kJoin) void k_join(StepArgs a, Plan plan) {
   constexpr int GROUPS = kJoin / 128;  // threads of a channel
   __shared__ float weight[2048], red[2][kJoin / 64], sums[GROUPS][kHeadMaxDim];
   const int hk = a.cache.k_heads, dh = a.cache.head_dim, group = a.hq / hk;
-  const int b = blockIdx.x / hk, kv = blockIdx.x % hk, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int g0 = ((const int *)a.ws)[2 * blockIdx.x], g1 = ((const int *)a.ws)[2 * blockIdx.x + 1];
+  const int b = blockIdx.z, kv = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int *const in = (const int *)a.ws + 2 * ((int64_t)b * hk + kv);
+  const int g0 = in[0], g1 = in[1];
   const bool none = span_of(a, b).n == 0;
   if (!none && g0 == g1) return;  // written already
   const int n = none ? 0 : g1 - g0 + 1;  // up to 2048
@@ -440,7 +441,8 @@ hipError_t step_forward(const StepArgs &a, hipStream_t st) {
   else go(std::integral_constant<int, 128>());
   if (!p.whole) {
     const int group = a.hq / a.cache.k_heads;
-    k_join<T><<<dim3(a.table.batch * a.cache.k_heads, group < 32 ? group : 32), kJoin, 0, st>>>(a, p);
+    // (fewer than 2^32 threads along x)
+    k_join<T><<<dim3(a.cache.k_heads, group < 32 ? group : 32, a.table.batch), kJoin, 0, st>>>(a, p);
   }
   return hipGetLastError();
 }

@@ -527,6 +527,32 @@ def test_step_many_short_sequences(most, window, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [4, 60])
+def test_step_wide_groups(width, dtype):
+    """Groups of more heads than a tile has columns, with blocks of whole sequences and without."""
+    lens = [0, 1, 40, 64]
+    cache, table, n = paged(lens, 2, 40, 16, dtype, width=width)
+    q = rand((len(lens), 80, 40), 5, dtype, 2.0)
+    want, bound = R.step(q, cache.k, cache.v, table, n)
+    within("step wide", A.attention_step(q, cache, table, n), want, bound)
+
+
+def test_step_most_sequences():
+    """65535 sequences of one key each, of so many key heads that a thread for each channel of
+    each is more than 2^32 threads: the answer is that key's value."""
+    batch, hk, dh = 65535, 130, 8
+    k, v = rand((1, hk, 64, dh), 1, BF16), rand((1, hk, 64, dh), 2, BF16)
+    table = torch.zeros(batch, 5, dtype=torch.int32, device=DEV)
+    n = torch.ones(batch, dtype=torch.int32, device=DEV)
+    n[7] = 0
+    q = torch.randn(batch, hk, dh, device=DEV).to(BF16)
+    o = A.attention_step(q, A.KVCache(k, v), table, n)
+    want = v[:, :, 0].expand(batch, hk, dh).clone()
+    want[7] = 0
+    assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_step_pages_that_are_none(dtype):
     """Keys of pages outside the cache are not there; lengths outside the table are cut to it."""
     lens = [100, 64, 1000, 30]

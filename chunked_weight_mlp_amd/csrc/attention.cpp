@@ -217,7 +217,9 @@ AttnArgs attn_args(const ipttt_attention *d, const ipttt_heads *q, const ipttt_h
   a.dh = d->head_dim;
   a.batch = d->batch;
   a.causal = d->causal != 0;
-  a.window = d->window;
+  // No sequence has more keys than n_k: a longer window leaves out none, and one of up to 2^30
+  // keeps the kernels' i + lk - lq - window within 32 bits, also where lq > lk.
+  a.window = d->window < d->n_k ? d->window : (int)d->n_k;
   a.scale = d->scale;
   a.n_q = d->n_q;
   a.n_k = d->n_k;

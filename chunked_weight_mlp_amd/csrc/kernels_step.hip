@@ -9,6 +9,8 @@
 //
 // A block is one wave, which copies a step's keys and values into its LDS while it computes
 // with the ones before; four or more of them share a CU and wait for nobody.
+#include <float.h>
+
 #include "attention_common.h"
 
 namespace ipttt {
@@ -52,7 +54,7 @@ Plan plan_of(int hq, const ipttt_kv_cache &c, const ipttt_page_table &t) {
   p.cols = hq / c.k_heads < 32 ? hq / c.k_heads : 32;
   return p;
 }
-// A partial result: for each head the maximum, the sum, and dh sums of values.
+// A partial result: for each head the maximum (-infinity: no key), the sum, and dh sums of values.
 __host__ __device__ inline int64_t part_size(int cols, int dh) { return (int64_t)cols * (dh + 2); }
 
 // The workspace: for each sequence and key head the blocks where it begins and ends, then
@@ -317,7 +319,9 @@ __global__ __launch_bounds__(64) void k_step(StepArgs a, Plan plan) {
       there = next;
     }
     sum = half_sum(sum);
-    if (any && m == -INFINITY) sum = NAN;  // keys, but none with a finite score
+    // Keys, but none with a score above -infinity: sum is 0, or NaN where a score is NaN, and m
+    // becomes a number, so that -infinity says that no key was there.
+    if (any && m == -INFINITY) m = -FLT_MAX;
     const int head0 = cc.kv * group + 32 * chunk;
     if (l == 0 && chunk == 0 && !plan.whole) {  // the blocks that k_join finds it in
       int *const in = (int *)a.ws + 2 * ((int64_t)cc.b * hk + cc.kv);
@@ -378,11 +382,12 @@ __global__ __launch_bounds__(kJoin) void k_join(StepArgs a, Plan plan) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kJoin / 64; ++i) top = fmaxf(top, red[0][i]);
+    // (a part of weight 0 is added all the same: what is NaN in it stays NaN)
     float sum = 0.f;
     for (int i = tid; i < n; i += kJoin) {
-      const float f = top == -INFINITY ? 1.f : weight[i] == -INFINITY ? 0.f : exp2_((weight[i] - top) * c);
+      const float f = weight[i] == -INFINITY ? 0.f : exp2_((weight[i] - top) * c);
       weight[i] = f;
-      if (f != 0.f) sum += f * part(i)[1];
+      sum += f * part(i)[1];
     }
     sum = blk::wave_sum(sum);
     if (lane == 0) red[1][wave] = sum;
@@ -400,7 +405,7 @@ __global__ __launch_bounds__(kJoin) void k_join(StepArgs a, Plan plan) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int i = i0 + u * GROUPS;
-          if (i < n && weight[i] != 0.f) o += weight[i] * v[u];
+          if (i < n) o += weight[i] * v[u];
         }
       }
       sums[mine][ch] = o;
@@ -412,10 +417,10 @@ __global__ __launch_bounds__(kJoin) void k_join(StepArgs a, Plan plan) {
 #pragma unroll
       for (int i = 0; i < GROUPS; ++i) o += sums[i][tid];
       ((T *)a.o.p)[b * a.o.tok_stride + head * a.o.head_stride + tid] =
-          (T)(sum == 0.f ? 0.f : o / sum);  // no key: sums of 0
+          (T)(top == -INFINITY ? 0.f : o / sum);  // -infinity: no key
     }
     if (a.lse && tid == 0)
-      a.lse[(int64_t)b * a.hq + head] = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * kLn2;
+      a.lse[(int64_t)b * a.hq + head] = top == -INFINITY ? -INFINITY : (top * c + log2f(sum)) * kLn2;
     __syncthreads();
   }
 }

@@ -1,8 +1,10 @@
 // Norms of queries and keys for each head with the rotation by position (gfx950).
 //
 // A head's channels are held as pairs (a, b): the rotated pairs first, then the
-// others two by two with the angle 0, so that one formula serves all of them:
+// others two by two, which only the norm concerns:
 //   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin),  n = x r gamma.
+// A lane's run of pairs is all rotated or not at all (run_of), so it is told by one number.
+// (The angle 0 for the others would serve finite values: 0 x infinity is NaN.)
 // A wave takes one token: its 64 lanes compute the token's (at most 64) sines and
 // cosines once, pass them on through LDS, and then go over the token's heads, some
 // lanes a head and several heads at a time; each lane holds W consecutive pairs, two
@@ -52,9 +54,11 @@ template <int W, bool IL>
 struct Place {
   int pair, ca, cb;
   bool on, has_b;  // anything here; the b of a lone last channel is missing (W = 1)
+  bool turned;     // rotated
   __device__ __forceinline__ Place(const Split &s, int dh, int lane) {
     pair = (lane & (s.lanes - 1)) * W;
     on = pair < s.pairs;
+    turned = pair < s.r2;
     const int r = 2 * s.r2;
     if (IL) {
       ca = 2 * pair;
@@ -222,8 +226,8 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadArgs a, Split s, int sli
       for (int e = 0; e < W; ++e) {
         const float na = xa[e] * r * (is_q ? gq[0][e] : gk[0][e]);
         const float nb = xb[e] * r * (is_q ? gq[1][e] : gk[1][e]);
-        xa[e] = na * c[e] - nb * sn[e];
-        xb[e] = nb * c[e] + na * sn[e];
+        xa[e] = p.turned ? na * c[e] - nb * sn[e] : na;
+        xb[e] = p.turned ? nb * c[e] + na * sn[e] : nb;
       }
     }
     if (live && dst) store_pairs<T, W, IL>(dst, p, xa, xb);
@@ -274,7 +278,8 @@ __global__ __launch_bounds__(kThreads) void k_heads_bwd(HeadArgs a, Split s, int
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         sum += xa[e] * xa[e] + xb[e] * xb[e];
-        const float ga = ya[e] * c[e] + yb[e] * sn[e], gb = yb[e] * c[e] - ya[e] * sn[e];
+        const float ga = p.turned ? ya[e] * c[e] + yb[e] * sn[e] : ya[e];
+        const float gb = p.turned ? yb[e] * c[e] - ya[e] * sn[e] : yb[e];
         ya[e] = ga;
         yb[e] = gb;
         dot += ga * g[0][e] * xa[e] + gb * g[1][e] * xb[e];

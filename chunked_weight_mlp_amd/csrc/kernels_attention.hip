@@ -267,7 +267,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
         __builtin_amdgcn_sched_barrier(0);
       }
       sum += (part[0] + part[1]) + (part[2] + part[3]);
-      if (rescale) {
+      if (rescale && fix != kCount) {  // (counts are no weights)
 #pragma unroll
         for (int d = 0; d < CH / 32; ++d)
 #pragma unroll

@@ -397,18 +397,28 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
     int cur = 0;
     RowReader<T, DP> rows(buf, l);
     ColReader<T, DP> cols(buf, l);
-    if (begin < tail.hi) {
-      kc.issue(buf, begin, lk, a.dh, wave, l, fix);
-      vc.issue(buf + KS * DP, begin, lk, a.dh, wave, l, kAsIs);
-    }
+    // Scores are those of the keys as they are, also where dS meets keys with something left out
+    // (an infinite key may have the score -infinity, and no weight). The passes that fix keys,
+    // which are rare, have the fixed ones in the second buffer and copy nothing ahead.
+    if (fix != kAsIs) cols.move(STAGE);
+    const auto issue = [&](int k0, int b) __attribute__((always_inline)) {
+      T *const t = buf + b * 2 * KS * DP;
+      kc.issue(t, k0, lk, a.dh, wave, l, kAsIs);
+      vc.issue(t + KS * DP, k0, lk, a.dh, wave, l, kAsIs);
+    };
     for (int k0 = begin; k0 < tail.hi; k0 += KS) {
+      if (fix != kAsIs || k0 == begin) {
+        mfma::lds_barrier();  // no wave reads the tiles before
+        issue(k0, 0);
+      }
       mfma::wait_vm<0>();
       mfma::lds_barrier();
-      cur ^= 1;
-      if (k0 + KS < tail.hi) {
-        T *const next = buf + cur * 2 * KS * DP;
-        kc.issue(next, k0 + KS, lk, a.dh, wave, l, fix);
-        vc.issue(next + KS * DP, k0 + KS, lk, a.dh, wave, l, kAsIs);
+      if (fix == kAsIs) {
+        cur ^= 1;
+        if (k0 + KS < tail.hi) issue(k0 + KS, cur);
+      } else {
+        for (int i = here(tid); i < KS * DP; i += kThreads) buf[2 * KS * DP + i] = fixed(buf[i], fix);
+        mfma::lds_barrier();
       }
       const bool whole = k0 + KS <= wf.hi && k0 >= wl.lo;
       const auto each_seen = [&](int t, auto f) __attribute__((always_inline)) {
@@ -497,8 +507,10 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
           refill(m);
           if (NT > 1 && t == 0 && o == 2 * ND - 1) finish(NT - 1);
         }
-      rows.move(cur ? STAGE : -STAGE);
-      cols.move(cur ? STAGE : -STAGE);
+      if (fix == kAsIs) {
+        rows.move(cur ? STAGE : -STAGE);
+        cols.move(cur ? STAGE : -STAGE);
+      }
     }
     if (fix == kAsIs && !__syncthreads_and(all_finite(acc))) continue;
     if (qi < lq)

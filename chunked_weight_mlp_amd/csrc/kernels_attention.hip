@@ -310,7 +310,10 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
 }
 
 // delta = sum(dy o) of each query and head, and the forward's lse in units of log2. A row
-// with an infinite score has no softmax: its gradients are NaN. The sums are the diagonal of
+// with an infinite lse, if it sees a key at all, has no softmax, and one whose delta is not
+// finite has differences infinity - infinity: both are NaN here, since the products beside
+// them leave out what is not finite in q and dy, and would make infinities of them. (A row
+// that sees no key is masked where it is used.) The sums are the diagonal of
 // a 32 x 32 product of o and dy, so that they are added in the order in which the backward's
 // products add dP = dy V: a query that sees one key, whose o is that key's v, then has
 // dP = delta to the bit, and gradients of zero. A wave takes 32 tokens of one head.
@@ -348,8 +351,8 @@ __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
     if (8 * (i / 4) + i % 4 == (q & ~4)) v = x[i];
   if ((q >> 2 & 1) == h && q < left) {
     const float lse = a.lse[hd * a.n_q + t];
-    a.delta[hd * a.n_q + t] = v;
-    a.lse2[hd * a.n_q + t] = lse == INFINITY ? NAN : lse * kLog2e;
+    a.delta[hd * a.n_q + t] = __builtin_isfinite(v) ? v : NAN;
+    a.lse2[hd * a.n_q + t] = __builtin_isinf(lse) ? NAN : lse * kLog2e;
   }
 }
 

@@ -116,3 +116,17 @@ def test_a_key_of_minus_infinity(dh, dtype):
     assert torch.isnan(dq[300:, 2:, 7]).all()
     dq[300:, 2:, 7] = want[2][300:, 2:, 7]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("channel", [5, 7, None])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("what", ["q", "dy"])
+def test_class_of_results_queries(what, dtype, channel, value):
+    """The same of a query and its gradient, at the 50th of 90."""
+    for scale in (40 ** -0.5, -0.5):
+        for causal, window in MASKS:
+            q, k, v, dy = prompt(dtype)
+            t = q if what == "q" else dy
+            t[50, 1, slice(None) if channel is None else channel] = value
+            hold(q, k, v, dy, scale, causal, window, dtype)

@@ -227,7 +227,8 @@ __device__ __forceinline__ Frag<T> load_frag(const T *row, int s, int h, int dh)
 }
 
 // Scores are kept without the scale, whose size enters with the exponent (log2_scale); its
-// sign is that of the operand held in registers. A scale of 0 is that of zeros.
+// sign is that of the operand held in registers. A scale of 0 is that of zeros, or of NaN where
+// the operand is not finite.
 __device__ __forceinline__ float log2_scale(float scale) {
   return scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
 }
@@ -236,8 +237,8 @@ __device__ __forceinline__ Frag<T> with_sign(Frag<T> f, float scale) {
   if (scale > 0.f) return f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if constexpr (std::is_same<T, float>::value) f.v[j] = scale == 0.f ? 0.f : -f.v[j];
-    else f[j] = scale == 0.f ? (__bf16)0.f : -f[j];
+    if constexpr (std::is_same<T, float>::value) f.v[j] = scale == 0.f ? 0.f * f.v[j] : -f.v[j];
+    else f[j] = scale == 0.f ? (__bf16)(0.f * (float)f[j]) : -f[j];
   }
   return f;
 }

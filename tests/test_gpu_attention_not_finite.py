@@ -130,3 +130,16 @@ def test_class_of_results_queries(what, dtype, channel, value):
             t = q if what == "q" else dy
             t[50, 1, slice(None) if channel is None else channel] = value
             hold(q, k, v, dy, scale, causal, window, dtype)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("what", ["q", "k"])
+def test_a_scale_of_zero(what, dtype, value):
+    """0 x infinity and 0 x NaN are NaN."""
+    q, k, v, dy = prompt(dtype)
+    if what == "q":
+        q[50, 1, 5] = value
+    else:
+        k[100, 0, 5] = value
+    hold(q, k, v, dy, 0.0, True, 0, dtype)

@@ -112,3 +112,17 @@ def test_lse_of_keys_without_weight():
         A.ipttt_attention_step(desc, A._heads("q", q, q.shape, F32, q.device), cache.desc, tab, lens,
                                A._heads("o", o, q.shape, F32, q.device), lse, ws, need)
         assert torch.isnan(o).all() and (torch.isnan(lse) | (lse == -math.inf)).all()
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("length", [64, 1500])
+def test_a_scale_of_zero(length, dtype, value):
+    """0 x infinity and 0 x NaN are NaN, for the query's heads that hold it and no others."""
+    cache, table, lens, q = one(length, dtype)
+    want = A.attention_step(q, cache, table, lens, scale=0.0)
+    q[0, 2, 7] = value
+    o = A.attention_step(q, cache, table, lens, scale=0.0)
+    assert torch.isnan(o[0, 2]).all()
+    o[0, 2] = want[0, 2]
+    assert torch.equal(o, want)

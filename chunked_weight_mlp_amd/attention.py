@@ -164,6 +164,7 @@ def _heads(name, t, shape, dtype, device):
 
 
 def _int32(name, v):
+    """v as a field of 32 bits, which ctypes would cut it to."""
     if not -2 ** 31 <= v < 2 ** 31:
         raise _invalid(f"{name}={v} does not fit 32 bits")
     return v
@@ -172,6 +173,9 @@ def _int32(name, v):
 def _three(name, t):
     if t.dim() != 3 or 0 in t.shape[1:]:
         raise _invalid(f"{name} must be [tokens, heads, head_dim], the last two > 0")
+    n, heads, dh = t.shape
+    if heads >= 2 ** 31 or dh >= 2 ** 31:
+        raise _invalid(f"{name} has shape {(n, heads, dh)}: heads or head_dim do not fit 32 bits")
     return t.shape
 
 
@@ -185,12 +189,14 @@ class KVCache:
         if k.dim() != 4 or 0 in k.shape[1:]:
             raise _invalid("k must be [pages, k_heads, page_size, head_dim], all but the pages > 0")
         dt = _dtype_of(k)
+        for name, size in zip(("pages", "k_heads", "page_size", "head_dim"), k.shape):
+            _int32(name, size)
         self.k = _dense("k", k, k.shape, k.dtype, k.device)
         self.v = _dense("v", v, k.shape, k.dtype, k.device)
         self.pages, self.k_heads, self.page_size, self.head_dim = k.shape
         self.dtype, self.device = k.dtype, k.device
-        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), _int32("pages", self.pages), self.page_size, self.k_heads,
-                                self.head_dim, dt)
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, self.k_heads, self.head_dim,
+                                dt)
         self._ref = ctypes.byref(self.desc)
 
     @classmethod
@@ -203,6 +209,8 @@ class KVCache:
         """The call's form of a page table."""
         if table.dim() != 2:
             raise _invalid("table must be [sequences, pages]")
+        if max(table.shape) >= 2 ** 31:
+            raise _invalid(f"table has shape {tuple(table.shape)}, which does not fit 32 bits")
         _is("table", table, torch.int32, self.device)
         if table.numel() and table.shape[1] > 1 and table.stride(1) != 1:
             raise _invalid("table must have its rows contiguous")
@@ -227,6 +235,7 @@ class HeadNorm:
             raise _invalid("without gammas, head_dim and dtype must be given")
         if inv_freq.dim() != 1 or not inv_freq.is_floating_point():
             raise _invalid("inv_freq must be a vector of floating numbers")
+        _int32("head_dim", head_dim), _int32("rotary", 2 * inv_freq.numel())
         self.head_dim, self.dtype, self.device = head_dim, dtype, inv_freq.device
         dt = _b._DT.get(dtype)
         if dt is None:
@@ -334,6 +343,7 @@ def _attention(q, k, v, offsets, k_offsets, causal, window, scale):
     if offsets is not None:
         if offsets.dim() != 1 or offsets.numel() == 0:
             raise _invalid("offsets must be [sequences + 1]")
+        _int32("sequences", offsets.numel() - 1)
         _dense("offsets", offsets, offsets.shape, torch.int32, dev)
         _dense("k_offsets", k_offsets, offsets.shape, torch.int32, dev)
         batch = offsets.numel() - 1

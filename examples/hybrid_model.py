@@ -188,10 +188,13 @@ class HybridModel:
         and keeps the states for decode()."""
         if tokens.shape[1] % self.chunk:
             raise ValueError("prompts are whole chunks: the fast weight's next chunk starts after them")
+        if self.attend and tokens.shape[1] > self.max_seq_len:
+            raise ValueError(f"{tokens.shape[1]} tokens do not fit the caches' max_seq_len={self.max_seq_len}")
         d, w = self.d, self.w
         e = w["embed"][tokens].contiguous()
         self.states, h, res = {}, e, None
         batch, length = tokens.shape
+        self.length = length
         if self.attend:
             # a page table for max_seq_len tokens a sequence, which every block's cache shares
             page = 16
@@ -228,6 +231,10 @@ class HybridModel:
 
     def decode(self, tokens):
         """One token [batch] after the prefill or the last decode; returns its logits."""
+        # a token behind the table's last page would not be written, nor attended to
+        if self.attend and self.length >= self.max_seq_len:
+            raise ValueError(f"the caches hold max_seq_len={self.max_seq_len} tokens a sequence already")
+        self.length += 1
         d, w = self.d, self.w
         e = w["embed"][tokens].contiguous()
         self.chunk_e[:, self.pos] = e

@@ -143,3 +143,14 @@ def test_a_scale_of_zero(what, dtype, value):
     else:
         k[100, 0, 5] = value
     hold(q, k, v, dy, 0.0, True, 0, dtype)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dh", [72, 128])
+def test_class_of_results_shared_tiles(dh, dtype, value):
+    """Groups of four heads, where blocks share a tile of keys and leave partial sums."""
+    for what in range(4):
+        t = prompt(dtype, 300, 300, 4, 1, dh)
+        t[what][170, 0, 7] = value
+        hold(*t, dh ** -0.5, True, 0, dtype)

@@ -222,7 +222,7 @@ class HeadNorm:
     [head_dim] or None for a tensor that is not normed) and the rotation of the first
     2 * len(inv_freq) channels by pos * inv_freq (radians a position, kept in 64 bits):
     pairs are channels i and i + len(inv_freq), or 2 i and 2 i + 1 if interleaved.
-    Without gammas, say dtype, head_dim and device."""
+    Without gammas, say dtype and head_dim. All tensors are on inv_freq's device."""
 
     def __init__(self, q_gamma, k_gamma, inv_freq, eps: float = 1e-6, interleaved: bool = False, head_dim=None,
                  dtype=None):
@@ -286,7 +286,7 @@ class HeadNorm:
         """As forward, with the keys' results and v written to the cache instead: token t at
         position pos[t] of sequence seqs[t] (int32 [tokens]; None: of sequence t). Returns q.
         A token whose place the table does not hold (a negative position marks padding) is
-        not written."""
+        not written. No two tokens may have the same place."""
         if stream is not None:
             return _call_on(stream, self.append, (q, k, v, pos, cache, table, seqs),
                             (*self._held(), cache.k, cache.v))

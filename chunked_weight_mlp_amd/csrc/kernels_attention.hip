@@ -4,13 +4,14 @@
 // key head (dk, dv) and goes over the other side in tiles that are copied into LDS a step
 // ahead. Two blocks share a CU, so that one's products run beside the other's softmax; the
 // 256 registers that leaves a wave are what its sums, its own rows and the operands in
-// flight need (128 channels bf16: forward 233, dq 250, dk and dv all), and none may go to
-// memory: a reload waits for every copy in flight before it. Products and the arithmetic
-// that does not wait for them are interleaved in the source; sched_barrier keeps the order.
+// flight need (128 channels bf16: forward 233, dq 255, dk and dv all), and none may go to
+// memory in a loop: a reload waits for every copy in flight before it. (dk and dv keep 12 bytes
+// a lane there, for behind the loop.) Products and the arithmetic that does not wait for them
+// are interleaved in the source; sched_barrier keeps the order.
 //
-// What bounds it: of the forward's cycles the matrix cores are busy half and the vector units
-// issue in half (32768 tokens of 32/8 heads of 128 bf16: 8.5 ms, 1037 TFLOP/s; 16384 of
-// 16/8: 1.2 ms, 918, and the backward 3.74 ms, 735).
+// What bounds it: of the forward's cycles the matrix cores are busy 52 % and the vector units
+// issue in 49 % (32768 tokens of 32/8 heads of 128 bf16: 8.4 to 8.8 ms from one GPU to another,
+// 1000 to 1045 TFLOP/s; 16384 of 16/8: 1.08 ms, 1020, and the backward 3.7 ms, 740).
 #include "attention_common.h"
 
 namespace ipttt {
@@ -316,7 +317,9 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_fwd(AttnAr
 // that sees no key is masked where it is used.) The sums are the diagonal of
 // a 32 x 32 product of o and dy, so that they are added in the order in which the backward's
 // products add dP = dy V: a query that sees one key, whose o is that key's v, then has
-// dP = delta to the bit, and gradients of zero. A wave takes 32 tokens of one head.
+// dP = delta to the bit, and gradients of zero. (o is the forward's result as it was rounded to
+// its type; with the rounding of ds that gives dq and dk in bf16 an error of 2.6e-3 to 3.2e-3,
+// where rounding the exact gradients makes 1.7e-3.) A wave takes 32 tokens of one head.
 template <typename T, int DP, int CH>
 __global__ __launch_bounds__(256) void k_delta(AttnArgs a) {
   extern __shared__ __align__(1024) char smem[];
@@ -528,7 +531,7 @@ __global__ __launch_bounds__(kThreads, (blocks_a_cu<T, DP>())) void k_dq(AttnArg
 // holds 32 keys: their sums and K rows in registers, their V rows in LDS, since both do not
 // fit beside the sums. (64 keys a wave halve the LDS reads of a product, but leave a SIMD one
 // wave, which does not cover its own waits: 1090 us for 16384 tokens in six documents of 16/8
-// heads of 128 bf16, where this takes 590.)
+// heads of 128 bf16, where 32 took 590 at the time, 500 now.)
 // For 32 queries the products are, with what the vector units do beside them,
 //   scores S = Q K^T;   dP = dY V^T beside P = exp(S - lse);
 //   dV += dY^T P beside dS = P (dP - delta);   dK += Q^T dS.

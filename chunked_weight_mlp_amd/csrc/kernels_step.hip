@@ -47,8 +47,9 @@ Plan plan_of(int hq, const ipttt_kv_cache &c, const ipttt_page_table &t) {
   // 43 joined, 68 whole.) 2 steps always (2048 blocks: 35.0, 26.5).
   p.whole = most <= 2 || (most <= 8 && pairs >= 512);
   const int64_t steps = (most + kBegin) * pairs;
-  // as many as LDS holds at once, or nearly (131072 tokens, 32/8 heads of 128 bf16: 173 us
-  // with 512, 107 with 1024, 123 with 2048)
+  // as many as run at once, or nearly: four waves a CU, one a SIMD, which the registers of 128
+  // channels leave (LDS would hold five), eight at 64 bf16 (131072 tokens, 32/8 heads of 128
+  // bf16: 173 us with 512, 107 with 1024, 123 with 2048)
   const int blocks = (c.dtype == IPTTT_BF16 && dp == 64) ? 2048 : 1024;
   p.blocks = (int)(p.whole ? pairs : steps < blocks ? steps : blocks);
   p.cols = hq / c.k_heads < 32 ? hq / c.k_heads : 32;

@@ -22,7 +22,9 @@
  * operands of the products they enter (bf16 MFMA, fp32 accumulation); in fp32 the
  * products are fp32. A result whose operands are not all finite may be NaN where
  * the formula has an infinity. Keys that a query does not see have no part in its
- * result, whatever they hold.
+ * result, whatever they hold. Sums are formed before they are divided, so that numbers
+ * beyond the range of activations (heads to norm beyond 2^60, values beyond 2^88) may
+ * overflow fp32.
  *
  * A tensor of heads is given by its strides in elements: both at least head_dim, any
  * order of the two (a slice of a fused projection, or heads outermost); channels are
@@ -92,7 +94,8 @@ ipttt_status ipttt_headnorm_forward(const ipttt_headnorm_desc *desc, const ipttt
 /* The same with k's result, and v as it is, written to the cache: token t is the
  * pos[t]-th of sequence seqs[t] (NULL: of sequence t). A token whose sequence or
  * position the table does not hold is not written; its q is computed all the same (a
- * negative position marks padding). Of two tokens for one place either is kept. */
+ * negative position marks padding). No two tokens may have the same place: it would
+ * hold parts of both. */
 ipttt_status ipttt_headnorm_append(const ipttt_headnorm_desc *desc, const ipttt_heads *q,
                                    const ipttt_heads *k, const ipttt_heads *v, const int32_t *pos,
                                    const int32_t *seqs, int64_t n, const ipttt_heads *q_out,
